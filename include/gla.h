@@ -393,6 +393,111 @@ gla_status conv1d_silu_decode_step(const void* x, const int32_t* slot_idx, int n
                                    int N, int D, int W, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Gated delta rule.  (The pages describe Simple GLA; this is the mixer of the
+ * same family that corrects what the state already predicts.)  Per sequence
+ * and value head, with log-decay a_t <= 0 and write strength beta_t:
+ *
+ *     S'_t = exp(a_t) S_{t-1}
+ *     S_t  = S'_t + k_t^T beta_t (v_t - k_t S'_t)      S: dk x dv, fp32
+ *     o_t  = scale q_t S_t
+ *
+ * The keys are meant to have unit length and beta to lie in 0 .. 1 (0 .. 2
+ * keeps the state bounded too); neither is checked, nor normalised here.
+ *
+ * Head layout: q and k have Hk heads, v, a, beta and o have H, H a multiple of
+ * Hk; value head h reads q and k of head h / (H / Hk).
+ *   q, k     [N, T, Hk, dk] bf16   token stride ld_qkv elements (0 = packed:
+ *   v        [N, T, H, dv]  bf16   Hk*dk for q and k, H*dv for v), as in
+ *                                  gla_chunk_fwd.
+ *   a, beta  [N, T, H]      fp32   contiguous.
+ *   s0, s_final [N, H, dk, dv] fp32, or NULL (zeros / not wanted).
+ *   o        [N, T, H, dv]  bf16   contiguous.
+ *   cu_seqlens  NULL, or a DEVICE pointer to [N+1] int32: then the N sequences
+ *            are packed, T is the number of rows of all of them, the leading
+ *            dimensions are [T, ...], and sequence n has rows cu_seqlens[n] ..
+ *            cu_seqlens[n+1]-1 (any length, 0 included).  Offsets have to be
+ *            non-decreasing and inside 0 .. T: a sequence whose own two are
+ *            not is skipped, GLA_ERR_INVALID_ARG is recorded in the device
+ *            status word, and the other sequences' outputs are undefined.
+ *            Rows outside every sequence are not written.
+ *   ws       workspace of ws_bytes >= gated_delta_chunk_workspace_bytes(N, T,
+ *            H, dk, dv, packed, for_bwd); contents on entry do not matter.
+ *            Calls that may overlap on the GPU need one each.
+ * Supported: dk in {64, 96, 128}; dv a multiple of 32, 32 .. 256; dt GLA_BF16
+ * (GLA_F32 is GLA_ERR_UNSUPPORTED here; gated_delta_decode_step takes it).
+ * States, decays and sums are fp32 or wider; the state is carried to about
+ * 16 bits through the products of a chunk of 64 tokens (two bf16 terms).
+ *
+ * gated_delta_chunk_bwd recomputes what it needs of the forward.  dO [N, T, H,
+ * dv] bf16 contiguous; ds_final [N, H, dk, dv] fp32 or NULL (zeros).  grad_q,
+ * grad_k [N, T, Hk, dk] and grad_v [N, T, H, dv] bf16, contiguous (summed over
+ * the value heads that share a q/k head); grad_a and grad_beta [N, T, H] fp32;
+ * grad_s0 [N, H, dk, dv] fp32 or NULL.  Repeated calls give the same bits.
+ * ------------------------------------------------------------------------ */
+size_t gated_delta_chunk_workspace_bytes(int N, int T, int H, int dk, int dv, int packed, int for_bwd);
+
+gla_status gated_delta_chunk_fwd(const void* q, const void* k, const void* v, const float* a, const float* beta,
+                                 const int32_t* cu_seqlens, const float* s0, void* o, float* s_final, void* ws,
+                                 size_t ws_bytes, int N, int T, int Hk, int H, int dk, int dv, int64_t ld_qkv,
+                                 float scale, gla_dtype dt, cudaStream_t stream);
+
+gla_status gated_delta_chunk_bwd(const void* q, const void* k, const void* v, const float* a, const float* beta,
+                                 const int32_t* cu_seqlens, const float* s0, const void* dO, const float* ds_final,
+                                 void* grad_q, void* grad_k, void* grad_v, float* grad_a, float* grad_beta,
+                                 float* grad_s0, void* ws, size_t ws_bytes, int N, int T, int Hk, int H, int dk,
+                                 int dv, int64_t ld_qkv, float scale, gla_dtype dt, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The gated delta rule token by token, in place on a pool of states: T tokens
+ * (1 when decoding, a few when drafted tokens are checked) for each of N
+ * sequences, as gla_decode_step addresses its pool.
+ *   state    [n_slots, H, dk, dv] fp32, updated in place.
+ *   slot_idx [N] int32 or NULL (identity; then n_slots >= N).  Slots must be
+ *            distinct within one call.  A slot outside [0, n_slots) is skipped
+ *            (nothing read or written for that sequence) and
+ *            GLA_ERR_INVALID_ARG is recorded in the device status word.
+ *   q, k, v  [N, T, heads, d] bf16 or fp32 (dt), token stride ld_qkv (0 =
+ *            packed).  a, beta [N, T, H] fp32.  o [N, T, H, dv] fp32.
+ * All arithmetic is fp32.  Supported: dk and dv as above.
+ * ------------------------------------------------------------------------ */
+gla_status gated_delta_decode_step(float* state, const int32_t* slot_idx, int n_slots, const void* q, const void* k,
+                                   const void* v, const float* a, const float* beta, float* o, int N, int T, int Hk,
+                                   int H, int dk, int dv, int64_t ld_qkv, float scale, gla_dtype dt,
+                                   cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Group norm with an activation, channels last: the norm and gate behind a
+ * mixer's output.  Every row (token) has G groups of d channels (heads), each
+ * normalised by itself:
+ *
+ *     x^ = (x - mean) / sqrt(mean((x - mean)^2) + eps)     mean: 0 if !center
+ *     n  = x^ weight + bias
+ *     y  = n act(gate), or act(n) without a gate           act: SiLU, or the
+ *                                                          identity if !act
+ *   x        [M, G, d] bf16 or fp32 (dt), row stride ld_x elements (0 = G*d).
+ *   gate     [M, G, d] bf16 or NULL, row stride ld_gate (0 = G*d): it may be a
+ *            slice of a fused projection.
+ *   weight, bias  [G, d] fp32, or [d] for all groups when shared_weight; NULL:
+ *            ones, zeros.
+ *   y        [M, G, d] bf16, contiguous.
+ * Backward: dy [M, G, d] bf16 contiguous; grad_x in x's type and grad_gate
+ * bf16, both contiguous; grad_weight, grad_bias as weight and bias, or NULL;
+ * ws of group_norm_silu_bwd_workspace_bytes when either is wanted.  Sums over
+ * rows are added in a fixed order (repeated calls give the same bits).
+ * Supported: d a multiple of 8, d <= 1024, G*d <= 2^20; statistics are fp32.
+ * ------------------------------------------------------------------------ */
+size_t group_norm_silu_bwd_workspace_bytes(int M, int G, int d);
+
+gla_status group_norm_silu(const void* x, const void* gate, const float* weight, const float* bias, void* y, int M,
+                           int G, int d, int64_t ld_x, int64_t ld_gate, int shared_weight, int center, int act,
+                           float eps, gla_dtype dt, cudaStream_t stream);
+
+gla_status group_norm_silu_bwd(const void* x, const void* gate, const float* weight, const float* bias, const void* dy,
+                               void* grad_x, void* grad_gate, float* grad_weight, float* grad_bias, void* ws,
+                               size_t ws_bytes, int M, int G, int d, int64_t ld_x, int64_t ld_gate, int shared_weight,
+                               int center, int act, float eps, gla_dtype dt, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Device status.  gla_get_device_status SYNCHRONISES the stream, copies the
  * device status word of the current device (0 or a gla_status recorded by a
  * kernel, e.g. GLA_ERR_TIMEOUT) into *device_status and clears it.

@@ -27,7 +27,10 @@ __all__ = [
     "conv1d_silu_causal_bwd_workspace_bytes", "gla_chunk_fwd_varlen", "gla_segment_workspace_bytes",
     "gla_segment_state_fwd", "gla_segment_state_bwd", "gla_state_fold", "gla_build_flags",
     "gla_chunk_varlen_workspace_bytes", "gla_chunk_saved_state_bytes", "gla_chunk_fwd_train",
-    "gla_chunk_bwd_saved", "EXPORTED_SYMBOLS",
+    "gla_chunk_bwd_saved",
+    "gated_delta_chunk_workspace_bytes", "gated_delta_chunk_fwd", "gated_delta_chunk_bwd",
+    "gated_delta_decode_step", "group_norm_silu", "group_norm_silu_bwd",
+    "group_norm_silu_bwd_workspace_bytes", "EXPORTED_SYMBOLS",
     "LIB_PATH", "LIB_DEBUG_PATH", "GLA_BUILD_DEBUG_BOUNDS",
 ]
 
@@ -45,6 +48,9 @@ EXPORTED_SYMBOLS = (
     "gla_segment_state_fwd", "gla_segment_state_bwd", "gla_state_fold", "gla_build_flags",
     "gla_chunk_varlen_workspace_bytes", "gla_chunk_saved_state_bytes", "gla_chunk_fwd_train",
     "gla_chunk_bwd_saved",
+    "gated_delta_chunk_workspace_bytes", "gated_delta_chunk_fwd", "gated_delta_chunk_bwd",
+    "gated_delta_decode_step", "group_norm_silu", "group_norm_silu_bwd",
+    "group_norm_silu_bwd_workspace_bytes",
 )
 
 GLA_BF16, GLA_F32 = 0, 1
@@ -155,6 +161,21 @@ def declare(L):
                                     ctypes.POINTER(ctypes.c_double), _i]
     L.gla_build_flags.restype = _i
     L.gla_build_flags.argtypes = []
+    sz = ctypes.c_size_t
+    L.gated_delta_chunk_workspace_bytes.restype = sz
+    L.gated_delta_chunk_workspace_bytes.argtypes = [_i] * 7
+    L.gated_delta_chunk_fwd.restype = _i
+    L.gated_delta_chunk_fwd.argtypes = [_vp] * 10 + [sz] + [_i] * 6 + [_i64, _f, _i, _vp]
+    L.gated_delta_chunk_bwd.restype = _i
+    L.gated_delta_chunk_bwd.argtypes = [_vp] * 16 + [sz] + [_i] * 6 + [_i64, _f, _i, _vp]
+    L.gated_delta_decode_step.restype = _i
+    L.gated_delta_decode_step.argtypes = [_vp, _vp, _i] + [_vp] * 6 + [_i] * 6 + [_i64, _f, _i, _vp]
+    L.group_norm_silu_bwd_workspace_bytes.restype = sz
+    L.group_norm_silu_bwd_workspace_bytes.argtypes = [_i] * 3
+    L.group_norm_silu.restype = _i
+    L.group_norm_silu.argtypes = [_vp] * 5 + [_i] * 3 + [_i64, _i64] + [_i] * 3 + [_f, _i, _vp]
+    L.group_norm_silu_bwd.restype = _i
+    L.group_norm_silu_bwd.argtypes = [_vp] * 10 + [sz] + [_i] * 3 + [_i64, _i64] + [_i] * 3 + [_f, _i, _vp]
     return L
 
 
@@ -634,6 +655,220 @@ def conv1d_silu_decode_step(x, w, conv_state, slot_idx=None, apply_ln=True, ln_g
                                        _ptr(y), N, D, W, _stream(stream))
     _check("conv1d_silu_decode_step", st)
     return y
+
+# ---- gated delta rule, group norm with an activation
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, first.device))
+
+
+def _call_on(t, fn, *args, stream=None):
+    """Call the C entry point `fn` with t's device current, on `stream` or that
+    device's current stream."""
+    with torch.cuda.device(t.device):
+        s = stream if stream is not None else torch.cuda.current_stream(t.device)
+        _check(fn, getattr(lib(), fn)(*args, ctypes.c_void_p(s.cuda_stream)))
+
+
+def _rows_stride(x, name):
+    """Row stride (elements) of [..., heads, d] with the last two dims packed
+    and the leading dims in row order."""
+    if x.dim() < 2 or (x.shape[-1] > 1 and x.stride(-1) != 1) or \
+            (x.shape[-2] > 1 and x.stride(-2) != x.shape[-1]):
+        raise ValueError("%s: the head and feature dims must be packed (strides %s)" % (name, x.stride()))
+    ld, want = x.shape[-2] * x.shape[-1], None
+    for n, s in reversed(list(zip(x.shape[:-2], x.stride()[:-2]))):
+        if n == 1:
+            continue
+        if want is None:
+            ld = s
+        elif s != want:
+            raise ValueError("%s: the rows must be equally far apart (strides %s)" % (name, x.stride()))
+        want = s * n
+    if ld < x.shape[-2] * x.shape[-1]:
+        raise ValueError("%s: rows overlap (strides %s)" % (name, x.stride()))
+    return ld
+
+
+def _gated_delta_args(fn, q, k, v, a, beta, cu_seqlens, types):
+    """Check the shared arguments; returns (N, T, Hk, H, dk, dv, ld_qkv)."""
+    lead = q.shape[:-2]
+    if len(lead) != (1 if cu_seqlens is not None else 2):
+        raise ValueError("%s: q must be [%s, Hk, dk]" % (fn, "T" if cu_seqlens is not None else "N, T"))
+    if q.dtype not in types:
+        raise TypeError("%s takes %s q, k, v, got %s" % (fn, " or ".join(map(str, types)), q.dtype))
+    Hk, dk = q.shape[-2:]
+    H, dv = v.shape[-2:]
+    _need(q, "q", q.dtype, contiguous=False)
+    _need(k, "k", q.dtype, lead + (Hk, dk), contiguous=False)
+    _need(v, "v", q.dtype, lead + (H, dv), contiguous=False)
+    _need(a, "a", torch.float32, lead + (H,))
+    _need(beta, "beta", torch.float32, lead + (H,))
+    _same_device(q, k=k, v=v, a=a, beta=beta, cu_seqlens=cu_seqlens)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must have N + 1 entries")
+        N, T = cu_seqlens.numel() - 1, lead[0]
+    else:
+        N, T = lead
+    ld = [_rows_stride(x, name) for x, name in ((q, "q"), (k, "k"), (v, "v"))]
+    if q.numel() == 0 or v.numel() == 0 or ld == [Hk * dk, Hk * dk, H * dv]:
+        return N, T, Hk, H, dk, dv, 0
+    if not ld[0] == ld[1] == ld[2]:
+        raise ValueError("q, k and v must share one token stride when not packed (got %d, %d, %d)" % tuple(ld))
+    return N, T, Hk, H, dk, dv, ld[0]
+
+
+def _new(t, name, like, shape, dtype):
+    """`t` checked against shape and type, or a new tensor on like's device."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(t, name, dtype, shape)
+    _same_device(like, **{name: t})
+    return t
+
+
+def gated_delta_chunk_workspace_bytes(N, T, H, dk=96, dv=192, packed=False, for_bwd=False):
+    """Workspace bytes of gated_delta_chunk_fwd or, with for_bwd, gated_delta_chunk_bwd."""
+    return int(lib().gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, int(packed), int(for_bwd)))
+
+
+def gated_delta_chunk_fwd(q, k, v, a, beta, s0=None, cu_seqlens=None, o=None, s_final=None, ws=None, scale=None,
+                          want_final_state=True, stream=None):
+    """Chunked forward of the gated delta rule
+    S_t = e^a_t S_{t-1} + k_t^T beta_t (v_t - k_t e^a_t S_{t-1}), o_t = scale q_t S_t.
+    q, k [N,T,Hk,dk], v [N,T,H,dv] bf16 (may be views into a fused buffer), a,
+    beta [N,T,H] fp32; with cu_seqlens [N+1] int32 (on the device) the N
+    sequences are packed and the leading dims are [T].  Returns (o in v's
+    shape, s_final [N,H,dk,dv] fp32 or None)."""
+    N, T, Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_fwd", q, k, v, a, beta, cu_seqlens,
+                                                (torch.bfloat16,))
+    _need(s0, "s0", torch.float32, (N, H, dk, dv))
+    _same_device(q, s0=s0, ws=ws)
+    o = _new(o, "o", q, tuple(v.shape), torch.bfloat16)
+    if s_final is not None or want_final_state:
+        s_final = _new(s_final, "s_final", q, (N, H, dk, dv), torch.float32)
+    if ws is None:
+        need = gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _need(ws, "ws", torch.uint8)
+    _call_on(q, "gated_delta_chunk_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(cu_seqlens), _ptr(s0),
+             _ptr(o), _ptr(s_final), _ptr(ws), ws.numel(), N, T, Hk, H, dk, dv, ld,
+             float(dk ** -0.5 if scale is None else scale), GLA_BF16, stream=stream)
+    return o, s_final
+
+
+def gated_delta_chunk_bwd(q, k, v, a, beta, dO, s0=None, ds_final=None, cu_seqlens=None, grads=None, ws=None,
+                          scale=None, want_grad_s0=True, stream=None):
+    """Backward of gated_delta_chunk_fwd (it recomputes what it needs of the
+    forward).  dO in v's shape, bf16; ds_final [N,H,dk,dv] fp32 or None.  Returns
+    (dq, dk, dv, da, dbeta, ds0): dq, dk, dv bf16 in q, k and v's shapes, da and
+    dbeta fp32, ds0 fp32 or None."""
+    N, T, Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_bwd", q, k, v, a, beta, cu_seqlens,
+                                                (torch.bfloat16,))
+    _need(s0, "s0", torch.float32, (N, H, dk, dv))
+    _need(ds_final, "ds_final", torch.float32, (N, H, dk, dv))
+    _need(dO, "dO", torch.bfloat16, tuple(v.shape))
+    _same_device(q, s0=s0, ds_final=ds_final, dO=dO, ws=ws)
+    gq, gk, gv, ga, gb, gs = grads if grads is not None else (None,) * 6
+    gq = _new(gq, "grad_q", q, tuple(q.shape), torch.bfloat16)
+    gk = _new(gk, "grad_k", q, tuple(k.shape), torch.bfloat16)
+    gv = _new(gv, "grad_v", q, tuple(v.shape), torch.bfloat16)
+    ga = _new(ga, "grad_a", q, tuple(a.shape), torch.float32)
+    gb = _new(gb, "grad_beta", q, tuple(a.shape), torch.float32)
+    if gs is not None or (want_grad_s0 and grads is None):
+        gs = _new(gs, "grad_s0", q, (N, H, dk, dv), torch.float32)
+    if ws is None:
+        need = gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None, True)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _need(ws, "ws", torch.uint8)
+    _call_on(q, "gated_delta_chunk_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(cu_seqlens), _ptr(s0),
+             _ptr(dO), _ptr(ds_final), _ptr(gq), _ptr(gk), _ptr(gv), _ptr(ga), _ptr(gb), _ptr(gs), _ptr(ws),
+             ws.numel(), N, T, Hk, H, dk, dv, ld, float(dk ** -0.5 if scale is None else scale), GLA_BF16,
+             stream=stream)
+    return gq, gk, gv, ga, gb, gs
+
+
+def gated_delta_decode_step(state, q, k, v, a, beta, o=None, slot_idx=None, scale=None, stream=None):
+    """Gated delta rule token by token, in place on a pool of states.  state
+    [n_slots,H,dk,dv] fp32; q, k [N,Hk,dk] and v [N,H,dv] (one token), or
+    [N,T,Hk,dk] and [N,T,H,dv] (T tokens in order), bf16 or fp32; a, beta [N,H]
+    or [N,T,H] fp32; slot_idx [N] int32 or None.  Returns o in v's shape, fp32."""
+    one = q.dim() == 3
+    xs = [x.unsqueeze(1) if one else x for x in (q, k, v, a, beta)]
+    N, T, Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_decode_step", *xs, None,
+                                                (torch.bfloat16, torch.float32))
+    _need(state, "state", torch.float32)
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dk, dv):
+        raise ValueError("state must be [n_slots, %d, %d, %d]" % (H, dk, dv))
+    _need(slot_idx, "slot_idx", torch.int32, (N,))
+    if slot_idx is None and state.shape[0] != N:
+        raise ValueError("without slot_idx the state must have N slots")
+    _same_device(q, state=state, slot_idx=slot_idx)
+    o = _new(o, "o", q, tuple(v.shape), torch.float32)
+    _call_on(q, "gated_delta_decode_step", _ptr(state), _ptr(slot_idx), state.shape[0], *map(_ptr, xs), _ptr(o), N, T,
+             Hk, H, dk, dv, ld, float(dk ** -0.5 if scale is None else scale), _dt(q), stream=stream)
+    return o
+
+
+def _norm_args(x, weight, bias, gate):
+    """Check group_norm_silu's tensors; returns (M, G, d, ld_x, ld_gate, shared)."""
+    if x.dim() < 2:
+        raise ValueError("x must be [..., G, d]")
+    G, d = x.shape[-2:]
+    _need(x, "x", x.dtype, contiguous=False)
+    _dt(x)
+    _need(gate, "gate", torch.bfloat16, tuple(x.shape), contiguous=False)
+    first = weight if weight is not None else bias
+    shared = first is not None and first.dim() == 1
+    _need(weight, "weight", torch.float32, (d,) if shared else (G, d))
+    _need(bias, "bias", torch.float32, (d,) if shared else (G, d))
+    _same_device(x, weight=weight, bias=bias, gate=gate)
+    M = x.numel() // (G * d) if G * d else 0
+    return M, G, d, _rows_stride(x, "x") if M else 0, _rows_stride(gate, "gate") if gate is not None and M else 0, shared
+
+
+def group_norm_silu(x, weight=None, bias=None, gate=None, center=True, act=True, eps=1e-5, y=None, stream=None):
+    """Group norm of each row's channels with an activation: x [..., G, d] bf16
+    or fp32 (every group of d channels normalised by itself; center=False: by its
+    root mean square), weight and bias [G, d] or [d] fp32, gate [..., G, d] bf16.
+    x and gate may be slices whose rows are equally far apart.  Returns
+    n * silu(gate), or silu(n) without a gate (act=False: the identity in
+    silu's place), bf16 in x's shape."""
+    M, G, d, ldx, ldg, shared = _norm_args(x, weight, bias, gate)
+    y = _new(y, "y", x, tuple(x.shape), torch.bfloat16)
+    _call_on(x, "group_norm_silu", _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y), M, G, d, ldx, ldg,
+             int(shared), int(center), int(act), float(eps), _dt(x), stream=stream)
+    return y
+
+
+def group_norm_silu_bwd_workspace_bytes(M, G, d):
+    return int(lib().group_norm_silu_bwd_workspace_bytes(M, G, d))
+
+
+def group_norm_silu_bwd(x, dy, weight=None, bias=None, gate=None, center=True, act=True, eps=1e-5, grads=None, ws=None,
+                        stream=None):
+    """Backward of group_norm_silu.  dy [..., G, d] bf16.  Returns (dx in x's
+    type, dgate bf16 or None, dweight, dbias in the shapes of weight and bias,
+    fp32, or None)."""
+    M, G, d, ldx, ldg, shared = _norm_args(x, weight, bias, gate)
+    _need(dy, "dy", torch.bfloat16, tuple(x.shape))
+    _same_device(x, dy=dy, ws=ws)
+    gx, gg, gw, gb = grads if grads is not None else (None,) * 4
+    gx = _new(gx, "grad_x", x, tuple(x.shape), x.dtype)
+    gg = _new(gg, "grad_gate", x, tuple(x.shape), torch.bfloat16) if gate is not None else None
+    gw = _new(gw, "grad_weight", x, tuple(weight.shape), torch.float32) if weight is not None else None
+    gb = _new(gb, "grad_bias", x, tuple(bias.shape), torch.float32) if bias is not None else None
+    if ws is None and (gw is not None or gb is not None):
+        ws = torch.empty(group_norm_silu_bwd_workspace_bytes(M, G, d), dtype=torch.uint8, device=x.device)
+    _need(ws, "ws", torch.uint8)
+    _call_on(x, "group_norm_silu_bwd", _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(gx), _ptr(gg),
+             _ptr(gw), _ptr(gb), _ptr(ws), 0 if ws is None else ws.numel(), M, G, d, ldx, ldg, int(shared),
+             int(center), int(act), float(eps), _dt(x), stream=stream)
+    return gx, gg, gw, gb
 
 
 def gla_get_device_status(stream=None):

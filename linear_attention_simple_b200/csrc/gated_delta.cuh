@@ -1,0 +1,209 @@
+// gated_delta.cuh -- shared by the gated delta rule's kernels: the sequence
+// geometry, the workspace layout, warp-level matrix products on bf16
+// fragments and the splitting of fp32 values into bf16 terms.
+//
+// Chunks have 64 tokens.  With b the running sum of the log-decays inside a
+// chunk, G_i = e^{b_i}, R_i = e^{b_63 - b_i}, D_ij = e^{b_i - b_j} and S the
+// state that enters the chunk:
+//
+//   T  = (I + tril(K K^T . D_ij beta_j, -1))^-1        unit lower triangular
+//   y  = G K S - (T - I)(V - G K S)                    what the state predicts
+//   z  = V - y,   V' = beta z
+//   o  = scale G Q S + P V',   P = tril(scale Q K^T . D)
+//   S' = G_63 S + K^T (R V')
+//
+// States are held transposed, [dv][dk], with 16 dv rows to a warp: a warp's
+// rows never meet another's, so the whole recurrence of its rows stays in its
+// registers, an accumulator of one product becomes the left operand of the
+// next without a shuffle, and only the chunk's shared operands (K, Q, T, P)
+// pass through shared memory.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "gla_device.cuh"
+
+namespace gla {
+
+constexpr int kGdC = 64;                 // tokens per chunk
+constexpr int kGdPad = 8;                // bf16 elements behind each shared-memory row: rows an odd
+                                         // multiple of 16 bytes apart, so ldmatrix has no bank conflicts
+constexpr int kGdTP = kGdC + kGdPad;     // row stride of a shared T or P tile
+constexpr int kGdSc = 6;                 // per-token scalars of a chunk: G, R, beta, P_ii, b (high, low)
+enum { kScG = 0, kScR = 1, kScBeta = 2, kScPd = 3, kScBh = 4, kScBl = 5 };
+
+// Sequences of one call: dense [N][T] (cu null) or packed rows cu[n] .. cu[n+1]-1.
+struct GdSeqs {
+    const int* cu;
+    int N, T;          // T: tokens of each sequence (dense), of all together (packed)
+    int H, Hk;         // value heads, query/key heads
+    // Row of token 0 and length of sequence n; length -1 for packed offsets
+    // that are not inside 0 .. T.
+    __device__ __forceinline__ void span(int n, int64_t& row, int& len) const
+    {
+        if (!cu) {
+            row = static_cast<int64_t>(n) * T;
+            len = T;
+            return;
+        }
+        const int s = cu[n], e = cu[n + 1];
+        const bool ok = s >= 0 && e >= s && e <= T;
+        row = ok ? s : 0;
+        len = ok ? e - s : -1;
+    }
+    // Chunk slot of sequence n's first chunk: distinct for all chunks of all
+    // sequences, without the lengths on the host.
+    __device__ __forceinline__ int64_t slot0(int n, int64_t row) const
+    {
+        return cu ? row / kGdC + n : static_cast<int64_t>(n) * ((T + kGdC - 1) / kGdC);
+    }
+};
+
+inline int64_t gd_slots(bool packed, int64_t N, int64_t T)
+{
+    return packed ? T / kGdC + N : N * ((T + kGdC - 1) / kGdC);
+}
+
+// ---- asynchronous copies: 16 bytes, zero-filled when !valid (src readable anyway).
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// 64 rows of `width` bf16 values into rows of `stride`; rows from `valid` on are zeros.
+__device__ __forceinline__ void gd_load_rows(__nv_bfloat16* dst, int stride, const __nv_bfloat16* src, int64_t ld,
+                                             int width, int valid, int tid, int nthreads)
+{
+    const int per = width >> 3;
+    for (int i = tid; i < kGdC * per; i += nthreads) {
+        const int r = i / per, c = (i - r * per) * 8;
+        const bool ok = r < valid;
+        cp_async16(dst + r * stride + c, ok ? src + r * ld + c : src, ok);
+    }
+}
+
+// ---- fragments
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};\n"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Address of this lane's row for the three ldmatrix patterns, as an element
+// offset from the tile's origin, `ld` elements a row.
+//   rows_n: a 16 x 16 tile stored [n][k]: r0, r1 = the right operand of n 0-7
+//           (k 0-7, k 8-15), r2, r3 of n 8-15.
+//   rows_k: the same from a tile stored [k][n], with ldsm4_t.
+//   rows_a: a left operand of 16 rows from a tile stored [m][k].
+//   rows_at: a left operand, or an accumulator-shaped tile, from a tile stored
+//           [k][m], with ldsm4_t (and stsm4_t).
+__device__ __forceinline__ int rows_n(int lane, int ld) { return ((lane & 7) + ((lane >> 4) << 3)) * ld + (((lane >> 3) & 1) << 3); }
+__device__ __forceinline__ int rows_k(int lane, int ld) { return ((lane & 7) + (((lane >> 3) & 1) << 3)) * ld + ((lane >> 4) << 3); }
+__device__ __forceinline__ int rows_a(int lane, int ld) { return (lane & 15) * ld + ((lane >> 4) << 3); }
+__device__ __forceinline__ int rows_at(int lane, int ld) { return ((lane & 7) + ((lane >> 4) << 3)) * ld + (((lane >> 3) & 1) << 3); }
+
+// ---- fp32 values as sums of bf16 terms.  Two terms hold 16 bits of a
+// value (error at most 2^-17 of it), three 24: what the fp32 outputs need,
+// where one bf16 rounding (2^-9) would be all of the error.
+template <int NT>
+struct Split {
+    uint32_t t[NT][4];
+};
+// Two neighbouring tiles of accumulators (16 x 8 each) as the left operand of
+// a 16-deep step, in NT terms.
+template <int NT>
+__device__ __forceinline__ void split_pair(Split<NT>& s, int i, float x, float y)
+{
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const uint32_t w = pack_bf16(x, y);
+        s.t[n][i] = w;
+        if (n + 1 < NT) {
+            x -= bf16_lo(w);
+            y -= bf16_hi(w);
+        }
+    }
+}
+template <int NT>
+__device__ __forceinline__ Split<NT> split_tiles(const float (&a)[4], const float (&b)[4])
+{
+    Split<NT> s;
+    split_pair<NT>(s, 0, a[0], a[1]);
+    split_pair<NT>(s, 1, a[2], a[3]);
+    split_pair<NT>(s, 2, b[0], b[1]);
+    split_pair<NT>(s, 3, b[2], b[3]);
+    return s;
+}
+// d += s * B for an exact (one-term) right operand.
+template <int NT>
+__device__ __forceinline__ void mma_split(float (&d)[4], const Split<NT>& s, uint32_t b0, uint32_t b1)
+{
+#pragma unroll
+    for (int n = NT - 1; n >= 0; --n) mma_bf16(d, s.t[n], b0, b1);
+}
+
+// 2^x for the decay factors: x <= 0 here (0 -> 1, very negative -> 0).
+__device__ __forceinline__ float gd_exp2(float x) { return exp2f(x); }
+
+// ---- parameters
+struct GdParams {
+    GdSeqs seqs;
+    const __nv_bfloat16 *q, *k, *v, *dO;
+    const float *a, *beta, *s0, *ds_final;
+    int64_t ld_qk, ld_v, ld_do;
+    int dk, dv;
+    float scale;
+    __nv_bfloat16 *o, *dq, *dkk, *dvv;
+    float *s_final, *da, *dbeta, *ds0;
+    // workspace, one entry per chunk slot and value head (u = slot * H + h)
+    __nv_bfloat16* tm;      // [u][2][64][64]: -(T - I), high and low
+    __nv_bfloat16* pm;      // [u][1 or 2][64][64]: P without its diagonal
+    float* sc;              // [u][6][64]
+    // backward only
+    __nv_bfloat16 *sb, *eb; // [u][dv][dk]: the state entering, the gradient of the state leaving
+    float* sn;              // [u][dv / 16][dk / 8 * 128]: the state entering in fp32, a warp's register order
+    float* sn_last;         // [N H][..]: the final state in the same form
+    float* yn;              // [u][dv / 16][1024]: y in register order
+    __nv_bfloat16* vp;      // [u][64][dv]: V'
+    float* part;            // [u][3][dv / 16][64]: per-warp sums over dv
+    float* anch;            // [u][dv / 16]: <gradient of the state leaving, state leaving>
+    int64_t slots;
+    int* status;
+};
+
+gla_status gd_launch_intra(const GdParams& p, bool bwd, cudaStream_t st);
+gla_status gd_launch_sweep_fwd(const GdParams& p, bool bwd, cudaStream_t st);
+gla_status gd_launch_sweep_rev(const GdParams& p, cudaStream_t st);
+gla_status gd_launch_grad(const GdParams& p, cudaStream_t st);
+
+}  // namespace gla

@@ -1,0 +1,351 @@
+// gated_delta_grad.cu -- dq, dk, da and dbeta of the gated delta rule, every
+// chunk at once.  With X = scale dO, Y = -dv, the state S that enters the
+// chunk and the gradient E of the state that leaves it:
+//
+//   A_ij = X_i . v'_j D_ij (i >= j)      B_ij = Y_i . v'_j D_ij (i > j)
+//   dq = A K + G X S^T
+//   dk = A^T Q + B^T K + B K + G Y S^T + R V' E^T
+//   da_t = sum over i >= t in the chunk of (o.dO - dv.y - dvs.z)_i + <E, S'>
+//
+// One CTA of 4 warps per (chunk, q/k head), 16 token rows to a warp; the
+// value heads that share the q/k head are summed in its accumulators.  A
+// first pass over dv (32 columns a stage, two stages) gives A, A^T, B and
+// B^T, each warp its own rows, the tiles on the masked side left out; they
+// become left operands in place (bf16) and multiply K and Q; a second pass
+// adds the three products with the states.  Both transposes are computed
+// rather than exchanged: 64 x 64 tiles over dv cost less than a trip through
+// shared memory.  dq and dk leave in bf16, so every operand is one bf16
+// rounding of its value; the sums behind da and dbeta come in fp32 from the
+// sweeps.
+#include "gated_delta.cuh"
+
+namespace gla {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kSl = 32;                    // dv columns per stage
+constexpr int kVs = kSl + kGdPad;          // row stride of a staged token slice
+
+template <int DK>
+struct GradSmem {
+    static constexpr int KS = DK + kGdPad;
+    static constexpr int tok = kGdC * kVs;             // one staged token slice
+    static constexpr int st = kSl * KS;                // one staged state slice
+    static constexpr int stage = 3 * tok + 2 * st;
+    static constexpr int bytes = (2 * kGdC * KS + 2 * stage) * 2 + kGdSc * kGdC * 4;
+};
+
+struct Src {
+    const __nv_bfloat16 *d, *y, *vp, *s, *e;
+    int64_t ld_do, ld_dv;
+    int dv, valid;
+};
+
+// Stage i of pass 1 (dO, dv, V') or of pass 2 (those and both states).
+template <int DK>
+__device__ __forceinline__ void load_slice(__nv_bfloat16* st, const Src& x, int col, bool states, int tid)
+{
+    constexpr int KS = GradSmem<DK>::KS, tok = GradSmem<DK>::tok;
+    gd_load_rows(st, kVs, x.d + col, x.ld_do, kSl, x.valid, tid, kThreads);
+    gd_load_rows(st + tok, kVs, x.y + col, x.ld_dv, kSl, x.valid, tid, kThreads);
+    gd_load_rows(st + 2 * tok, kVs, x.vp + col, x.dv, kSl, kGdC, tid, kThreads);
+    if (states) {
+        __nv_bfloat16* ss = st + 3 * tok;
+        for (int i = tid; i < 2 * kSl * (DK / 8); i += kThreads) {
+            const int which = i / (kSl * (DK / 8)), j = i - which * (kSl * (DK / 8));
+            const int r = j / (DK / 8), c = (j - r * (DK / 8)) * 8;
+            cp_async16(ss + which * GradSmem<DK>::st + r * KS + c,
+                       (which ? x.e : x.s) + static_cast<int64_t>(col + r) * DK + c, true);
+        }
+    }
+}
+
+// The left operand of two neighbouring accumulator tiles, rounded to bf16.
+__device__ __forceinline__ void to_a(uint32_t (&r)[4], const float (&a)[4], const float (&b)[4])
+{
+    r[0] = pack_bf16(a[0], a[1]);
+    r[1] = pack_bf16(a[2], a[3]);
+    r[2] = pack_bf16(b[0], b[1]);
+    r[3] = pack_bf16(b[2], b[3]);
+}
+// A left operand's rows g and g + 8 times f0 and f1.
+__device__ __forceinline__ void scale_a(uint32_t (&r)[4], float f0, float f1)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f = i & 1 ? f1 : f0;
+        r[i] = pack_bf16(f * bf16_lo(r[i]), f * bf16_hi(r[i]));
+    }
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
+{
+    using M = GradSmem<DK>;
+    constexpr int KS = M::KS, NT = DK / 8;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    __nv_bfloat16* sk = reinterpret_cast<__nv_bfloat16*>(smem_raw);
+    __nv_bfloat16* sq = sk + kGdC * KS;
+    __nv_bfloat16* sst = sq + kGdC * KS;
+    float* sc = reinterpret_cast<float*>(sst + 2 * M::stage);
+
+    const int64_t slot = blockIdx.x;
+    const int hk = blockIdx.y;
+    // the sequence of this slot
+    int n = 0;
+    if (!p.seqs.cu) {
+        n = static_cast<int>(slot / ((p.seqs.T + kGdC - 1) / kGdC));
+    } else {
+        int hi = p.seqs.N - 1;
+        while (n < hi) {
+            const int mid = (n + hi + 1) >> 1;
+            const int c = max(p.seqs.cu[mid], 0);
+            if (c / kGdC + mid <= slot) n = mid;
+            else hi = mid - 1;
+        }
+    }
+    int64_t row0;
+    int len;
+    p.seqs.span(n, row0, len);
+    if (len < 0) return;
+    const int64_t c = slot - p.seqs.slot0(n, row0);
+    if (c < 0 || c * kGdC >= len) return;
+    const int valid = min(kGdC, len - static_cast<int>(c) * kGdC);
+    const int64_t row = row0 + c * kGdC;
+    const int H = p.seqs.H, group = H / p.seqs.Hk;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, c2 = (lane & 3) * 2;
+    const int nst = p.dv / kSl, wtot = p.dv >> 4;
+
+    gd_load_rows(sk, KS, p.k + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
+    gd_load_rows(sq, KS, p.q + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
+
+    float dq[NT][4], dk[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dq[t][e] = dk[t][e] = 0.f;
+
+    for (int j = 0; j < group; ++j) {
+        const int h = hk * group + j;
+        const int64_t u = slot * H + h;
+        Src x{p.dO + row * p.ld_do + static_cast<int64_t>(h) * p.dv, p.dvv + row * H * p.dv + static_cast<int64_t>(h) * p.dv,
+              p.vp + u * kGdC * p.dv, p.sb + u * p.dv * DK, p.eb + u * p.dv * DK,
+              p.ld_do, static_cast<int64_t>(H) * p.dv, p.dv, valid};
+        __syncthreads();                   // the last head's scalars and stages are read
+        for (int i = tid; i < kGdSc * kGdC; i += kThreads) sc[i] = p.sc[u * kGdSc * kGdC + i];
+        load_slice<DK>(sst, x, 0, false, tid);
+        cp_async_commit();
+
+        // pass 1: products over dv of 16 rows with the 64 tokens, before the masks
+        float fa[8][4], fat[8][4], fb[8][4], fbt[8][4];
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) fa[t][e] = fat[t][e] = fb[t][e] = fbt[t][e] = 0.f;
+        for (int i = 0; i < nst; ++i) {
+            cp_async_wait<0>();
+            __syncthreads();
+            if (i + 1 < nst) load_slice<DK>(sst + ((i + 1) & 1) * M::stage, x, (i + 1) * kSl, false, tid);
+            cp_async_commit();
+            const __nv_bfloat16* st = sst + (i & 1) * M::stage;
+            const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
+            const uint32_t br = smem_u32(st + rows_n(lane, kVs));
+            constexpr int tk = M::tok * 2, rp = 16 * kVs * 2;
+#pragma unroll
+            for (int s = 0; s < kSl / 16; ++s) {
+                uint32_t d[4], y[4], v[4];
+                ldsm4(d, ar + s * 32);
+                ldsm4(y, ar + tk + s * 32);
+                ldsm4(v, ar + 2 * tk + s * 32);
+#pragma unroll
+                for (int np = 0; np < 4; ++np) {
+                    uint32_t b[4];
+                    if (np <= w) {
+                        ldsm4(b, br + 2 * tk + np * rp + s * 32);
+                        mma_bf16(fa[2 * np], d, b[0], b[1]);
+                        mma_bf16(fa[2 * np + 1], d, b[2], b[3]);
+                        mma_bf16(fb[2 * np], y, b[0], b[1]);
+                        mma_bf16(fb[2 * np + 1], y, b[2], b[3]);
+                    }
+                    if (np >= w) {
+                        ldsm4(b, br + np * rp + s * 32);
+                        mma_bf16(fat[2 * np], v, b[0], b[1]);
+                        mma_bf16(fat[2 * np + 1], v, b[2], b[3]);
+                        ldsm4(b, br + tk + np * rp + s * 32);
+                        mma_bf16(fbt[2 * np], v, b[0], b[1]);
+                        mma_bf16(fbt[2 * np + 1], v, b[2], b[3]);
+                    }
+                }
+            }
+        }
+        __syncthreads();                   // both stages are read
+        load_slice<DK>(sst, x, 0, true, tid);
+        cp_async_commit();
+
+        // da and dbeta of this head: one warp, two tokens a lane
+        if (w == (j & 3)) {
+            const float* part = p.part + u * 3 * wtot * kGdC + 2 * lane;
+            float2 od = make_float2(0.f, 0.f), s1 = od, s2 = od;
+            float tail = 0.f;
+            for (int t = 0; t < wtot; ++t) {
+                const float2 a = *reinterpret_cast<const float2*>(part + t * kGdC);
+                const float2 b = *reinterpret_cast<const float2*>(part + (wtot + t) * kGdC);
+                const float2 e = *reinterpret_cast<const float2*>(part + (2 * wtot + t) * kGdC);
+                od.x += a.x; od.y += a.y;
+                s1.x += b.x; s1.y += b.y;
+                s2.x += e.x; s2.y += e.y;
+                tail += p.anch[u * wtot + t];
+            }
+            const float d1 = od.y - s1.y;
+            float s = (od.x - s1.x) + d1;          // sums over this lane's tokens and all later ones
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float z = __shfl_down_sync(0xFFFFFFFFu, s, o);
+                if (lane + o < 32) s += z;
+            }
+            const float after = __shfl_down_sync(0xFFFFFFFFu, s, 1);
+            const float later = lane < 31 ? after : 0.f;
+            const int64_t at = (row + 2 * lane) * H + h;
+            if (2 * lane < valid) {
+                p.da[at] = s + tail;
+                p.dbeta[at] = s2.x / sc[kScBeta * kGdC + 2 * lane];
+            }
+            if (2 * lane + 1 < valid) {
+                p.da[at + H] = later + d1 + tail;
+                p.dbeta[at + H] = s2.y / sc[kScBeta * kGdC + 2 * lane + 1];
+            }
+        }
+
+        // masks and decays; A and B by rows i = this warp's, A^T and B^T by rows j
+        const float bh0 = sc[kScBh * kGdC + 16 * w + g], bl0 = sc[kScBl * kGdC + 16 * w + g];
+        const float bh1 = sc[kScBh * kGdC + 16 * w + g + 8], bl1 = sc[kScBl * kGdC + 16 * w + g + 8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 16 * w + g + 8 * (e >> 1), q = 8 * t + c2 + (e & 1);
+                const float diff = ((e >> 1 ? bh1 : bh0) - sc[kScBh * kGdC + q]) + ((e >> 1 ? bl1 : bl0) - sc[kScBl * kGdC + q]);
+                const float d = gd_exp2(-fabsf(diff));          // D between the earlier and the later token
+                const float ds = d * p.scale;
+                fa[t][e] = q <= r ? fa[t][e] * ds : 0.f;
+                fb[t][e] = q < r ? -fb[t][e] * d : 0.f;
+                fat[t][e] = q >= r ? fat[t][e] * ds : 0.f;
+                fbt[t][e] = q > r ? -fbt[t][e] * d : 0.f;
+            }
+        }
+        // dq += A K; dk += A^T Q + (B + B^T) K: B + B^T has one rounding, both halves in place
+        {
+            const uint32_t kt = smem_u32(sk + rows_k(lane, KS)), qt = smem_u32(sq + rows_k(lane, KS));
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                uint32_t a[4], at[4], bb[4];
+                to_a(a, fa[2 * s], fa[2 * s + 1]);
+                to_a(at, fat[2 * s], fat[2 * s + 1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    fb[2 * s][e] += fbt[2 * s][e];
+                    fb[2 * s + 1][e] += fbt[2 * s + 1][e];
+                }
+                to_a(bb, fb[2 * s], fb[2 * s + 1]);
+#pragma unroll
+                for (int np = 0; np < DK / 16; ++np) {
+                    uint32_t kf[4], qf[4];
+                    ldsm4_t(kf, kt + s * 16 * KS * 2 + np * 32);
+                    if (s <= w) {
+                        mma_bf16(dq[2 * np], a, kf[0], kf[1]);
+                        mma_bf16(dq[2 * np + 1], a, kf[2], kf[3]);
+                    }
+                    mma_bf16(dk[2 * np], bb, kf[0], kf[1]);
+                    mma_bf16(dk[2 * np + 1], bb, kf[2], kf[3]);
+                    if (s >= w) {
+                        ldsm4_t(qf, qt + s * 16 * KS * 2 + np * 32);
+                        mma_bf16(dk[2 * np], at, qf[0], qf[1]);
+                        mma_bf16(dk[2 * np + 1], at, qf[2], qf[3]);
+                    }
+                }
+            }
+        }
+        // pass 2: dq += G X S^T, dk += G Y S^T + R V' E^T
+        const float G0 = sc[kScG * kGdC + 16 * w + g], G1 = sc[kScG * kGdC + 16 * w + g + 8];
+        const float R0 = sc[kScR * kGdC + 16 * w + g], R1 = sc[kScR * kGdC + 16 * w + g + 8];
+        for (int i = 0; i < nst; ++i) {
+            cp_async_wait<0>();
+            __syncthreads();
+            if (i + 1 < nst) load_slice<DK>(sst + ((i + 1) & 1) * M::stage, x, (i + 1) * kSl, true, tid);
+            cp_async_commit();
+            const __nv_bfloat16* st = sst + (i & 1) * M::stage;
+            const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
+            const uint32_t sr = smem_u32(st + 3 * M::tok + rows_k(lane, KS));
+            constexpr int tk = M::tok * 2;
+#pragma unroll
+            for (int s = 0; s < kSl / 16; ++s) {
+                uint32_t d[4], y[4], v[4];
+                ldsm4(d, ar + s * 32);
+                ldsm4(y, ar + tk + s * 32);
+                ldsm4(v, ar + 2 * tk + s * 32);
+                scale_a(d, p.scale * G0, p.scale * G1);
+                scale_a(y, -G0, -G1);
+                scale_a(v, R0, R1);
+#pragma unroll
+                for (int np = 0; np < DK / 16; ++np) {
+                    uint32_t sf[4], ef[4];
+                    ldsm4_t(sf, sr + s * 16 * KS * 2 + np * 32);
+                    ldsm4_t(ef, sr + M::st * 2 + s * 16 * KS * 2 + np * 32);
+                    mma_bf16(dq[2 * np], d, sf[0], sf[1]);
+                    mma_bf16(dq[2 * np + 1], d, sf[2], sf[3]);
+                    mma_bf16(dk[2 * np], y, sf[0], sf[1]);
+                    mma_bf16(dk[2 * np + 1], y, sf[2], sf[3]);
+                    mma_bf16(dk[2 * np], v, ef[0], ef[1]);
+                    mma_bf16(dk[2 * np + 1], v, ef[2], ef[3]);
+                }
+            }
+        }
+    }
+    // out through this warp's own rows of the K and Q tiles
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int at = (16 * w + g + 8 * hf) * KS + 8 * t + c2;
+            *reinterpret_cast<uint32_t*>(sq + at) = pack_bf16(dq[t][2 * hf], dq[t][2 * hf + 1]);
+            *reinterpret_cast<uint32_t*>(sk + at) = pack_bf16(dk[t][2 * hf], dk[t][2 * hf + 1]);
+        }
+    __syncwarp();
+    const int64_t ld = static_cast<int64_t>(p.seqs.Hk) * DK;
+    for (int i = lane; i < 16 * (DK / 8); i += 32) {
+        const int r = 16 * w + i / (DK / 8), cc = (i % (DK / 8)) * 8;
+        if (r < valid) {
+            const int64_t at = (row + r) * ld + hk * DK + cc;
+            *reinterpret_cast<uint4*>(p.dq + at) = *reinterpret_cast<const uint4*>(sq + r * KS + cc);
+            *reinterpret_cast<uint4*>(p.dkk + at) = *reinterpret_cast<const uint4*>(sk + r * KS + cc);
+        }
+    }
+}
+
+template <int DK>
+gla_status launch(const GdParams& p, cudaStream_t st)
+{
+    constexpr int smem = GradSmem<DK>::bytes;
+    cudaError_t e = cudaFuncSetAttribute(gd_grad_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return status_of(e);
+    trace_begin(st);
+    gd_grad_kernel<DK><<<dim3(static_cast<unsigned>(p.slots), static_cast<unsigned>(p.seqs.Hk)), kThreads, smem, st>>>(p);
+    trace_end(st, "gd_grad_kernel");
+    count_launch();
+    return check_launch("gd_grad_kernel");
+}
+
+}  // namespace
+
+gla_status gd_launch_grad(const GdParams& p, cudaStream_t st)
+{
+    if (p.slots == 0) return GLA_OK;
+    switch (p.dk) {
+    case 64: return launch<64>(p, st);
+    case 96: return launch<96>(p, st);
+    default: return launch<128>(p, st);
+    }
+}
+
+}  // namespace gla

@@ -1,0 +1,341 @@
+"""The gated delta rule on the GPU against the token recurrence in 64 bits.
+
+Tolerances (relative 2-norm), from the roundings on each path; a bf16 rounding
+is off by at most U = 2^-8 of the value, a pair of bf16 terms by 2^-17:
+  o         rounded itself, and S, P and V' each once before their products:
+            four independent roundings, sqrt(4) U = 2 U.
+  dq, dk    rounded, and dO or dv, V' (twice) and the state each once: 2.5 U.
+  dv        computed from pairs, rounded once: U, and 2^-14 for the pairs.
+  S_T, dS0, dbeta   a pair for each operand of the four products on a chunk's
+            path, and 2^-17 of what the chunk before left: 8 x 2^-17.
+  da        sums of up to 64 tokens' terms of either sign: sqrt(64) = 8 times
+            that of its terms (2 x 2^-17, three terms elsewhere): 16 x 2^-17.
+            Under strong decays the terms themselves (o.dO) are up to 8 times
+            the sums, so the error is taken against the larger of the two.
+"""
+import pytest
+import torch
+
+import linear_attention_simple_b200 as gla
+from delta_reference import backward, forward, recurrence, rel
+
+pytestmark = pytest.mark.gpu
+
+U, P = 2.0 ** -8, 2.0 ** -17
+TOL_O, TOL_QK, TOL_V, TOL_S, TOL_DA = 2 * U, 2.5 * U, U + 2.0 ** -14, 8 * P, 16 * P
+
+
+def make(lead, Hk, H, dk, dv, seed, decay="usual", dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rnd(*s):
+        return torch.randn(s, generator=g, device="cuda")
+
+    q, k = rnd(*lead, Hk, dk), rnd(*lead, Hk, dk) + 0.5 * rnd(*(1,) * len(lead), Hk, dk)
+    a = {"usual": lambda: torch.nn.functional.logsigmoid(rnd(*lead, H) + 3),
+         "slow": lambda: -0.002 * torch.rand((*lead, H), generator=g, device="cuda"),
+         "none": lambda: torch.zeros((*lead, H), device="cuda"),
+         "strong": lambda: -8 * torch.rand((*lead, H), generator=g, device="cuda"),
+         "resets": lambda: torch.where(torch.rand((*lead, H), generator=g, device="cuda") < 0.05, -1e4, -0.05)}[decay]()
+    return dict(q=(q / q.norm(dim=-1, keepdim=True)).to(dtype), k=(k / k.norm(dim=-1, keepdim=True)).to(dtype),
+                v=rnd(*lead, H, dv).to(dtype), a=a, beta=torch.sigmoid(rnd(*lead, H)))
+
+
+def states(N, H, dk, dv, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return 0.1 * torch.randn((N, H, dk, dv), generator=g, device="cuda")
+
+
+def cu_of(lens):
+    c = [0]
+    for n in lens:
+        c.append(c[-1] + n)
+    return torch.tensor(c, dtype=torch.int32, device="cuda")
+
+
+def args(d):
+    return d["q"], d["k"], d["v"], d["a"], d["beta"]
+
+
+def check_fwd(d, s0, cu=None):
+    dk, z = d["q"].shape[-1], s0
+    if s0 is None:
+        N = cu.numel() - 1 if cu is not None else d["q"].shape[0]
+        z = torch.zeros(N, d["v"].shape[-2], dk, d["v"].shape[-1], device="cuda")
+    o, s = gla.gated_delta_chunk_fwd(*args(d), s0=s0, cu_seqlens=cu)
+    ro, rs = forward(d, z, dk ** -0.5, cu)
+    assert rel(o, ro) <= TOL_O and rel(s, rs) <= TOL_S, (rel(o, ro), rel(s, rs))
+
+
+def check_bwd(d, s0, dO, ds, cu=None, da_of_terms=False):
+    dk = d["q"].shape[-1]
+    N = cu.numel() - 1 if cu is not None else d["q"].shape[0]
+    z = torch.zeros(N, d["v"].shape[-2], dk, d["v"].shape[-1], device="cuda")
+    got = gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds, cu_seqlens=cu)
+    ref = backward(d, z if s0 is None else s0, dO, z if ds is None else ds, dk ** -0.5, cu)
+    for n, x, y, tol in zip(("dq", "dk", "dv", "da", "dbeta", "ds0"), got, ref,
+                            (TOL_QK, TOL_QK, TOL_V, TOL_DA, TOL_S, TOL_S)):
+        y = torch.zeros_like(x) if y is None else y
+        if n == "da" and da_of_terms:
+            o, _ = forward(d, z if s0 is None else s0, dk ** -0.5, cu)
+            terms = float((o * dO.double()).sum(-1).norm())
+            assert float((x - y).norm()) <= tol * max(terms, float(y.norm()))
+            continue
+        assert rel(x, y) <= tol, (n, rel(x, y), tol)
+    return got
+
+
+SHAPES = [  # N, T, Hk, H, dk, dv
+    (1, 1, 1, 1, 96, 192), (2, 1, 2, 4, 64, 32), (1, 63, 1, 1, 64, 64), (2, 64, 1, 2, 96, 192), (1, 65, 2, 2, 128, 128),
+    (3, 130, 2, 6, 128, 96), (1, 200, 16, 16, 96, 192), (2, 97, 1, 3, 128, 256), (1, 129, 3, 3, 64, 160),
+    (1, 66, 1, 1, 96, 224), (140, 67, 1, 1, 96, 192), (12, 70, 4, 16, 64, 128),
+]
+
+
+@pytest.mark.parametrize("N,T,Hk,H,dk,dv", SHAPES)
+@pytest.mark.parametrize("with_s0", [False, True])
+def test_chunk_fwd(N, T, Hk, H, dk, dv, with_s0):
+    check_fwd(make((N, T), Hk, H, dk, dv, 1 + T), states(N, H, dk, dv, 2) if with_s0 else None)
+
+
+@pytest.mark.parametrize("N,T,Hk,H,dk,dv", SHAPES)
+@pytest.mark.parametrize("with_states", [False, True])
+def test_chunk_bwd(N, T, Hk, H, dk, dv, with_states):
+    d = make((N, T), Hk, H, dk, dv, 3 + T)
+    dO = make((N, T), Hk, H, dk, dv, 4 + T)["v"]
+    s0, ds = (states(N, H, dk, dv, 5), states(N, H, dk, dv, 6)) if with_states else (None, None)
+    check_bwd(d, s0, dO, ds)
+
+
+@pytest.mark.parametrize("decay", ["slow", "none", "strong", "resets"])
+def test_decays(decay):
+    d = make((2, 150), 2, 2, 96, 192, 7, decay)
+    s0, ds, dO = states(2, 2, 96, 192, 8), states(2, 2, 96, 192, 9), make((2, 150), 2, 2, 96, 192, 10)["v"]
+    check_fwd(d, s0)
+    check_bwd(d, s0, dO, ds, da_of_terms=decay in ("strong", "resets"))
+
+
+def test_a_minus_infinity_is_a_reset():
+    d = make((1, 100), 1, 1, 96, 192, 11)
+    d["a"][0, 40] = -float("inf")
+    o, s = gla.gated_delta_chunk_fwd(*args(d))
+    ro, rs = forward(d, torch.zeros(1, 1, 96, 192, device="cuda"), 96 ** -0.5)
+    assert rel(o, ro) <= TOL_O and rel(s, rs) <= TOL_S
+
+
+@pytest.mark.parametrize("beta", [0.0, 1.0, 2.0])
+def test_write_strengths(beta):
+    """beta = 0 (nothing written, dbeta still defined), 1 (the prediction replaced) and 2 (a reflection)."""
+    d = make((1, 140), 1, 2, 96, 192, 12)
+    d["beta"].fill_(beta)
+    dO = make((1, 140), 1, 2, 96, 192, 13)["v"]
+    s0, ds = states(1, 2, 96, 192, 14), states(1, 2, 96, 192, 15)
+    check_fwd(d, s0)
+    got = gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds)
+    ref = backward(d, s0, dO, ds, 96 ** -0.5)
+    for x, y, tol in zip(got, ref, (TOL_QK, TOL_QK, TOL_V, TOL_DA, TOL_S, TOL_S)):
+        if not float(y.norm()):
+            assert float(x.float().norm()) <= 1e-25         # dv = 0: beta stands at 1e-30
+        else:
+            assert rel(x, y) <= tol, rel(x, y)
+
+
+def test_keys_that_repeat_and_keys_of_zero():
+    d = make((1, 128), 1, 1, 96, 192, 16)
+    d["k"][:, :64] = d["k"][:, :1]
+    d["k"][:, 100:110] = 0
+    d["q"][:, 5] = 0
+    check_fwd(d, None)
+    check_bwd(d, None, make((1, 128), 1, 1, 96, 192, 17)["v"], None)
+
+
+@pytest.mark.parametrize("lens", [[1], [0], [64, 64], [5, 0, 1, 130, 63, 65], [0, 0, 200, 0], [3] * 40])
+def test_packed(lens):
+    cu = cu_of(lens)
+    T, N = int(cu[-1]), len(lens)
+    d = make((T,), 2, 4, 96, 192, 18)
+    s0, ds, dO = states(N, 4, 96, 192, 19), states(N, 4, 96, 192, 20), make((T,), 2, 4, 96, 192, 21)["v"]
+    if T == 0:
+        o, s = gla.gated_delta_chunk_fwd(*args(d), s0=s0, cu_seqlens=cu)
+        got = gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds, cu_seqlens=cu)
+        assert torch.equal(s, s0) and torch.equal(got[5], ds)
+        return
+    check_fwd(d, s0, cu)
+    check_bwd(d, s0, dO, ds, cu)
+
+
+def test_rows_outside_every_sequence_stay():
+    cu = torch.tensor([7, 80, 150], dtype=torch.int32, device="cuda")
+    d = make((160,), 1, 2, 96, 192, 22)
+    dO = make((160,), 1, 2, 96, 192, 23)["v"]
+    o = torch.full_like(d["v"], 5.0)
+    gla.gated_delta_chunk_fwd(*args(d), cu_seqlens=cu, o=o)
+    grads = [torch.full_like(x, 5.0) for x in args(d)] + [None]
+    gla.gated_delta_chunk_bwd(*args(d), dO, cu_seqlens=cu, grads=grads)
+    ro, _ = forward(d, torch.zeros(2, 2, 96, 192, device="cuda"), 96 ** -0.5, cu)
+    assert rel(o[7:150], ro) <= TOL_O
+    for x in [o] + grads[:5]:
+        assert bool((x[:7] == 5).all()) and bool((x[150:] == 5).all())
+
+
+def test_offsets_outside_the_rows_are_reported():
+    d = make((100,), 1, 1, 96, 192, 24)
+    gla.gla_get_device_status()
+    for bad in ([0, 50, 120], [0, 60, 40], [-5, 50, 100]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        gla.gated_delta_chunk_fwd(*args(d), cu_seqlens=cu)
+        assert gla.gla_get_device_status() == 1
+        gla.gated_delta_chunk_bwd(*args(d), d["v"], cu_seqlens=cu)
+        assert gla.gla_get_device_status() == 1
+    check_fwd(make((1, 100), 1, 1, 96, 192, 24), None)
+
+
+def test_views_into_a_fused_projection():
+    N, T, Hk, H, dk, dv = 2, 90, 2, 4, 96, 192
+    d = make((N, T), Hk, H, dk, dv, 25)
+    buf = torch.full((N, T, 2 * Hk * dk + H * dv + 40), float("nan"), dtype=torch.bfloat16, device="cuda")
+    at, views = 0, {}
+    for n, h, w in (("q", Hk, dk), ("k", Hk, dk), ("v", H, dv)):
+        buf[..., at:at + h * w] = d[n].reshape(N, T, -1)
+        views[n] = buf[..., at:at + h * w].unflatten(-1, (h, w))
+        at += h * w
+    e = dict(d, **views)
+    dO, s0 = make((N, T), Hk, H, dk, dv, 26)["v"], states(N, H, dk, dv, 27)
+    for x, y in zip(gla.gated_delta_chunk_fwd(*args(e), s0=s0), gla.gated_delta_chunk_fwd(*args(d), s0=s0)):
+        assert torch.equal(x, y)
+    for x, y in zip(gla.gated_delta_chunk_bwd(*args(e), dO, s0=s0), gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0)):
+        assert torch.equal(x, y)
+    st = states(2, H, dk, dv, 28)
+    st2 = st.clone()
+    assert torch.equal(gla.gated_delta_decode_step(st, *args(e)), gla.gated_delta_decode_step(st2, *args(d)))
+    assert torch.equal(st, st2)
+
+
+def test_workspace_contents_do_not_matter_and_calls_repeat():
+    d = make((2, 333), 2, 4, 96, 192, 29)
+    dO, s0, ds = make((2, 333), 2, 4, 96, 192, 30)["v"], states(2, 4, 96, 192, 31), states(2, 4, 96, 192, 32)
+    outs = []
+    for fill in (0, 255):
+        wf = torch.full((gla.gated_delta_chunk_workspace_bytes(2, 333, 4),), fill, dtype=torch.uint8, device="cuda")
+        wb = torch.full((gla.gated_delta_chunk_workspace_bytes(2, 333, 4, for_bwd=True),), fill, dtype=torch.uint8,
+                        device="cuda")
+        outs.append(gla.gated_delta_chunk_fwd(*args(d), s0=s0, ws=wf) +
+                    gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds, ws=wb))
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
+def test_other_stream_and_graph_replay():
+    d = make((1, 130), 1, 2, 96, 192, 33)
+    dO, s0 = make((1, 130), 1, 2, 96, 192, 34)["v"], states(1, 2, 96, 192, 35)
+    want = gla.gated_delta_chunk_fwd(*args(d), s0=s0) + gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = gla.gated_delta_chunk_fwd(*args(d), s0=s0) + gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0)
+    side.synchronize()
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = gla.gated_delta_chunk_fwd(*args(d), s0=s0) + gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0)
+    new = make((1, 130), 1, 2, 96, 192, 36)
+    for n in d:
+        d[n].copy_(new[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    want = gla.gated_delta_chunk_fwd(*args(new), s0=s0) + gla.gated_delta_chunk_bwd(*args(new), dO, s0=s0)
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+
+
+def test_gradients_against_differences():
+    """Central differences of the loss along random directions, by the GPU's own
+    forward: the loss in fp32 from S_T and the step's fp32 outputs (bf16 o would
+    drown the difference).  Second-order terms cancel; third-order ones and the
+    2^-17 of the states over a step of 2^-4 bound the error by 1%."""
+    N, T, H, dk, dv, h = 1, 70, 1, 96, 192, 2.0 ** -4
+    d = make((N, T), H, H, dk, dv, 37)
+    ds, zero = states(N, H, dk, dv, 38), torch.zeros(N, H, dk, dv, device="cuda")
+    dO = torch.zeros_like(d["v"])
+    got = gla.gated_delta_chunk_bwd(*args(d), dO, ds_final=ds)
+    g = torch.Generator(device="cuda").manual_seed(39)
+    for n, grad in zip(("a", "beta"), got[3:5]):
+        x = torch.randn(d[n].shape, generator=g, device="cuda")
+        side = []
+        for sign in (1, -1):
+            e = dict(d)
+            e[n] = d[n] + sign * h * x
+            side.append(float((gla.gated_delta_chunk_fwd(*args(e), s0=zero)[1].double() * ds).sum()))
+        diff, want = (side[0] - side[1]) / (2 * h), float((grad.double() * x).sum())
+        scale = float((grad.double() * x).abs().sum())
+        assert abs(diff - want) <= 1e-2 * scale, (n, diff, want)
+
+
+# ---------------------------------------------------------------- step
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,T,Hk,H,dk,dv", [(1, 1, 1, 1, 96, 192), (3, 1, 16, 16, 96, 192), (2, 5, 2, 4, 128, 256),
+                                            (5, 2, 1, 3, 64, 32), (40, 3, 8, 16, 128, 128), (30, 1, 16, 16, 64, 160)])
+def test_step(N, T, Hk, H, dk, dv, dtype):
+    """All fp32: a few hundred additions at 2^-24 each, 2e-6 in the 2-norm."""
+    d = make((N, T), Hk, H, dk, dv, 40, dtype=dtype)
+    slots = N + 3
+    st = states(slots, H, dk, dv, 41)
+    before = st.clone()
+    idx = torch.randperm(slots, generator=torch.Generator().manual_seed(42))[:N].to(torch.int32).cuda()
+    o = gla.gated_delta_decode_step(st, *args(d), slot_idx=idx)
+    ro, rs = forward(d, before[idx.long()], dk ** -0.5)
+    assert o.dtype == torch.float32 and rel(o, ro) <= 2e-6 and rel(st[idx.long()], rs) <= 2e-6
+    rest = [i for i in range(slots) if i not in idx.tolist()]
+    assert torch.equal(st[rest], before[rest])
+    if T == 1:
+        st2 = before.clone()
+        o2 = gla.gated_delta_decode_step(st2, *[d[n][:, 0] for n in ("q", "k", "v", "a", "beta")], slot_idx=idx)
+        assert torch.equal(o2, o[:, 0]) and torch.equal(st2, st)
+
+
+def test_step_skips_slots_outside_the_pool():
+    d = make((4, 1), 2, 2, 96, 192, 43)
+    st = states(3, 2, 96, 192, 44)
+    before = st.clone()
+    gla.gla_get_device_status()
+    o = torch.full((4, 1, 2, 192), 7.0, device="cuda")
+    idx = torch.tensor([2, -1, 3, 0], dtype=torch.int32, device="cuda")
+    gla.gated_delta_decode_step(st, *args(d), slot_idx=idx, o=o)
+    assert gla.gla_get_device_status() == 1
+    assert torch.equal(st[1], before[1]) and bool((o[1:3] == 7).all())
+    pick = {n: x[[0, 3]] for n, x in d.items()}
+    ro, rs = forward(pick, before[[2, 0]], 96 ** -0.5)
+    assert rel(o[[0, 3]], ro) <= 2e-6 and rel(st[[2, 0]], rs) <= 2e-6
+
+
+def test_prefill_decode_and_norm_together():
+    """A serving step as it is used: packed prefill into states, then decoded
+    tokens in the pool, each followed by the gated norm; against one recurrence
+    over all tokens."""
+    lens, H, dk, dv = [70, 5, 129], 4, 96, 192
+    cu, more = cu_of(lens), 6
+    d, tail = make((sum(lens),), 2, H, dk, dv, 45), make((3, more), 2, H, dk, dv, 46)
+    gate, gate2 = make((sum(lens),), 2, H, dk, dv, 47)["v"], make((3, more), 2, H, dk, dv, 48)["v"]
+    w = 1 + 0.1 * torch.randn(H, dv, generator=torch.Generator().manual_seed(49)).cuda()
+    o, s = gla.gated_delta_chunk_fwd(*args(d), cu_seqlens=cu)
+    y = gla.group_norm_silu(o, w, gate=gate)
+    pool = torch.zeros(5, H, dk, dv, device="cuda")
+    idx = torch.tensor([4, 0, 2], dtype=torch.int32, device="cuda")
+    pool[idx.long()] = s
+    ys = []
+    for t in range(more):
+        od = gla.gated_delta_decode_step(pool, *[tail[n][:, t].contiguous() for n in tail], slot_idx=idx)
+        ys.append(gla.group_norm_silu(od, w, gate=gate2[:, t]))
+    from delta_reference import norm
+    zero = torch.zeros(1, H, dk, dv, dtype=torch.float64, device="cuda")
+    for i, (b, e) in enumerate(zip(cu[:-1].tolist(), cu[1:].tolist())):
+        whole = {n: torch.cat([d[n][b:e], tail[n][i]])[None].double() for n in d}
+        ro, rs = recurrence(*args(whole), zero, dk ** -0.5)
+        gates = torch.cat([gate[b:e], gate2[i]])[None].double()
+        # the norm passes o's relative error on, and rounds once more
+        ref = norm(ro, w.double(), None, gates, True, True, 1e-5)[0]
+        assert rel(y[b:e], ref[:e - b]) <= TOL_O + 2 * U
+        assert rel(torch.stack([x[i] for x in ys]), ref[e - b:]) <= 2 * U
+        assert rel(pool[idx[i].long()], rs[0]) <= TOL_S

@@ -1,0 +1,115 @@
+"""Group norm with an activation on the GPU against the formula in 64 bits.
+
+y, dgate and a bf16 dx are rounded once from fp32: at most 2^-8 of the value,
+and fp32 sums over at most 1,024 channels before that (2e-6).  An fp32 dx: the
+sums alone.  dweight and dbias: fp32 sums over the rows, 1e-5 of their terms'
+2-norm."""
+import pytest
+import torch
+
+import linear_attention_simple_b200 as gla
+from delta_reference import norm, rel
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+
+CASES = [  # M, G, d, dtype, gate, center, shared, weight, bias, act
+    (1, 1, 8, torch.bfloat16, True, True, False, True, True, True),
+    (3, 5, 24, torch.float32, False, True, True, True, True, True),
+    (37, 16, 192, torch.bfloat16, True, True, False, True, True, True),
+    (37, 16, 128, torch.float32, True, False, True, True, False, True),
+    (700, 2, 256, torch.bfloat16, True, False, False, False, False, True),
+    (65, 3, 264, torch.bfloat16, False, True, False, True, True, False),
+    (9, 1, 1024, torch.float32, True, True, False, True, True, True),
+    (5, 2, 776, torch.bfloat16, True, False, True, True, True, True),
+    (5001, 7, 40, torch.bfloat16, True, True, True, True, True, True),
+    (130, 33, 8, torch.float32, True, True, False, False, True, False),
+]
+
+
+def make(M, G, d, dtype, gate, shared, weight, bias, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rnd(*s):
+        return torch.randn(s, generator=g, device="cuda")
+
+    ws = (d,) if shared else (G, d)
+    return ((0.3 * rnd(M, G, d) + 0.2).to(dtype), 1 + 0.2 * rnd(*ws) if weight else None,
+            0.2 * rnd(*ws) if bias else None, rnd(M, G, d).bfloat16() if gate else None, rnd(M, G, d).bfloat16())
+
+
+@pytest.mark.parametrize("M,G,d,dtype,gate,center,shared,weight,bias,act", CASES)
+def test_forward_and_gradients(M, G, d, dtype, gate, center, shared, weight, bias, act):
+    x, w, b, z, dy = make(M, G, d, dtype, gate, shared, weight, bias, 1 + d)
+    y = gla.group_norm_silu(x, w, b, z, center=center, act=act)
+    got = gla.group_norm_silu_bwd(x, dy, w, b, z, center=center, act=act)
+    leaves = [t.double().requires_grad_(True) if t is not None else None for t in (x, z, w, b)]
+    ref = norm(leaves[0], leaves[2], leaves[3], leaves[1], center, act, 1e-5)
+    assert y.dtype == torch.bfloat16 and rel(y, ref) <= U
+    want = iter(torch.autograd.grad(ref, [t for t in leaves if t is not None], dy.double()))
+    for n, t, g in zip(("dx", "dgate", "dweight", "dbias"), leaves, got):
+        assert (t is None) == (g is None)
+        if t is None:
+            continue
+        r = next(want)
+        tol = 1e-5 if g.dtype == torch.float32 else U
+        if n == "dx" and d == 8:
+            tol *= 4            # centred groups of eight: dx is a difference of terms a few times its size
+        assert rel(g, r) <= tol, (n, rel(g, r))
+    again = gla.group_norm_silu_bwd(x, dy, w, b, z, center=center, act=act)
+    for p, q in zip(got, again):
+        assert p is None or torch.equal(p, q)
+
+
+def test_rows_that_are_constant_or_zero():
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    x[1:3] = 3.0
+    y = gla.group_norm_silu(x, act=False)
+    assert bool((y == 0).all())
+    dx, _, _, _ = gla.group_norm_silu_bwd(x, torch.ones_like(x), act=False)
+    assert bool(torch.isfinite(dx).all())
+
+
+def test_no_rows():
+    x = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(4, 64, device="cuda")
+    assert gla.group_norm_silu(x, w).shape == x.shape
+    assert bool((gla.group_norm_silu_bwd(x, x, w)[2] == 0).all())
+
+
+def test_slices_other_stream_and_graph():
+    x, w, b, z, dy = make(50, 4, 96, torch.bfloat16, True, False, True, True, 3)
+    buf = torch.full((50, 3 * 4 * 96 + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    buf[:, 384:768], buf[:, 768:1152] = x.flatten(1), z.flatten(1)
+    xs, zs = buf[:, 384:768].unflatten(-1, (4, 96)), buf[:, 768:1152].unflatten(-1, (4, 96))
+    want = (gla.group_norm_silu(x, w, b, z),) + gla.group_norm_silu_bwd(x, dy, w, b, z)
+    got = (gla.group_norm_silu(xs, w, b, zs),) + gla.group_norm_silu_bwd(xs, dy, w, b, zs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rep = (gla.group_norm_silu(x, w, b, z),) + gla.group_norm_silu_bwd(x, dy, w, b, z)
+    graph.replay()
+    torch.cuda.synchronize()
+    for p, q, r in zip(want, got, rep):
+        assert torch.equal(p, q) and torch.equal(p, r)
+
+
+def test_gradients_against_differences():
+    """fp32 x, identity activation: the loss <n, c> along random directions.
+    Central differences with a step of 2^-6 of x's size leave third-order terms
+    (2^-12) and fp32 roundings of y... y is bf16, so the loss is taken from the
+    formula in 64 bits and only the gradient from the kernel."""
+    x, w, b, z, dy = make(20, 3, 64, torch.float32, True, False, True, True, 5)
+    got = gla.group_norm_silu_bwd(x, dy, w, b, z)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    h = 2.0 ** -12
+    for i, grad in ((0, got[0]), (3, got[1]), (1, got[2]), (2, got[3])):
+        ins = [t.double() for t in (x, w, b, z)]
+        v = torch.randn(ins[i].shape, generator=g, device="cuda").double()
+        side = []
+        for s in (1, -1):
+            e = list(ins)
+            e[i] = ins[i] + s * h * v
+            side.append(float((norm(e[0], e[1], e[2], e[3], True, True, 1e-5) * dy.double()).sum()))
+        diff, want = (side[0] - side[1]) / (2 * h), float((grad.double() * v).sum())
+        assert abs(diff - want) <= 2 * U * float((grad.double() * v).norm()), (i, diff, want)
