@@ -129,6 +129,9 @@ __device__ __forceinline__ void state_store_bf16(const float (&S)[DK / 8][4], __
     }
 }
 
+// Products are issued term by term over all tiles, so that a tile's next
+// product comes after those of its neighbours and finds the last one done.
+
 // acc[token tile] += state . X^T for X = K or Q in shared memory ([token][dk]).
 template <int DK, int NT>
 __device__ __forceinline__ void state_times(float (&acc)[8][4], const float (&S)[DK / 8][4], uint32_t xs)
@@ -137,13 +140,16 @@ __device__ __forceinline__ void state_times(float (&acc)[8][4], const float (&S)
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
         const Split<NT> a = split_tiles<NT>(S[2 * s], S[2 * s + 1]);
+        uint32_t b[4][4];
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-            uint32_t b[4];
-            ldsm4(b, xs + np * 16 * KS * 2 + s * 32);
-            mma_split<NT>(acc[2 * np], a, b[0], b[1]);
-            mma_split<NT>(acc[2 * np + 1], a, b[2], b[3]);
-        }
+        for (int np = 0; np < 4; ++np) ldsm4(b[np], xs + np * 16 * KS * 2 + s * 32);
+#pragma unroll
+        for (int n = NT - 1; n >= 0; --n)
+#pragma unroll
+            for (int np = 0; np < 4; ++np) {
+                mma_bf16(acc[2 * np], a.t[n], b[np][0], b[np][1]);
+                mma_bf16(acc[2 * np + 1], a.t[n], b[np][2], b[np][3]);
+            }
     }
 }
 
@@ -151,13 +157,64 @@ __device__ __forceinline__ void state_times(float (&acc)[8][4], const float (&S)
 template <int DK, int NT>
 __device__ __forceinline__ void state_add(float (&S)[DK / 8][4], const Split<NT>& a, uint32_t xk, int s)
 {
-    constexpr int KS = DK + kGdPad;
+    constexpr int KS = DK + kGdPad, NP = DK / 16, GR = NP % 3 == 0 ? 3 : 4;
 #pragma unroll
-    for (int np = 0; np < DK / 16; ++np) {
-        uint32_t b[4];
-        ldsm4_t(b, xk + s * 16 * KS * 2 + np * 32);
-        mma_split<NT>(S[2 * np], a, b[0], b[1]);
-        mma_split<NT>(S[2 * np + 1], a, b[2], b[3]);
+    for (int g = 0; g < NP; g += GR) {
+        uint32_t b[GR][4];
+#pragma unroll
+        for (int i = 0; i < GR; ++i) ldsm4_t(b[i], xk + s * 16 * KS * 2 + (g + i) * 32);
+#pragma unroll
+        for (int n = NT - 1; n >= 0; --n)
+#pragma unroll
+            for (int i = 0; i < GR; ++i) {
+                mma_bf16(S[2 * (g + i)], a.t[n], b[i][0], b[i][1]);
+                mma_bf16(S[2 * (g + i) + 1], a.t[n], b[i][2], b[i][3]);
+            }
+    }
+}
+
+// acc[tiles 2 np, 2 np + 1] += A . B for the pairs np = N0 .. N1 - 1, B a tile
+// of two terms (hi, lo) in shared memory: A hi x B lo, then each term of A x B hi.
+template <int N0, int N1, int NT, bool TRANS>
+__device__ __forceinline__ void pairs_add(float (&acc)[8][4], const Split<NT>& a, uint32_t hi, uint32_t lo, int step,
+                                          bool with_lo)
+{
+    uint32_t b[4][4];
+    if (with_lo) {
+#pragma unroll
+        for (int np = N0; np < N1; ++np) {
+            if (TRANS) ldsm4_t(b[np], lo + np * step);
+            else ldsm4(b[np], lo + np * step);
+        }
+#pragma unroll
+        for (int np = N0; np < N1; ++np) {
+            mma_bf16(acc[2 * np], a.t[0], b[np][0], b[np][1]);
+            mma_bf16(acc[2 * np + 1], a.t[0], b[np][2], b[np][3]);
+        }
+    }
+#pragma unroll
+    for (int np = N0; np < N1; ++np) {
+        if (TRANS) ldsm4_t(b[np], hi + np * step);
+        else ldsm4(b[np], hi + np * step);
+    }
+#pragma unroll
+    for (int n = NT - 1; n >= 0; --n)
+#pragma unroll
+        for (int np = N0; np < N1; ++np) {
+            mma_bf16(acc[2 * np], a.t[n], b[np][0], b[np][1]);
+            mma_bf16(acc[2 * np + 1], a.t[n], b[np][2], b[np][3]);
+        }
+}
+// The same for step s of a triangular tile: UP: pairs s .. 3, else 0 .. s.
+template <bool UP, int NT, bool TRANS>
+__device__ __forceinline__ void tri_add(float (&acc)[8][4], const Split<NT>& a, uint32_t hi, uint32_t lo, int step, int s,
+                                        bool with_lo)
+{
+    switch (s) {          // s is a constant wherever this is called
+    case 0: pairs_add<0, UP ? 4 : 1, NT, TRANS>(acc, a, hi, lo, step, with_lo); break;
+    case 1: pairs_add<UP ? 1 : 0, UP ? 4 : 2, NT, TRANS>(acc, a, hi, lo, step, with_lo); break;
+    case 2: pairs_add<UP ? 2 : 0, UP ? 4 : 3, NT, TRANS>(acc, a, hi, lo, step, with_lo); break;
+    default: pairs_add<UP ? 3 : 0, 4, NT, TRANS>(acc, a, hi, lo, step, with_lo); break;
     }
 }
 
@@ -270,17 +327,7 @@ __global__ void __launch_bounds__(max_warps<DK>() * 32, 1) gd_sweep_fwd_kernel(G
             }
         }
 #pragma unroll
-        for (int np = 0; np < 4; ++np)
-#pragma unroll
-            for (int s = 0; s <= np; ++s) {
-                uint32_t hi[4], lo[4];
-                ldsm4(hi, tn + np * tstep + s * 32);
-                ldsm4(lo, tn + tile + np * tstep + s * 32);
-                mma_bf16(y[2 * np], r[s].t[0], lo[0], lo[1]);
-                mma_bf16(y[2 * np + 1], r[s].t[0], lo[2], lo[3]);
-                mma_split<2>(y[2 * np], r[s], hi[0], hi[1]);
-                mma_split<2>(y[2 * np + 1], r[s], hi[2], hi[3]);
-            }
+        for (int s = 0; s < 4; ++s) tri_add<true, 2, false>(y, r[s], tn + s * 32, tn + tile + s * 32, tstep, s, true);
         if (BWD) {
             float* yn = p.yn + (u * wtot + wt) * (kGdC * 16) + lane * 4;
 #pragma unroll
@@ -322,18 +369,7 @@ __global__ void __launch_bounds__(max_warps<DK>() * 32, 1) gd_sweep_fwd_kernel(G
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const Split<BWD ? 3 : 1> a = split_tiles<BWD ? 3 : 1>(y[2 * s], y[2 * s + 1]);
-#pragma unroll
-            for (int np = s; np < 4; ++np) {
-                uint32_t b[4];
-                if (BWD) {
-                    ldsm4(b, pn + tile + np * tstep + s * 32);
-                    mma_bf16(o[2 * np], a.t[0], b[0], b[1]);
-                    mma_bf16(o[2 * np + 1], a.t[0], b[2], b[3]);
-                }
-                ldsm4(b, pn + np * tstep + s * 32);
-                mma_split(o[2 * np], a, b[0], b[1]);
-                mma_split(o[2 * np + 1], a, b[2], b[3]);
-            }
+            tri_add<true, BWD ? 3 : 1, false>(o, a, pn + s * 32, pn + tile + s * 32, tstep, s, BWD);
         }
         if (BWD) {
             // sum over dv of (o without its own token's part) . dO
@@ -485,18 +521,9 @@ __global__ void __launch_bounds__(max_warps<DK>() * 32, 1) gd_sweep_rev_kernel(G
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            uint32_t d[4];
-            ldsm4_t(d, da + s * vstep);
-#pragma unroll
-            for (int np = 0; np <= s; ++np) {
-                uint32_t hi[4], lo[4];
-                ldsm4_t(hi, pt + s * tstep + np * 32);
-                ldsm4_t(lo, pt + tile + s * tstep + np * 32);
-                mma_bf16(y[2 * np], d, lo[0], lo[1]);
-                mma_bf16(y[2 * np + 1], d, lo[2], lo[3]);
-                mma_bf16(y[2 * np], d, hi[0], hi[1]);
-                mma_bf16(y[2 * np + 1], d, hi[2], hi[3]);
-            }
+            Split<1> d;
+            ldsm4_t(d.t[0], da + s * vstep);
+            tri_add<false, 1, true>(y, d, pt + s * tstep, pt + tile + s * tstep, 32, s, true);
         }
         // y: beta dVs'; r: -beta dV' (T is kept as -(T - I)); then dvs = y + (T - I)^T (beta dV')
         Split<2> r[4];
@@ -522,17 +549,8 @@ __global__ void __launch_bounds__(max_warps<DK>() * 32, 1) gd_sweep_rev_kernel(G
             }
         }
 #pragma unroll
-        for (int np = 0; np < 4; ++np)
-#pragma unroll
-            for (int s = np; s < 4; ++s) {
-                uint32_t hi[4], lo[4];
-                ldsm4_t(hi, tt + s * tstep + np * 32);
-                ldsm4_t(lo, tt + tile + s * tstep + np * 32);
-                mma_bf16(y[2 * np], r[s].t[0], lo[0], lo[1]);
-                mma_bf16(y[2 * np + 1], r[s].t[0], lo[2], lo[3]);
-                mma_split<2>(y[2 * np], r[s], hi[0], hi[1]);
-                mma_split<2>(y[2 * np + 1], r[s], hi[2], hi[3]);
-            }
+        for (int s = 0; s < 4; ++s)
+            tri_add<false, 2, true>(y, r[s], tt + s * tstep, tt + tile + s * tstep, 32, s, true);
         // the sums; y becomes dv
         {
             const float* yn = p.yn + (u * wtot + wt) * (kGdC * 16) + lane * 4;

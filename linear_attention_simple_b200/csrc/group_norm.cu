@@ -9,13 +9,16 @@
 //   dx = rstd (g - x^ <g x^> - <g>),  <.> the mean over the group (<g> only
 //   when centred);  dweight = sum dn x^, dbias = sum dn over the rows.
 //
-// Pure streams: a few flops per byte, HBM bandwidth bounds them.  A group is
-// held by 1 to 32 lanes of a warp, 8 channels (16 bytes of bf16) a lane and
-// step, so its sums are a few shuffles and every row is read once.  A lane
-// keeps its channels for all rows it walks, so weight and bias are read once
-// a thread, and the backward's sums over rows stay in registers until one
-// partial row per walker goes to the workspace; a second kernel adds those in
-// a fixed order.
+// Pure streams: HBM bandwidth bounds them as long as enough loads are in
+// flight.  A group is held by `lanes` lanes of a warp (a power of two) with NV
+// vectors of 8 channels each, lanes x NV as close to d / 8 as it gets, so its
+// sums are a few shuffles, every row is read once and no lane idles (d = 192:
+// 8 lanes of 3 vectors).  The forward walks neighbouring groups of a row with
+// neighbouring lanes and loads its next row while it works on this one.  In
+// the backward a CTA stays with one group: weight and bias sit in shared
+// memory, the sums over rows in registers until they are added up within the
+// CTA, and one partial row per CTA goes to the workspace; a second kernel adds
+// those in a fixed order.
 #include <cuda_bf16.h>
 
 #include "gla_device.cuh"
@@ -24,7 +27,7 @@ namespace gla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxWalkers = 296;           // partial rows of the backward
+constexpr int kSms = 148;
 
 struct NormParams {
     const void* x;
@@ -33,28 +36,45 @@ struct NormParams {
     __nv_bfloat16* y;
     void* dx;
     __nv_bfloat16* dgate;
-    float* part;                           // [walkers][2][G d]
+    float* part;                           // [CTAs of a group][2][G d]
     int64_t ld_x, ld_gate;
     int M, G, d, shared_w, center, act, walkers;
     float eps;
 };
 
-__device__ __forceinline__ void load8(float (&f)[8], const __nv_bfloat16* p)
-{
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+// Eight channels as they lie in memory.
+template <class T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(a[i]);
-        f[2 * i + 1] = bf16_hi(a[i]);
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16_lo(w[i]);
+            f[2 * i + 1] = bf16_hi(w[i]);
+        }
     }
-}
-__device__ __forceinline__ void load8(float (&f)[8], const float* p)
-{
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
+};
+template <>
+struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8])
 {
     *reinterpret_cast<uint4*>(p) =
@@ -70,53 +90,35 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes)
     for (int o = lanes >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + expf(-z)); }
+// The fast exponential and quotient are good to a few 2^-22 here, far below
+// the bf16 rounding of y and the fp32 sums; 1 + e^-z past 2^126 gives 0.
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
-// The lanes of one group and the rows they walk.  NV: steps of 8 channels a lane.
-struct Walk {
-    int lane, g, walker, lanes;
-    bool on;                               // whether this thread has a group
-    __device__ __forceinline__ Walk(const NormParams& p, int lanes_)
-    {
-        lanes = lanes_;
-        const int64_t seat = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / lanes;
-        lane = threadIdx.x & (lanes - 1);
-        g = static_cast<int>(seat % p.G);
-        walker = static_cast<int>(seat / p.G);
-        on = walker < p.walkers;
-    }
-};
-
-// x^ of this lane's channels (zeros behind d) and rstd of the group.
-template <int NV, class T>
-__device__ __forceinline__ float normalise(float (&x)[NV][8], const T* px, bool on, const Walk& k, const NormParams& p)
+// x^ in place of x (zeros behind d), and rstd of the group.
+template <int NV>
+__device__ __forceinline__ float normalise(float (&x)[NV][8], int lane, int lanes, const NormParams& p)
 {
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * k.lanes + k.lane) * 8;
-        if (on && c < p.d) {
-            load8(x[j], px + c);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[j][e] = 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += x[j][e];
-    }
     const float inv = 1.f / static_cast<float>(p.d);
-    const float mean = p.center ? lanes_sum(sum, k.lanes) * inv : 0.f;
+    if (p.center) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += x[j][e];
+        const float mean = lanes_sum(sum, lanes) * inv;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const float m = (j * lanes + lane) * 8 < p.d ? mean : 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[j][e] -= m;
+        }
+    }
     float sq = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const bool in = (j * k.lanes + k.lane) * 8 < p.d;
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[j][e] = in ? x[j][e] - mean : 0.f;
-            sq = fmaf(x[j][e], x[j][e], sq);
-        }
-    }
-    const float rstd = rsqrtf(lanes_sum(sq, k.lanes) * inv + p.eps);
+        for (int e = 0; e < 8; ++e) sq = fmaf(x[j][e], x[j][e], sq);
+    const float rstd = rsqrtf(lanes_sum(sq, lanes) * inv + p.eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -124,98 +126,134 @@ __device__ __forceinline__ float normalise(float (&x)[NV][8], const T* px, bool 
     return rstd;
 }
 
-template <int NV>
-__device__ __forceinline__ void load_params(float (&w)[NV][8], float (&b)[NV][8], const Walk& k, const NormParams& p)
-{
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * k.lanes + k.lane) * 8;
-        const int at = (p.shared_w ? 0 : k.g * p.d) + c;
-        const bool in = k.on && c < p.d;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[j][e] = 1.f;
-            b[j][e] = 0.f;
-        }
-        if (in && p.weight) load8(w[j], p.weight + at);
-        if (in && p.bias) load8(b[j], p.bias + at);
-    }
-}
-
-template <int NV, class T>
+template <int NV, class T, bool GATE>
 __global__ void __launch_bounds__(kThreads) group_norm_silu_kernel(NormParams p, int lanes)
 {
-    const Walk k(p, lanes);
+    const int64_t seat = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / lanes;
+    const int lane = threadIdx.x & (lanes - 1), g = static_cast<int>(seat % p.G);
+    const int64_t walker = seat / p.G;
+    const int c0 = lane * 8, cstep = lanes * 8;
     float w[NV][8], b[NV][8];
-    load_params<NV>(w, b, k, p);
-    const T* x = static_cast<const T*>(p.x);
-    // every lane of a warp makes the same number of steps: the sums are shuffles
-    for (int64_t r0 = 0; r0 < p.M; r0 += p.walkers) {
-        const int64_t r = r0 + k.walker;
-        const bool on = k.on && r < p.M;
-        float f[NV][8], z[NV][8];
-        if (p.gate) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * lanes + k.lane) * 8;
-                if (on && c < p.d) load8(z[j], p.gate + r * p.ld_gate + k.g * p.d + c);
-            }
+    for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * cstep, at = (p.shared_w ? 0 : g * p.d) + c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[j][e] = p.weight && c < p.d ? p.weight[at + e] : 1.f;
+            b[j][e] = p.bias && c < p.d ? p.bias[at + e] : 0.f;
         }
-        normalise<NV>(f, x + r * p.ld_x + k.g * p.d, on, k, p);
+    }
+    const T* px = static_cast<const T*>(p.x) + g * p.d + c0;
+    const __nv_bfloat16* pg = p.gate + g * p.d + c0;
+    Raw<T> rx[NV];
+    Raw<__nv_bfloat16> rz[NV];
+    auto fetch = [&](int64_t r) {
+        const bool on = walker < p.walkers && r < p.M;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * lanes + k.lane) * 8;
+            rx[j].zero();
+            if (GATE) rz[j].zero();
+            if (on && c0 + j * cstep < p.d) {
+                rx[j].load(px + r * p.ld_x + j * cstep);
+                if (GATE) rz[j].load(pg + r * p.ld_gate + j * cstep);
+            }
+        }
+    };
+    fetch(walker);
+    // every lane of a warp makes the same number of steps: the sums are shuffles
+    for (int64_t r0 = 0; r0 < p.M; r0 += p.walkers) {
+        const int64_t r = r0 + walker;
+        const bool on = walker < p.walkers && r < p.M;
+        float f[NV][8], z[NV][8];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            rx[j].get(f[j]);
+            if (GATE) rz[j].get(z[j]);
+        }
+        if (r0 + p.walkers < p.M) fetch(r + p.walkers);
+        normalise<NV>(f, lane, lanes, p);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = c0 + j * cstep;
             if (!on || c >= p.d) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float n = fmaf(f[j][e], w[j][e], b[j][e]);
-                const float a = p.gate ? z[j][e] : n;
+                const float a = GATE ? z[j][e] : n;
                 const float s = p.act ? a * sigmoid_f(a) : a;
-                f[j][e] = p.gate ? n * s : s;
+                f[j][e] = GATE ? n * s : s;
             }
-            store8(p.y + (r * p.G + k.g) * p.d + c, f[j]);
+            store8(p.y + (r * p.G + g) * p.d + c, f[j]);
         }
     }
 }
 
-template <int NV, class T>
-__global__ void __launch_bounds__(kThreads) group_norm_silu_bwd_kernel(NormParams p, int lanes)
+template <int NV, class T, bool GATE>
+__global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : 2) group_norm_silu_bwd_kernel(NormParams p, int lanes)
 {
-    const Walk k(p, lanes);
-    float w[NV][8], b[NV][8], sw[NV][8], sb[NV][8];
-    load_params<NV>(w, b, k, p);
+    extern __shared__ __align__(16) float smem[];          // weight, bias [2][d]; later the warps' sums [8][2][d]
+    const int lane = threadIdx.x & (lanes - 1), g = blockIdx.x % p.G;
+    const int64_t walker = static_cast<int64_t>(blockIdx.x / p.G) * (kThreads / lanes) + threadIdx.x / lanes;
+    const int c0 = lane * 8, cstep = lanes * 8;
+    for (int i = threadIdx.x; i < p.d; i += kThreads) {
+        const int at = (p.shared_w ? 0 : g * p.d) + i;
+        smem[i] = p.weight ? p.weight[at] : 1.f;
+        smem[p.d + i] = p.bias ? p.bias[at] : 0.f;
+    }
+    __syncthreads();
+    float sw[NV][8], sb[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sw[j][e] = sb[j][e] = 0.f;
-    const T* x = static_cast<const T*>(p.x);
+    const T* px = static_cast<const T*>(p.x) + g * p.d + c0;
+    const __nv_bfloat16* pg = p.gate + g * p.d + c0;
     const float inv = 1.f / static_cast<float>(p.d);
+    Raw<T> rx[NV];
+    Raw<__nv_bfloat16> rz[NV], rd[NV];
+    auto fetch = [&](int64_t r) {
+        const bool on = r < p.M;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            rx[j].zero();
+            rd[j].zero();
+            if (GATE) rz[j].zero();
+            if (on && c0 + j * cstep < p.d) {
+                rx[j].load(px + r * p.ld_x + j * cstep);
+                rd[j].load(p.dy + (r * p.G + g) * p.d + c0 + j * cstep);
+                if (GATE) rz[j].load(pg + r * p.ld_gate + j * cstep);
+            }
+        }
+    };
+    fetch(walker);
     for (int64_t r0 = 0; r0 < p.M; r0 += p.walkers) {
-        const int64_t r = r0 + k.walker;
-        const bool on = k.on && r < p.M;
-        const int64_t at = (r * p.G + k.g) * p.d;
+        const int64_t r = r0 + walker;
+        const bool on = r < p.M;
+        const int64_t at = (r * p.G + g) * p.d;
         float f[NV][8], z[NV][8], dn[NV][8];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * lanes + k.lane) * 8;
-            if (on && c < p.d) {
-                load8(dn[j], p.dy + at + c);
-                if (p.gate) load8(z[j], p.gate + r * p.ld_gate + k.g * p.d + c);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) dn[j][e] = z[j][e] = 0.f;
-            }
+            rx[j].get(f[j]);
+            rd[j].get(dn[j]);
+            if (GATE) rz[j].get(z[j]);
         }
-        const float rstd = normalise<NV>(f, x + r * p.ld_x + k.g * p.d, on, k, p);
+        if (r0 + p.walkers < p.M) fetch(r + p.walkers);
+        const float rstd = normalise<NV>(f, lane, lanes, p);
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * lanes + k.lane) * 8;
-            const bool in = on && c < p.d;
+            const int c = c0 + j * cstep;
+            if (c >= p.d) continue;
+            float w[8], b[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                *reinterpret_cast<float4*>(w + e) = *reinterpret_cast<const float4*>(smem + c + e);
+                *reinterpret_cast<float4*>(b + e) = *reinterpret_cast<const float4*>(smem + p.d + c + e);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float n = fmaf(f[j][e], w[j][e], b[j][e]);
-                const float a = p.gate ? z[j][e] : n;
+                const float n = fmaf(f[j][e], w[e], b[e]);
+                const float a = GATE ? z[j][e] : n;
                 float val = a, slope = 1.f;
                 if (p.act) {
                     const float sg = sigmoid_f(a);
@@ -223,43 +261,61 @@ __global__ void __launch_bounds__(kThreads) group_norm_silu_bwd_kernel(NormParam
                     slope = sg * fmaf(a, 1.f - sg, 1.f);
                 }
                 const float dy = dn[j][e];
-                dn[j][e] = dy * (p.gate ? val : slope);
+                dn[j][e] = dy * (GATE ? val : slope);
                 z[j][e] = dy * n * slope;
                 sw[j][e] = fmaf(dn[j][e], f[j][e], sw[j][e]);
                 sb[j][e] += dn[j][e];
-                dn[j][e] *= w[j][e];
+                dn[j][e] *= w[e];
                 s1 += dn[j][e];
                 s2 = fmaf(dn[j][e], f[j][e], s2);
             }
-            if (in && p.gate) store8(p.dgate + at + c, z[j]);
+            if (GATE && on) store8(p.dgate + at + c, z[j]);
         }
         s1 = p.center ? lanes_sum(s1, lanes) * inv : 0.f;
         s2 = lanes_sum(s2, lanes) * inv;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * lanes + k.lane) * 8;
+            const int c = c0 + j * cstep;
             if (!on || c >= p.d) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[j][e] = rstd * (dn[j][e] - fmaf(f[j][e], s2, s1));
             store8(static_cast<T*>(p.dx) + at + c, f[j]);
         }
     }
-    if (p.part && k.on) {
-        float* part = p.part + static_cast<int64_t>(k.walker) * 2 * p.G * p.d + k.g * p.d;
+    if (!p.part) return;
+    // the seats of a warp, then the warps, in a fixed order
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            for (int o = lanes; o < 32; o <<= 1) {
+                sw[j][e] += __shfl_xor_sync(0xFFFFFFFFu, sw[j][e], o);
+                sb[j][e] += __shfl_xor_sync(0xFFFFFFFFu, sb[j][e], o);
+            }
+    __syncthreads();
+    float* mine = smem + (threadIdx.x >> 5) * 2 * p.d;
+    if ((threadIdx.x & 31) < lanes) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * lanes + k.lane) * 8;
+            const int c = c0 + j * cstep;
             if (c >= p.d) continue;
-            store8(part + c, sw[j]);
-            store8(part + p.G * p.d + c, sb[j]);
+            store8(mine + c, sw[j]);
+            store8(mine + p.d + c, sb[j]);
         }
+    }
+    __syncthreads();
+    float* part = p.part + static_cast<int64_t>(blockIdx.x / p.G) * 2 * p.G * p.d + g * p.d;
+    for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
+        float v = 0.f;
+        for (int k = 0; k < kThreads / 32; ++k) v += smem[k * 2 * p.d + i];
+        part[i < p.d ? i : p.G * p.d + i - p.d] = v;
     }
 }
 
 // dweight, dbias [C]: the partial rows, and with a shared weight the groups,
 // added in a fixed order.  32 channels a CTA, 8 threads a channel.
 __global__ void __launch_bounds__(256) group_norm_reduce_kernel(const float* __restrict__ part, float* __restrict__ dw,
-                                                                float* __restrict__ db, int walkers, int G, int d,
+                                                                float* __restrict__ db, int rows, int G, int d,
                                                                 int shared_w)
 {
     __shared__ float s[2][8][32];
@@ -268,12 +324,12 @@ __global__ void __launch_bounds__(256) group_norm_reduce_kernel(const float* __r
     const int groups = shared_w ? G : 1;
     float w = 0.f, b = 0.f;
     if (ch < C) {
-        for (int r = k; r < walkers; r += 8)
-            for (int g = 0; g < groups; ++g) {
-                const float* p = part + static_cast<int64_t>(r) * 2 * G * d + g * d + ch;
-                w += p[0];
-                b += p[static_cast<int64_t>(G) * d];
-            }
+        for (int i = k; i < rows * groups; i += 8) {
+            const int r = i / groups, g = i - r * groups;
+            const float* p = part + static_cast<int64_t>(r) * 2 * G * d + g * d + ch;
+            w += p[0];
+            b += p[static_cast<int64_t>(G) * d];
+        }
     }
     s[0][k][c] = w;
     s[1][k][c] = b;
@@ -288,49 +344,91 @@ __global__ void __launch_bounds__(256) group_norm_reduce_kernel(const float* __r
     }
 }
 
-// Lanes of a group: as few as hold d channels at 8 a lane, at most a warp.
-int lanes_for(int d)
+// Lanes of a group and vectors of a lane: the least idle of 1 to 4 vectors,
+// of equals two (loads in flight) before one (lanes).
+void shape_for(int d, int* lanes, int* nv)
 {
-    int l = 1;
-    while (l < 32 && l * 8 < d) l *= 2;
-    return l;
+    const int v = d / 8;
+    int best = 1 << 30;
+    const int order[4] = {2, 1, 3, 4};
+    for (int n : order) {
+        int l = 1;
+        while (l < 32 && l * n < v) l *= 2;
+        if (l * n >= v && l * n < best) {
+            best = l * n;
+            *lanes = l;
+            *nv = n;
+        }
+    }
 }
 
-// Rows are dealt to `walkers` seats per group; at most four CTAs' worth a SM.
-int walkers_for(int M, int G, int d, bool bwd)
+// The backward's CTAs of a group: about four a SM over all groups, no more
+// than the rows need.
+int ctas_of_group(int M, int G, int d)
 {
-    const int64_t seats = static_cast<int64_t>(148) * (bwd ? 4 : 8) * kThreads / lanes_for(d);
-    int64_t w = seats / G;
-    if (w < 1) w = 1;
-    if (bwd && w > kMaxWalkers) w = kMaxWalkers;
-    return static_cast<int>(w < M ? w : (M > 0 ? M : 1));
+    int lanes, nv;
+    shape_for(d, &lanes, &nv);
+    const int seats = kThreads / lanes;
+    const int want = (4 * kSms + G - 1) / G, need = (M + seats - 1) / seats;
+    return want < need ? want : (need > 0 ? need : 1);
 }
 
-template <class T, bool BWD>
-gla_status run(const NormParams& p, cudaStream_t st)
+template <class T, bool BWD, bool GATE, int NV>
+gla_status start(const NormParams& p, int lanes, int blocks, cudaStream_t st)
 {
-    const int lanes = lanes_for(p.d);
-    const int64_t blocks = (static_cast<int64_t>(p.walkers) * p.G * lanes + kThreads - 1) / kThreads;
-    const dim3 grid(static_cast<unsigned>(blocks));
-    const int nv = (p.d + lanes * 8 - 1) / (lanes * 8);
     trace_begin(st);
-#define GLA_NORM(NV) \
-    if (BWD) group_norm_silu_bwd_kernel<NV, T><<<grid, kThreads, 0, st>>>(p, lanes); \
-    else group_norm_silu_kernel<NV, T><<<grid, kThreads, 0, st>>>(p, lanes)
-    if (nv == 1) { GLA_NORM(1); }
-    else if (nv == 2) { GLA_NORM(2); }
-    else { GLA_NORM(4); }
-#undef GLA_NORM
+    if (BWD) {
+        const int smem = (kThreads / 32) * 2 * p.d * 4;      // 64 KB at most
+        cudaError_t e = cudaSuccess;
+        if (smem > 48 * 1024)
+            e = cudaFuncSetAttribute(group_norm_silu_bwd_kernel<NV, T, GATE>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return status_of(e);
+        group_norm_silu_bwd_kernel<NV, T, GATE><<<blocks, kThreads, smem, st>>>(p, lanes);
+    } else {
+        group_norm_silu_kernel<NV, T, GATE><<<blocks, kThreads, 0, st>>>(p, lanes);
+    }
     trace_end(st, BWD ? "group_norm_silu_bwd_kernel" : "group_norm_silu_kernel");
     count_launch();
     return check_launch("group_norm_silu_kernel");
+}
+
+template <class T, bool BWD, bool GATE>
+gla_status run(const NormParams& q, cudaStream_t st)
+{
+    NormParams p = q;
+    int lanes = 32, nv = 4;
+    shape_for(p.d, &lanes, &nv);
+    int64_t blocks;
+    if (BWD) {
+        const int per = ctas_of_group(p.M, p.G, p.d);
+        p.walkers = per * (kThreads / lanes);
+        blocks = static_cast<int64_t>(per) * p.G;
+    } else {
+        const int64_t w = static_cast<int64_t>(kSms) * 8 * kThreads / lanes / p.G;
+        p.walkers = static_cast<int>(w < 1 ? 1 : (w < p.M ? w : p.M));
+        blocks = (static_cast<int64_t>(p.walkers) * p.G * lanes + kThreads - 1) / kThreads;
+    }
+    switch (nv) {
+    case 1: return start<T, BWD, GATE, 1>(p, lanes, static_cast<int>(blocks), st);
+    case 2: return start<T, BWD, GATE, 2>(p, lanes, static_cast<int>(blocks), st);
+    case 3: return start<T, BWD, GATE, 3>(p, lanes, static_cast<int>(blocks), st);
+    default: return start<T, BWD, GATE, 4>(p, lanes, static_cast<int>(blocks), st);
+    }
+}
+
+template <bool BWD>
+gla_status run_any(const NormParams& p, bool f32, cudaStream_t st)
+{
+    if (f32) return p.gate ? run<float, BWD, true>(p, st) : run<float, BWD, false>(p, st);
+    return p.gate ? run<__nv_bfloat16, BWD, true>(p, st) : run<__nv_bfloat16, BWD, false>(p, st);
 }
 
 }  // namespace
 
 size_t group_norm_bwd_workspace_bytes(int M, int G, int d)
 {
-    return static_cast<size_t>(walkers_for(M, G, d, true)) * 2 * G * d * 4;
+    return static_cast<size_t>(ctas_of_group(M, G, d)) * 2 * G * d * 4;
 }
 
 gla_status launch_group_norm(const void* x, bool f32, const void* gate, const float* weight, const float* bias, void* y,
@@ -352,8 +450,7 @@ gla_status launch_group_norm(const void* x, bool f32, const void* gate, const fl
     p.center = center;
     p.act = act;
     p.eps = eps;
-    p.walkers = walkers_for(M, G, d, false);
-    return f32 ? run<float, false>(p, st) : run<__nv_bfloat16, false>(p, st);
+    return run_any<false>(p, f32, st);
 }
 
 gla_status launch_group_norm_bwd(const void* x, bool f32, const void* gate, const float* weight, const float* bias,
@@ -379,15 +476,14 @@ gla_status launch_group_norm_bwd(const void* x, bool f32, const void* gate, cons
     p.center = center;
     p.act = act;
     p.eps = eps;
-    p.walkers = walkers_for(M, G, d, true);
     if (M > 0) {
-        const gla_status s = f32 ? run<float, true>(p, st) : run<__nv_bfloat16, true>(p, st);
+        const gla_status s = run_any<true>(p, f32, st);
         if (s != GLA_OK || !p.part) return s;
     }
     if (!dweight && !dbias) return GLA_OK;
     const int C = shared_w ? d : G * d;
     trace_begin(st);
-    group_norm_reduce_kernel<<<(C + 31) / 32, 256, 0, st>>>(ws, dweight, dbias, M > 0 ? p.walkers : 0, G, d, shared_w);
+    group_norm_reduce_kernel<<<(C + 31) / 32, 256, 0, st>>>(ws, dweight, dbias, M > 0 ? ctas_of_group(M, G, d) : 0, G, d, shared_w);
     trace_end(st, "group_norm_reduce_kernel");
     count_launch();
     return check_launch("group_norm_reduce_kernel");
