@@ -59,6 +59,49 @@ struct GdSeqs {
     }
 };
 
+// What the all-chunks kernel leaves of a (chunk, value head) for the sweeps:
+// one record, copied to shared memory as it is, its tiles in the layouts that
+// the tensor core reads: K and scale G Q as blocks of [64 tokens][32] (64-byte
+// swizzle), T and P as [64][64] (128-byte swizzle); then the scalars.  The
+// backward's record has Q, T and P in two bf16 terms, T without its unit
+// diagonal and P without its diagonal.
+template <int DK, bool BWD>
+struct GdRec {
+    static constexpr int K = 0;
+    static constexpr int SC = DK * 128;
+    static constexpr int KSC = SC + kGdSc * kGdC * 4;              // K and the scalars: one copy
+    static constexpr int Q = (KSC + 1023) / 1024 * 1024;           // tiles start on their swizzle's period
+    static constexpr int QL = Q + DK * 128;                        // BWD only
+    static constexpr int T = BWD ? QL + DK * 128 : QL;
+    static constexpr int TL = T + 8192;
+    static constexpr int P = TL + 8192;
+    static constexpr int PL = P + 8192;                            // BWD only
+    static constexpr int BYTES = BWD ? PL + 8192 : PL;
+};
+inline size_t gd_rec_bytes(int dk, bool bwd)
+{
+    switch (dk) {
+    case 64: return bwd ? GdRec<64, true>::BYTES : GdRec<64, false>::BYTES;
+    case 96: return bwd ? GdRec<96, true>::BYTES : GdRec<96, false>::BYTES;
+    default: return bwd ? GdRec<128, true>::BYTES : GdRec<128, false>::BYTES;
+    }
+}
+
+// Sequence of a chunk slot (the last n whose first slot is <= slot).
+__device__ __forceinline__ int gd_seq_of_slot(const GdSeqs& s, int64_t slot)
+{
+    if (!s.cu) return static_cast<int>(slot / ((s.T + kGdC - 1) / kGdC));
+    int lo = 0, hi = s.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        int c = s.cu[mid];
+        c = c < 0 ? 0 : c;
+        if (c / kGdC + mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
 inline int64_t gd_slots(bool packed, int64_t N, int64_t T)
 {
     return packed ? T / kGdC + N : N * ((T + kGdC - 1) / kGdC);
@@ -186,6 +229,7 @@ struct GdParams {
     __nv_bfloat16 *o, *dq, *dkk, *dvv;
     float *s_final, *da, *dbeta, *ds0;
     // workspace, one entry per chunk slot and value head (u = slot * H + h)
+    unsigned char* rec;     // [u]: GdRec (forward)
     __nv_bfloat16* tm;      // [u][2][64][64]: -(T - I), high and low
     __nv_bfloat16* pm;      // [u][1 or 2][64][64]: P without its diagonal
     float* sc;              // [u][6][64]
@@ -201,8 +245,10 @@ struct GdParams {
     int* status;
 };
 
+gla_status gd_launch_chunks(const GdParams& p, bool bwd, cudaStream_t st);
+gla_status gd_launch_sweep_fwd(const GdParams& p, const WaitCtl& ctl, cudaStream_t st);
 gla_status gd_launch_intra(const GdParams& p, bool bwd, cudaStream_t st);
-gla_status gd_launch_sweep_fwd(const GdParams& p, bool bwd, cudaStream_t st);
+gla_status gd_launch_sweep_old(const GdParams& p, bool bwd, cudaStream_t st);
 gla_status gd_launch_sweep_rev(const GdParams& p, cudaStream_t st);
 gla_status gd_launch_grad(const GdParams& p, cudaStream_t st);
 

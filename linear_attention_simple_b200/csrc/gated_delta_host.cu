@@ -50,7 +50,7 @@ gla_status gd_check(int N, int T, int Hk, int H, int dk, int dv, int64_t ld_qkv,
     const int64_t rows = packed ? T : static_cast<int64_t>(N) * T;
     const int64_t widest = *ld_qk > *ld_v ? *ld_qk : *ld_v;
     if (widest > 0 && rows > (int64_t(1) << 40) / widest) return GLA_ERR_UNSUPPORTED;
-    if (gd_slots(packed, N, T) > 0x7FFFFFFF) return GLA_ERR_UNSUPPORTED;
+    if (rows > 0x7FFFFFFF || gd_slots(packed, N, T) > 0x7FFFFFFF) return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
 }
 
@@ -65,6 +65,10 @@ size_t gd_layout(GdParams& p, bool bwd, unsigned char* base)
         at += (bytes + 255) / 256 * 256;
         return q;
     };
+    if (!bwd) {
+        p.rec = take(u * gd_rec_bytes(p.dk, false));
+        return at;
+    }
     p.tm = reinterpret_cast<__nv_bfloat16*>(take(u * 2 * kGdC * kGdC * 2));
     p.pm = reinterpret_cast<__nv_bfloat16*>(take(u * (bwd ? 2 : 1) * kGdC * kGdC * 2));
     p.sc = reinterpret_cast<float*>(take(u * kGdSc * kGdC * 4));
@@ -184,8 +188,8 @@ gla_status gated_delta_chunk_fwd(const void* q, const void* k, const void* v, co
     p.s_final = s_final;
     gd_layout(p, false, static_cast<unsigned char*>(ws));
     if (T > 0 && (s = gd_scan(p, stream)) != GLA_OK) return s;
-    if ((s = gd_launch_intra(p, false, stream)) != GLA_OK) return s;
-    return gd_launch_sweep_fwd(p, false, stream);
+    if ((s = gd_launch_chunks(p, false, stream)) != GLA_OK) return s;
+    return gd_launch_sweep_fwd(p, ctl, stream);
 }
 
 gla_status gated_delta_chunk_bwd(const void* q, const void* k, const void* v, const float* a, const float* beta,
@@ -229,7 +233,7 @@ gla_status gated_delta_chunk_bwd(const void* q, const void* k, const void* v, co
     gd_layout(p, true, static_cast<unsigned char*>(ws));
     if ((s = gd_scan(p, stream)) != GLA_OK) return s;
     if ((s = gd_launch_intra(p, true, stream)) != GLA_OK) return s;
-    if ((s = gd_launch_sweep_fwd(p, true, stream)) != GLA_OK) return s;
+    if ((s = gd_launch_sweep_old(p, true, stream)) != GLA_OK) return s;
     if ((s = gd_launch_sweep_rev(p, stream)) != GLA_OK) return s;
     return gd_launch_grad(p, stream);
 }

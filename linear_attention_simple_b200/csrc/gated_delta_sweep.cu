@@ -253,7 +253,7 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16* dst, int64_t ld, const
 // Forward.  BWD: the backward's own pass over the forward; it keeps the
 // states (fp32 and bf16), y and V', and sums o.dO instead of writing o.
 template <int DK, bool BWD>
-__global__ void __launch_bounds__(max_warps<DK>() * 32, 1) gd_sweep_fwd_kernel(GdParams p)
+__global__ void __launch_bounds__(max_warps<DK>() * 32, 1) gd_sweep_old_kernel(GdParams p)
 {
     constexpr int KS = DK + kGdPad;
     constexpr int PN = BWD ? 2 : 1;
@@ -661,19 +661,19 @@ gla_status launch(K kernel, const char* name, const GdParams& p, bool with_do, i
 
 }  // namespace
 
-gla_status gd_launch_sweep_fwd(const GdParams& p, bool bwd, cudaStream_t st)
+gla_status gd_launch_sweep_old(const GdParams& p, bool bwd, cudaStream_t st)
 {
     if (bwd) {
         switch (p.dk) {
-        case 64: return launch(gd_sweep_fwd_kernel<64, true>, "gd_sweep_fwd_bwd_kernel", p, true, 2, st);
-        case 96: return launch(gd_sweep_fwd_kernel<96, true>, "gd_sweep_fwd_bwd_kernel", p, true, 2, st);
-        default: return launch(gd_sweep_fwd_kernel<128, true>, "gd_sweep_fwd_bwd_kernel", p, true, 2, st);
+        case 64: return launch(gd_sweep_old_kernel<64, true>, "gd_sweep_fwd_bwd_kernel", p, true, 2, st);
+        case 96: return launch(gd_sweep_old_kernel<96, true>, "gd_sweep_fwd_bwd_kernel", p, true, 2, st);
+        default: return launch(gd_sweep_old_kernel<128, true>, "gd_sweep_fwd_bwd_kernel", p, true, 2, st);
         }
     }
     switch (p.dk) {
-    case 64: return launch(gd_sweep_fwd_kernel<64, false>, "gd_sweep_fwd_kernel", p, false, 1, st);
-    case 96: return launch(gd_sweep_fwd_kernel<96, false>, "gd_sweep_fwd_kernel", p, false, 1, st);
-    default: return launch(gd_sweep_fwd_kernel<128, false>, "gd_sweep_fwd_kernel", p, false, 1, st);
+    case 64: return launch(gd_sweep_old_kernel<64, false>, "gd_sweep_old_kernel", p, false, 1, st);
+    case 96: return launch(gd_sweep_old_kernel<96, false>, "gd_sweep_old_kernel", p, false, 1, st);
+    default: return launch(gd_sweep_old_kernel<128, false>, "gd_sweep_old_kernel", p, false, 1, st);
     }
 }
 

@@ -1,0 +1,484 @@
+// gated_delta_sweep_tc.cu -- the forward sweep of the gated delta rule over a
+// sequence's chunks: outputs and final state.
+//
+// The state is held transposed, [dv][dk], dv rows on the lanes of tensor
+// memory, so that every left operand of the recurrence (the state, R, V', the
+// update) comes from tensor memory and only the chunk's own operands (K, Q, T,
+// P) pass through shared memory, brought whole by one bulk copy a chunk.  Per
+// chunk, M = 128 lanes of dv rows, N tokens or dk columns:
+//
+//   Y  = S K^T            workers:  R  = V - G Y
+//   O  = S (scale G Q)^T
+//   Z  = R T^T                      V' = beta Z,  W = (e^{b_63 - b} V')
+//   dS = W K                        S  = G_63 S + dS   (fp32, in registers)
+//   O += V' P^T                     o
+//
+// with T = (I + tril(K K^T . D beta_j, -1))^-1.  Worker threads hold one lane
+// (dv row) and half of the columns.  S, R and W enter as two bf16 terms
+// against operands exact in bf16 (K) or of two terms (T): 16 bits of each
+// value, for the fp32 state; o leaves in bf16 and takes one term of each.
+//
+// V is read from a shared [token][row] slice and o leaves through the same
+// one, two stages, each a single tensor copy (a bulk copy per token row was
+// measured at twice the whole kernel's time: the copy unit takes some 80
+// cycles for each, however short).  Each step waits for the one before, so a CTA is bound by the chain of
+// small products and conversions; two CTAs share an SM (256 columns of tensor
+// memory and about 100 KB each at dk <= 96) and fill each other's gaps.
+#include "gated_delta.cuh"
+
+namespace gla {
+namespace {
+
+constexpr int kWorkers = 8;                          // worker warps
+constexpr int kThreads = (kWorkers + 2) * 32;        // + a copy warp and an issue warp
+
+// Tensor memory columns.
+template <int DK>
+struct Cols {
+    static constexpr int S = 0;                      // state terms -> Z -> dS
+    static constexpr int Y = DK;                     // Y -> R terms -> W terms
+    static constexpr int V = DK + 64;                // V', one term
+    static constexpr int O = DK + 96;
+    static constexpr int ALLOC = DK + 160 <= 256 ? 256 : 512;
+};
+
+// Tensor maps of V and o; the last slice of dv may be narrower than the others.
+struct SliceMaps {
+    CUtensorMap v, v_last, o, o_last;
+};
+
+struct __align__(8) Bars {
+    uint64_t full[2], empty[2];                      // K, scalars and V
+    uint64_t fq, ft, fp, eq, et, ep;                 // Q, T, P
+    uint64_t s, r, w, o;                             // workers -> issuer
+    uint64_t staged[2];                              // workers -> copies: o is in the V slice
+    uint64_t y, z, ds, out, drain;                   // issuer -> workers
+    uint32_t tmem;
+};
+
+// Shared memory of a CTA.
+template <int DK>
+struct Smem {
+    using Rec = GdRec<DK, false>;
+    static constexpr int KSC = (Rec::KSC + 1023) / 1024 * 1024;    // a stage of K and scalars
+    static constexpr int Q = 2 * KSC, T = Q + DK * 128, P = T + 16384, V = P + 8192;
+    static constexpr int bytes(int sw) { return V + 2 * kGdC * sw * 2 + 1024; }
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
+                     "r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+
+// Sixteen fp32 values as two bf16 terms: 8 columns each.
+__device__ __forceinline__ void split16(const float (&x)[16], uint32_t (&hi)[8], uint32_t (&lo)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        hi[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        lo[i] = pack_bf16(x[2 * i] - bf16_lo(hi[i]), x[2 * i + 1] - bf16_hi(hi[i]));
+    }
+}
+__device__ __forceinline__ void load16(float (&x)[16], const float* p)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(p + i);
+}
+__device__ __forceinline__ void get16(float (&x)[16], uint32_t taddr)
+{
+    uint32_t r[16];
+    tmem_ld16(taddr, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+// A wait of a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl)
+{
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ctl));
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ SliceMaps maps, int sw, WaitCtl ctl)
+{
+    using C = Cols<DK>;
+    using M = Smem<DK>;
+    using Rec = GdRec<DK, false>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ Bars B;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = blockIdx.x / p.seqs.H, h = blockIdx.x - n * p.seqs.H;
+    int64_t row0;
+    int len;
+    p.seqs.span(n, row0, len);
+    if (len < 0) {
+        if (tid == 0) record_status(p.status, GLA_ERR_INVALID_ARG);
+        return;
+    }
+    const int w0 = blockIdx.y * sw, rows = min(sw, p.dv - w0);      // this CTA's dv rows
+    const int nc = (len + kGdC - 1) / kGdC;
+    const unsigned char* rec = p.rec + (p.seqs.slot0(n, row0) * p.seqs.H + h) * Rec::BYTES;
+    const int64_t rec_step = static_cast<int64_t>(p.seqs.H) * Rec::BYTES;
+    const int64_t nh = static_cast<int64_t>(n) * p.seqs.H + h;
+    const int active = 2 * (rows >> 5);                             // worker warps with rows
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.full[i], 1);
+            mbar_init(&B.empty[i], 1 + active);
+            mbar_init(&B.staged[i], active);
+        }
+        uint64_t* tiles[6] = {&B.fq, &B.ft, &B.fp, &B.eq, &B.et, &B.ep};
+        for (uint64_t* b : tiles) mbar_init(b, 1);
+        uint64_t* from_workers[4] = {&B.s, &B.r, &B.w, &B.o};
+        for (uint64_t* b : from_workers) mbar_init(b, active);
+        uint64_t* from_issuer[5] = {&B.y, &B.z, &B.ds, &B.out, &B.drain};
+        for (uint64_t* b : from_issuer) mbar_init(b, 1);
+        mbar_init_fence();
+    }
+    if (warp == kWorkers + 1) {
+        tmem_alloc(&B.tmem, C::ALLOC);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = B.tmem;
+
+    if (warp == kWorkers) {
+        // ---- copies
+        if (lane == 0) {
+            const bool whole = rows == sw;               // the last slice may be narrower
+            const CUtensorMap* mv = whole ? &maps.v : &maps.v_last;
+            const CUtensorMap* mo = whole ? &maps.o : &maps.o_last;
+            const uint32_t vbytes = kGdC * rows * 2;
+            const int col = h * p.dv + w0;
+            bool ok = true;
+            // K, scalars and V of chunk c (rows behind the sequence's end are not used)
+            auto first = [&](int c) {
+                const int st = c & 1;
+                mbar_arrive_expect_tx(&B.full[st], Rec::KSC + vbytes);
+                bulk_load(smem + st * M::KSC, rec + c * rec_step, Rec::KSC, &B.full[st]);
+                tma_load_2d(smem + M::V + st * kGdC * sw * 2, mv, &B.full[st], col,
+                            static_cast<int>(row0) + c * kGdC);
+            };
+            auto tile = [&](int c, uint64_t* full, uint64_t* empty, int at, int from, uint32_t bytes) {
+                if (c > 0 && !mbar_wait(empty, (c - 1) & 1, ctl)) return false;
+                mbar_arrive_expect_tx(full, bytes);
+                bulk_load(smem + at, rec + c * rec_step + from, bytes, full);
+                return true;
+            };
+            int a = 0, q = 0, t = 0, pp = 0;             // copies issued of each kind
+            if (nc > 0) first(a++);
+            for (int c = 0; c < nc; ++c) {
+                ok = tile(c, &B.fq, &B.eq, M::Q, Rec::Q, DK * 128);
+                if (!ok) break;
+                ++q;
+                ok = tile(c, &B.ft, &B.et, M::T, Rec::T, 16384);
+                if (!ok) break;
+                ++t;
+                ok = tile(c, &B.fp, &B.ep, M::P, Rec::P, 8192);
+                if (!ok) break;
+                ++pp;
+                if (c > 0) {
+                    // o of the chunk before: out of its slice, which then takes the next chunk's V
+                    const int st = (c - 1) & 1;
+                    ok = mbar_wait(&B.staged[st], ((c - 1) >> 1) & 1, ctl);
+                    if (!ok) break;
+                    tma_store_2d(mo, smem + M::V + st * kGdC * sw * 2, col, static_cast<int>(row0) + (c - 1) * kGdC);
+                    tma_store_commit();
+                    tma_store_wait_read();
+                    if (c + 1 < nc) ok = mbar_wait(&B.empty[st], ((c - 1) >> 1) & 1, ctl);
+                    if (!ok) break;
+                }
+                if (c + 1 < nc) first(a++);
+            }
+            if (ok && nc > 0) {
+                const int c = nc - 1, st = c & 1, valid = len - c * kGdC;
+                const unsigned char* slice = smem + M::V + st * kGdC * sw * 2;
+                if (mbar_wait(&B.staged[st], (c >> 1) & 1, ctl)) {
+                    if (valid == kGdC) {
+                        tma_store_2d(mo, slice, col, static_cast<int>(row0) + c * kGdC);
+                    } else {                             // the rows behind are another sequence's
+                        const int64_t ld_o = static_cast<int64_t>(p.seqs.H) * p.dv;
+                        for (int i = 0; i < valid; ++i)
+                            bulk_store(p.o + (row0 + static_cast<int64_t>(c) * kGdC + i) * ld_o + col, slice + i * rows * 2,
+                                       rows * 2);
+                    }
+                }
+                tma_store_commit();
+            }
+            // no copy may be in flight when the block ends
+            tma_store_wait_read();
+            for (int c = max(0, a - 2); c < a; ++c) mbar_wait(&B.full[c & 1], (c >> 1) & 1, ctl);
+            if (q > 0) mbar_wait(&B.fq, (q - 1) & 1, ctl);
+            if (t > 0) mbar_wait(&B.ft, (t - 1) & 1, ctl);
+            if (pp > 0) mbar_wait(&B.fp, (pp - 1) & 1, ctl);
+        }
+    } else if (warp == kWorkers + 1) {
+        // ---- products
+        if (lane == 0) {
+            const uint64_t q_k = smem_desc(smem_u32(smem + M::Q), 16, 512, kLayoutSW64);
+            const uint64_t t_k = smem_desc(smem_u32(smem + M::T), 16, 1024, kLayoutSW128);
+            const uint64_t p_k = smem_desc(smem_u32(smem + M::P), 16, 1024, kLayoutSW128);
+            constexpr uint32_t idDk = idesc_bf16_f32(128, DK, 0, 1);
+            for (int c = 0; c < nc; ++c) {
+                const uint32_t st = smem_u32(smem + (c & 1) * M::KSC);
+                const uint64_t k_k = smem_desc(st, 16, 512, kLayoutSW64);
+                const uint64_t k_n = smem_desc(st, 4096, 512, kLayoutSW64);
+                constexpr uint32_t id64 = idesc_bf16_f32(128, 64, 0, 0);
+                if (!mbar_wait(&B.full[c & 1], (c >> 1) & 1, ctl)) break;
+                if (!mbar_wait(&B.s, c & 1, ctl)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k) {
+                    const uint64_t b = desc_add(k_k, (k >> 1) * 4096 + (k & 1) * 32);
+                    umma_bf16_ts(tm + C::Y, tm + C::S + 16 * k, b, id64, k > 0);
+                    umma_bf16_ts(tm + C::Y, tm + C::S + 16 * k + 8, b, id64, 1);
+                }
+                umma_commit(&B.y);
+                if (c > 0 && !mbar_wait(&B.o, (c - 1) & 1, ctl)) break;
+                if (!mbar_wait(&B.fq, c & 1, ctl)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k)
+                    umma_bf16_ts(tm + C::O, tm + C::S + 16 * k, desc_add(q_k, (k >> 1) * 4096 + (k & 1) * 32), id64,
+                                 k > 0);
+                umma_commit(&B.eq);
+                if (!mbar_wait(&B.ft, c & 1, ctl)) break;
+                if (!mbar_wait(&B.r, c & 1, ctl)) break;
+                tc_fence_after();
+                // T and P are lower triangular: step s reaches tokens 16 s on
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t id = idesc_bf16_f32(128, 64 - 16 * s, 0, 0);
+                    const uint64_t hi = desc_add(t_k, 2048 * s + 32 * s), lo = desc_add(hi, 8192);
+                    const uint32_t d = tm + C::S + 16 * s, a = tm + C::Y + 16 * s;
+                    umma_bf16_ts(d, a, hi, id, s > 0);
+                    umma_bf16_ts(d, a + 8, hi, id, 1);
+                    umma_bf16_ts(d, a, lo, id, 1);
+                }
+                umma_commit(&B.z);
+                umma_commit(&B.et);
+                if (!mbar_wait(&B.w, c & 1, ctl)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    umma_bf16_ts(tm + C::S, tm + C::Y + 16 * s, desc_add(k_n, 1024 * s), idDk, s > 0);
+                    umma_bf16_ts(tm + C::S, tm + C::Y + 16 * s + 8, desc_add(k_n, 1024 * s), idDk, 1);
+                }
+                umma_commit(&B.ds);
+                if (!mbar_wait(&B.fp, c & 1, ctl)) break;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    umma_bf16_ts(tm + C::O + 16 * s, tm + C::V + 8 * s, desc_add(p_k, 2048 * s + 32 * s),
+                                 idesc_bf16_f32(128, 64 - 16 * s, 0, 0), 1);
+                umma_commit(&B.out);
+                umma_commit(&B.ep);
+                umma_commit(&B.empty[c & 1]);
+            }
+            umma_commit(&B.drain);
+            mbar_wait(&B.drain, 0, ctl);
+        }
+    } else if ((warp & 3) * 32 < rows) {
+        // ---- workers: lane = dv row, half of the columns
+        const int half = warp >> 2, r = w0 + (warp & 3) * 32 + lane;
+        const uint32_t t0 = tm + (static_cast<uint32_t>(warp & 3) << 21);       // lane quarter
+        constexpr int HS = DK / 2;                                              // state columns of a thread
+        float S[HS];
+        const float* s0 = p.s0 ? p.s0 + (nh * DK + half * HS) * p.dv + r : nullptr;
+#pragma unroll
+        for (int i = 0; i < HS; ++i) S[i] = s0 ? s0[static_cast<int64_t>(i) * p.dv] : 0.f;
+        auto put_state = [&]() {
+#pragma unroll
+            for (int k = 0; k < HS / 16; ++k) {
+                float x[16];
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = S[16 * k + i];
+                split16(x, hi, lo);
+                tmem_st8(t0 + C::S + half * HS + 16 * k, hi);
+                tmem_st8(t0 + C::S + half * HS + 16 * k + 8, lo);
+            }
+        };
+        auto done = [&](uint64_t* bar) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        if (nc > 0) {
+            put_state();
+            done(&B.s);
+        }
+        bool ok = true;
+        for (int c = 0; c < nc; ++c) {
+            const int ph = c & 1;
+            const float* sc = reinterpret_cast<const float*>(smem + ph * M::KSC + Rec::SC);
+            __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(smem + M::V) + ph * kGdC * sw + half * 32 * rows +
+                                (warp & 3) * 32 + lane;                       // this row's 32 tokens
+            const int left = len - c * kGdC - half * 32;                      // tokens of those in the sequence
+            ok = warp_wait(&B.full[ph], (c >> 1) & 1, ctl) && warp_wait(&B.y, ph, ctl);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int s = half * 2 + b;
+                float x[16], G[16];
+                uint32_t hi[8], lo[8];
+                load16(G, sc + kScG * kGdC + 16 * s);
+                get16(x, t0 + C::Y + 16 * s);
+                // rows behind the sequence's end: what lies in the slice is not V
+                if (left >= 32) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = fmaf(-G[i], x[i], __bfloat162float(vs[(16 * b + i) * rows]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        x[i] = 16 * b + i < left ? fmaf(-G[i], x[i], __bfloat162float(vs[(16 * b + i) * rows])) : 0.f;
+                }
+                split16(x, hi, lo);
+                tmem_st8(t0 + C::Y + 16 * s, hi);
+                tmem_st8(t0 + C::Y + 16 * s + 8, lo);
+            }
+            done(&B.r);
+            ok = warp_wait(&B.z, ph, ctl);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int s = half * 2 + b;
+                float x[16], f[16];
+                uint32_t hi[8], lo[8];
+                get16(x, t0 + C::S + 16 * s);
+                load16(f, sc + kScBeta * kGdC + 16 * s);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] *= f[i];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hi[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+                tmem_st8(t0 + C::V + 8 * s, hi);
+                load16(f, sc + kScR * kGdC + 16 * s);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] *= f[i];
+                split16(x, hi, lo);
+                tmem_st8(t0 + C::Y + 16 * s, hi);
+                tmem_st8(t0 + C::Y + 16 * s + 8, lo);
+            }
+            done(&B.w);
+            const float gl = sc[kScG * kGdC + kGdC - 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.empty[ph]);          // the scalars are read
+            ok = warp_wait(&B.ds, ph, ctl);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < HS / 16; ++k) {
+                float x[16];
+                get16(x, t0 + C::S + half * HS + 16 * k);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[16 * k + i] = fmaf(gl, S[16 * k + i], x[i]);
+            }
+            if (c + 1 < nc) {
+                put_state();
+                done(&B.s);
+            }
+            ok = warp_wait(&B.out, ph, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t x[32];
+            tmem_ld32(t0 + C::O + half * 32, x);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) vs[i * rows] = __float2bfloat16_rn(__uint_as_float(x[i]));
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.staged[ph]);
+        }
+        if (ok && p.s_final) {
+            float* s = p.s_final + (nh * DK + half * HS) * p.dv + r;
+#pragma unroll
+            for (int i = 0; i < HS; ++i) s[static_cast<int64_t>(i) * p.dv] = S[i];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWorkers + 1) tmem_dealloc(tm, C::ALLOC);
+}
+
+// [token][width of all heads] bf16 rows, ld apart; a box is a chunk's tokens of one slice.
+gla_status slice_map(CUtensorMap* m, const void* base, int64_t width, int64_t ld, int64_t tokens, int box)
+{
+    const uint64_t dims[2] = {static_cast<uint64_t>(width), static_cast<uint64_t>(tokens)};
+    const uint64_t strides[2] = {2, static_cast<uint64_t>(ld) * 2};
+    const uint32_t boxes[2] = {static_cast<uint32_t>(box), kGdC};
+    return make_tmap(m, base, 2, dims, strides, boxes, 2, 0);
+}
+
+template <int DK>
+gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
+{
+    // as few slices of dv rows as 128 lanes allow, of equal width: a CTA's time
+    // does not depend on how many of its lanes hold rows
+    const int slices = (p.dv + 127) / 128, sw = (p.dv / 32 + slices - 1) / slices * 32;
+    const int last = p.dv - (slices - 1) * sw;
+    const int64_t width = static_cast<int64_t>(p.seqs.H) * p.dv;
+    const int64_t tokens = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;
+    SliceMaps maps{};
+    gla_status s = GLA_OK;
+    if (tokens > 0) {
+        if ((s = slice_map(&maps.v, p.v, width, p.ld_v, tokens, sw)) != GLA_OK ||
+            (s = slice_map(&maps.v_last, p.v, width, p.ld_v, tokens, last)) != GLA_OK ||
+            (s = slice_map(&maps.o, p.o, width, width, tokens, sw)) != GLA_OK ||
+            (s = slice_map(&maps.o_last, p.o, width, width, tokens, last)) != GLA_OK)
+            return s;
+    }
+    const int smem = Smem<DK>::bytes(sw);
+    cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return status_of(e);
+    trace_begin(st);
+    gd_sweep_fwd_kernel<DK><<<dim3(static_cast<unsigned>(p.seqs.N) * p.seqs.H, slices), kThreads, smem, st>>>(p, maps, sw, ctl);
+    trace_end(st, "gd_sweep_fwd_kernel");
+    count_launch();
+    return check_launch("gd_sweep_fwd_kernel");
+}
+
+}  // namespace
+
+gla_status gd_launch_sweep_fwd(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
+{
+    switch (p.dk) {
+    case 64: return launch<64>(p, ctl, st);
+    case 96: return launch<96>(p, ctl, st);
+    default: return launch<128>(p, ctl, st);
+    }
+}
+
+}  // namespace gla
