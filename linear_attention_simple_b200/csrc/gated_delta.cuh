@@ -148,12 +148,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr)
                  : "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b),
-                 "r"(c), "r"(d)
-                 : "memory");
-}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -168,52 +162,9 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 //           (k 0-7, k 8-15), r2, r3 of n 8-15.
 //   rows_k: the same from a tile stored [k][n], with ldsm4_t.
 //   rows_a: a left operand of 16 rows from a tile stored [m][k].
-//   rows_at: a left operand, or an accumulator-shaped tile, from a tile stored
-//           [k][m], with ldsm4_t (and stsm4_t).
 __device__ __forceinline__ int rows_n(int lane, int ld) { return ((lane & 7) + ((lane >> 4) << 3)) * ld + (((lane >> 3) & 1) << 3); }
 __device__ __forceinline__ int rows_k(int lane, int ld) { return ((lane & 7) + (((lane >> 3) & 1) << 3)) * ld + ((lane >> 4) << 3); }
 __device__ __forceinline__ int rows_a(int lane, int ld) { return (lane & 15) * ld + ((lane >> 4) << 3); }
-__device__ __forceinline__ int rows_at(int lane, int ld) { return ((lane & 7) + ((lane >> 4) << 3)) * ld + (((lane >> 3) & 1) << 3); }
-
-// ---- fp32 values as sums of bf16 terms.  Two terms hold 16 bits of a
-// value (error at most 2^-17 of it), three 24: what the fp32 outputs need,
-// where one bf16 rounding (2^-9) would be all of the error.
-template <int NT>
-struct Split {
-    uint32_t t[NT][4];
-};
-// Two neighbouring tiles of accumulators (16 x 8 each) as the left operand of
-// a 16-deep step, in NT terms.
-template <int NT>
-__device__ __forceinline__ void split_pair(Split<NT>& s, int i, float x, float y)
-{
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const uint32_t w = pack_bf16(x, y);
-        s.t[n][i] = w;
-        if (n + 1 < NT) {
-            x -= bf16_lo(w);
-            y -= bf16_hi(w);
-        }
-    }
-}
-template <int NT>
-__device__ __forceinline__ Split<NT> split_tiles(const float (&a)[4], const float (&b)[4])
-{
-    Split<NT> s;
-    split_pair<NT>(s, 0, a[0], a[1]);
-    split_pair<NT>(s, 1, a[2], a[3]);
-    split_pair<NT>(s, 2, b[0], b[1]);
-    split_pair<NT>(s, 3, b[2], b[3]);
-    return s;
-}
-// d += s * B for an exact (one-term) right operand.
-template <int NT>
-__device__ __forceinline__ void mma_split(float (&d)[4], const Split<NT>& s, uint32_t b0, uint32_t b1)
-{
-#pragma unroll
-    for (int n = NT - 1; n >= 0; --n) mma_bf16(d, s.t[n], b0, b1);
-}
 
 // 2^x for the decay factors: x <= 0 here (0 -> 1, very negative -> 0).
 __device__ __forceinline__ float gd_exp2(float x) { return exp2f(x); }
@@ -229,27 +180,22 @@ struct GdParams {
     __nv_bfloat16 *o, *dq, *dkk, *dvv;
     float *s_final, *da, *dbeta, *ds0;
     // workspace, one entry per chunk slot and value head (u = slot * H + h)
-    unsigned char* rec;     // [u]: GdRec (forward)
-    __nv_bfloat16* tm;      // [u][2][64][64]: -(T - I), high and low
-    __nv_bfloat16* pm;      // [u][1 or 2][64][64]: P without its diagonal
-    float* sc;              // [u][6][64]
-    // backward only
+    unsigned char* rec;     // [u]: GdRec
+    // backward only; a "half row" is a thread's: one dv row, half of the columns
     __nv_bfloat16 *sb, *eb; // [u][dv][dk]: the state entering, the gradient of the state leaving
-    float* sn;              // [u][dv / 16][dk / 8 * 128]: the state entering in fp32, a warp's register order
+    float* sn;              // [u][dv / 32][2][dk / 8][32 lanes][4]: the state entering in fp32, half rows
     float* sn_last;         // [N H][..]: the final state in the same form
-    float* yn;              // [u][dv / 16][1024]: y in register order
+    float* yn;              // [u][dv / 32][2][8][32 lanes][4]: y, half rows
     __nv_bfloat16* vp;      // [u][64][dv]: V'
-    float* part;            // [u][3][dv / 16][64]: per-warp sums over dv
-    float* anch;            // [u][dv / 16]: <gradient of the state leaving, state leaving>
+    float* part;            // [u][3][dv / 32][64]: sums over 32 dv rows, per token
+    float* anch;            // [u][dv / 32][2]: <gradient of the state leaving, state leaving>
     int64_t slots;
     int* status;
 };
 
 gla_status gd_launch_chunks(const GdParams& p, bool bwd, cudaStream_t st);
 gla_status gd_launch_sweep_fwd(const GdParams& p, const WaitCtl& ctl, cudaStream_t st);
-gla_status gd_launch_intra(const GdParams& p, bool bwd, cudaStream_t st);
-gla_status gd_launch_sweep_old(const GdParams& p, bool bwd, cudaStream_t st);
-gla_status gd_launch_sweep_rev(const GdParams& p, cudaStream_t st);
+gla_status gd_launch_sweeps_bwd(const GdParams& p, const WaitCtl& ctl, cudaStream_t st);
 gla_status gd_launch_grad(const GdParams& p, cudaStream_t st);
 
 }  // namespace gla

@@ -91,19 +91,7 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
 
     const int64_t slot = blockIdx.x;
     const int hk = blockIdx.y;
-    // the sequence of this slot
-    int n = 0;
-    if (!p.seqs.cu) {
-        n = static_cast<int>(slot / ((p.seqs.T + kGdC - 1) / kGdC));
-    } else {
-        int hi = p.seqs.N - 1;
-        while (n < hi) {
-            const int mid = (n + hi + 1) >> 1;
-            const int c = max(p.seqs.cu[mid], 0);
-            if (c / kGdC + mid <= slot) n = mid;
-            else hi = mid - 1;
-        }
-    }
+    const int n = gd_seq_of_slot(p.seqs, slot);
     int64_t row0;
     int len;
     p.seqs.span(n, row0, len);
@@ -114,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
     const int64_t row = row0 + c * kGdC;
     const int H = p.seqs.H, group = H / p.seqs.Hk;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, c2 = (lane & 3) * 2;
-    const int nst = p.dv / kSl, wtot = p.dv >> 4;
+    const int nst = p.dv / kSl, wtot = p.dv >> 5;
 
     gd_load_rows(sk, KS, p.k + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
     gd_load_rows(sq, KS, p.q + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
@@ -132,7 +120,8 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
               p.vp + u * kGdC * p.dv, p.sb + u * p.dv * DK, p.eb + u * p.dv * DK,
               p.ld_do, static_cast<int64_t>(H) * p.dv, p.dv, valid};
         __syncthreads();                   // the last head's scalars and stages are read
-        for (int i = tid; i < kGdSc * kGdC; i += kThreads) sc[i] = p.sc[u * kGdSc * kGdC + i];
+        const float* src_sc = reinterpret_cast<const float*>(p.rec + u * GdRec<DK, true>::BYTES + GdRec<DK, true>::SC);
+        for (int i = tid; i < kGdSc * kGdC; i += kThreads) sc[i] = src_sc[i];
         load_slice<DK>(sst, x, 0, false, tid);
         cp_async_commit();
 
@@ -194,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
                 od.x += a.x; od.y += a.y;
                 s1.x += b.x; s1.y += b.y;
                 s2.x += e.x; s2.y += e.y;
-                tail += p.anch[u * wtot + t];
+                const float2 an = *reinterpret_cast<const float2*>(p.anch + (u * wtot + t) * 2);
+                tail += an.x + an.y;
             }
             const float d1 = od.y - s1.y;
             float s = (od.x - s1.x) + d1;          // sums over this lane's tokens and all later ones

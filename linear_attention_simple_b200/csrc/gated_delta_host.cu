@@ -65,13 +65,7 @@ size_t gd_layout(GdParams& p, bool bwd, unsigned char* base)
         at += (bytes + 255) / 256 * 256;
         return q;
     };
-    if (!bwd) {
-        p.rec = take(u * gd_rec_bytes(p.dk, false));
-        return at;
-    }
-    p.tm = reinterpret_cast<__nv_bfloat16*>(take(u * 2 * kGdC * kGdC * 2));
-    p.pm = reinterpret_cast<__nv_bfloat16*>(take(u * (bwd ? 2 : 1) * kGdC * kGdC * 2));
-    p.sc = reinterpret_cast<float*>(take(u * kGdSc * kGdC * 4));
+    p.rec = take(u * gd_rec_bytes(p.dk, bwd));
     if (bwd) {
         p.sb = reinterpret_cast<__nv_bfloat16*>(take(u * dk * dv * 2));
         p.eb = reinterpret_cast<__nv_bfloat16*>(take(u * dk * dv * 2));
@@ -79,8 +73,8 @@ size_t gd_layout(GdParams& p, bool bwd, unsigned char* base)
         p.sn_last = reinterpret_cast<float*>(take(static_cast<size_t>(p.seqs.N) * p.seqs.H * dk * dv * 4));
         p.yn = reinterpret_cast<float*>(take(u * kGdC * dv * 4));
         p.vp = reinterpret_cast<__nv_bfloat16*>(take(u * kGdC * dv * 2));
-        p.part = reinterpret_cast<float*>(take(u * 3 * (dv / 16) * kGdC * 4));
-        p.anch = reinterpret_cast<float*>(take(u * (dv / 16) * 4));
+        p.part = reinterpret_cast<float*>(take(u * 3 * (dv / 32) * kGdC * 4));
+        p.anch = reinterpret_cast<float*>(take(u * (dv / 32) * 2 * 4));
     }
     return at;
 }
@@ -232,9 +226,8 @@ gla_status gated_delta_chunk_bwd(const void* q, const void* k, const void* v, co
     p.ds0 = grad_s0;
     gd_layout(p, true, static_cast<unsigned char*>(ws));
     if ((s = gd_scan(p, stream)) != GLA_OK) return s;
-    if ((s = gd_launch_intra(p, true, stream)) != GLA_OK) return s;
-    if ((s = gd_launch_sweep_old(p, true, stream)) != GLA_OK) return s;
-    if ((s = gd_launch_sweep_rev(p, stream)) != GLA_OK) return s;
+    if ((s = gd_launch_chunks(p, true, stream)) != GLA_OK) return s;
+    if ((s = gd_launch_sweeps_bwd(p, ctl, stream)) != GLA_OK) return s;
     return gd_launch_grad(p, stream);
 }
 

@@ -24,13 +24,10 @@
 // cycles for each, however short).  Each step waits for the one before, so a CTA is bound by the chain of
 // small products and conversions; two CTAs share an SM (256 columns of tensor
 // memory and about 100 KB each at dk <= 96) and fill each other's gaps.
-#include "gated_delta.cuh"
+#include "gated_delta_tc.cuh"
 
 namespace gla {
 namespace {
-
-constexpr int kWorkers = 8;                          // worker warps
-constexpr int kThreads = (kWorkers + 2) * 32;        // + a copy warp and an issue warp
 
 // Tensor memory columns.
 template <int DK>
@@ -40,11 +37,6 @@ struct Cols {
     static constexpr int V = DK + 64;                // V', one term
     static constexpr int O = DK + 96;
     static constexpr int ALLOC = DK + 160 <= 256 ? 256 : 512;
-};
-
-// Tensor maps of V and o; the last slice of dv may be narrower than the others.
-struct SliceMaps {
-    CUtensorMap v, v_last, o, o_last;
 };
 
 struct __align__(8) Bars {
@@ -65,65 +57,9 @@ struct Smem {
     static constexpr int bytes(int sw) { return V + 2 * kGdC * sw * 2 + 1024; }
 };
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
-                     "r"(smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
-                 : "memory");
-}
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-                 : "memory");
-}
-
-// Sixteen fp32 values as two bf16 terms: 8 columns each.
-__device__ __forceinline__ void split16(const float (&x)[16], uint32_t (&hi)[8], uint32_t (&lo)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        hi[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        lo[i] = pack_bf16(x[2 * i] - bf16_lo(hi[i]), x[2 * i + 1] - bf16_hi(hi[i]));
-    }
-}
-__device__ __forceinline__ void load16(float (&x)[16], const float* p)
-{
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(p + i);
-}
-__device__ __forceinline__ void get16(float (&x)[16], uint32_t taddr)
-{
-    uint32_t r[16];
-    tmem_ld16(taddr, r);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
-}
-
-// A wait of a whole warp: one answer for all lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl)
-{
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ctl));
-}
-
 template <int DK>
-__global__ void __launch_bounds__(kThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ SliceMaps maps, int sw, WaitCtl ctl)
+__global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v,
+                                                                                  const __grid_constant__ GdMap map_o, int sw, WaitCtl ctl)
 {
     using C = Cols<DK>;
     using M = Smem<DK>;
@@ -161,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_kerne
         for (uint64_t* b : from_issuer) mbar_init(b, 1);
         mbar_init_fence();
     }
-    if (warp == kWorkers + 1) {
+    if (warp == kGdWorkers + 1) {
         tmem_alloc(&B.tmem, C::ALLOC);
         tmem_relinquish();
     }
@@ -170,12 +106,12 @@ __global__ void __launch_bounds__(kThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_kerne
     tc_fence_after();
     const uint32_t tm = B.tmem;
 
-    if (warp == kWorkers) {
+    if (warp == kGdWorkers) {
         // ---- copies
         if (lane == 0) {
             const bool whole = rows == sw;               // the last slice may be narrower
-            const CUtensorMap* mv = whole ? &maps.v : &maps.v_last;
-            const CUtensorMap* mo = whole ? &maps.o : &maps.o_last;
+            const CUtensorMap* mv = whole ? &map_v.all : &map_v.last;
+            const CUtensorMap* mo = whole ? &map_o.all : &map_o.last;
             const uint32_t vbytes = kGdC * rows * 2;
             const int col = h * p.dv + w0;
             bool ok = true;
@@ -240,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_kerne
             if (t > 0) mbar_wait(&B.ft, (t - 1) & 1, ctl);
             if (pp > 0) mbar_wait(&B.fp, (pp - 1) & 1, ctl);
         }
-    } else if (warp == kWorkers + 1) {
+    } else if (warp == kGdWorkers + 1) {
         // ---- products
         if (lane == 0) {
             const uint64_t q_k = smem_desc(smem_u32(smem + M::Q), 16, 512, kLayoutSW64);
@@ -430,41 +366,26 @@ __global__ void __launch_bounds__(kThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_kerne
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kWorkers + 1) tmem_dealloc(tm, C::ALLOC);
-}
-
-// [token][width of all heads] bf16 rows, ld apart; a box is a chunk's tokens of one slice.
-gla_status slice_map(CUtensorMap* m, const void* base, int64_t width, int64_t ld, int64_t tokens, int box)
-{
-    const uint64_t dims[2] = {static_cast<uint64_t>(width), static_cast<uint64_t>(tokens)};
-    const uint64_t strides[2] = {2, static_cast<uint64_t>(ld) * 2};
-    const uint32_t boxes[2] = {static_cast<uint32_t>(box), kGdC};
-    return make_tmap(m, base, 2, dims, strides, boxes, 2, 0);
+    if (warp == kGdWorkers + 1) tmem_dealloc(tm, C::ALLOC);
 }
 
 template <int DK>
 gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
 {
-    // as few slices of dv rows as 128 lanes allow, of equal width: a CTA's time
-    // does not depend on how many of its lanes hold rows
-    const int slices = (p.dv + 127) / 128, sw = (p.dv / 32 + slices - 1) / slices * 32;
-    const int last = p.dv - (slices - 1) * sw;
+    const GdSlices sl(p.dv);
     const int64_t width = static_cast<int64_t>(p.seqs.H) * p.dv;
     const int64_t tokens = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;
-    SliceMaps maps{};
+    GdMap v{}, o{};
     gla_status s = GLA_OK;
-    if (tokens > 0) {
-        if ((s = slice_map(&maps.v, p.v, width, p.ld_v, tokens, sw)) != GLA_OK ||
-            (s = slice_map(&maps.v_last, p.v, width, p.ld_v, tokens, last)) != GLA_OK ||
-            (s = slice_map(&maps.o, p.o, width, width, tokens, sw)) != GLA_OK ||
-            (s = slice_map(&maps.o_last, p.o, width, width, tokens, last)) != GLA_OK)
-            return s;
-    }
-    const int smem = Smem<DK>::bytes(sw);
+    if (tokens > 0 && ((s = gd_slice_map(&v, p.v, width, p.ld_v, tokens, sl.width, sl.last)) != GLA_OK ||
+                       (s = gd_slice_map(&o, p.o, width, width, tokens, sl.width, sl.last)) != GLA_OK))
+        return s;
+    const int smem = Smem<DK>::bytes(sl.width);
     cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
     trace_begin(st);
-    gd_sweep_fwd_kernel<DK><<<dim3(static_cast<unsigned>(p.seqs.N) * p.seqs.H, slices), kThreads, smem, st>>>(p, maps, sw, ctl);
+    gd_sweep_fwd_kernel<DK><<<dim3(static_cast<unsigned>(p.seqs.N) * p.seqs.H, sl.n), kGdThreads, smem, st>>>(p, v, o, sl.width,
+                                                                                                            ctl);
     trace_end(st, "gd_sweep_fwd_kernel");
     count_launch();
     return check_launch("gd_sweep_fwd_kernel");
