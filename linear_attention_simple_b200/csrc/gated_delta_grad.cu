@@ -5,7 +5,8 @@
 //   A_ij = X_i . v'_j D_ij (i >= j)      B_ij = Y_i . v'_j D_ij (i > j)
 //   dq = A K + G X S^T
 //   dk = A^T Q + B^T K + B K + G Y S^T + R V' E^T
-//   da_t = sum over i >= t in the chunk of (o.dO - dv.y - dvs.z)_i + <E, S'>
+//   da_t = sum over i >= t of (o.dO - dv.y - dvs.z)_i up to the next <E, S'>
+//          (every 128 tokens), and that
 //
 // One CTA of 4 warps per (chunk, q/k head), 16 token rows to a warp; the
 // value heads that share the q/k head are summed in its accumulators.  A
@@ -173,9 +174,12 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
 
         // da and dbeta of this head: one warp, two tokens a lane
         if (w == (j & 3)) {
+            // <E, S'> is there after every second chunk and the last; before the
+            // others come the sums of the chunk in between
             const float* part = p.part + u * 3 * wtot * kGdC + 2 * lane;
+            const bool between = (c & 1) == 0 && (c + 1) * kGdC < len;
             float2 od = make_float2(0.f, 0.f), s1 = od, s2 = od;
-            float tail = 0.f;
+            float tail = 0.f, next = 0.f;
             for (int t = 0; t < wtot; ++t) {
                 const float2 a = *reinterpret_cast<const float2*>(part + t * kGdC);
                 const float2 b = *reinterpret_cast<const float2*>(part + (wtot + t) * kGdC);
@@ -183,9 +187,19 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
                 od.x += a.x; od.y += a.y;
                 s1.x += b.x; s1.y += b.y;
                 s2.x += e.x; s2.y += e.y;
-                const float2 an = *reinterpret_cast<const float2*>(p.anch + (u * wtot + t) * 2);
+                const int64_t un = between ? u + H : u;
+                const float2 an = *reinterpret_cast<const float2*>(p.anch + (un * wtot + t) * 2);
                 tail += an.x + an.y;
+                if (between) {
+                    const float* pn = part + static_cast<int64_t>(H) * 3 * wtot * kGdC;
+                    const float2 f = *reinterpret_cast<const float2*>(pn + t * kGdC);
+                    const float2 k = *reinterpret_cast<const float2*>(pn + (wtot + t) * kGdC);
+                    next += (f.x - k.x) + (f.y - k.y);
+                }
             }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) next += __shfl_xor_sync(0xFFFFFFFFu, next, o);
+            tail += next;
             const float d1 = od.y - s1.y;
             float s = (od.x - s1.x) + d1;          // sums over this lane's tokens and all later ones
 #pragma unroll

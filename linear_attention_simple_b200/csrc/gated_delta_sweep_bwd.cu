@@ -225,6 +225,18 @@ __device__ __forceinline__ void put16(uint32_t taddr, const float (&x)[16])
     for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i]);
     tmem_st16(taddr, w);
 }
+// This row's 32 tokens of a slice, zeros from `left` on (what lies there is
+// not the sequence's).  The loads do not wait for the comparison.
+__device__ __forceinline__ void load_rows(float (&f)[32], const __nv_bfloat16* s, int stride, int left)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = __bfloat162float(s[i * stride]);
+    if (left < 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = i < left ? f[i] : 0.f;
+    }
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // Arrive for this warp once its tensor-memory accesses are done.
 __device__ __forceinline__ void warp_done(uint64_t* bar, int lane)
 {
@@ -390,14 +402,10 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
             __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(x.slice(0, ph)) + half * 32 * x.rows + (warp & 3) * 32 + lane;
             const __nv_bfloat16* ds = reinterpret_cast<const __nv_bfloat16*>(x.slice(1, ph)) + (vs - reinterpret_cast<__nv_bfloat16*>(x.slice(0, ph)));
             const int left = x.len - c * kGdC - half * 32;
-            // while the first product runs: the state that enters the chunk
-            store_half_row<HS>(p.sb + (u * p.dv + r) * DK + half * HS, S);
-            if (c > 0) keep(p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32) + lane * 4);
             ok = warp_wait(&B.full[ph], (c >> 1) & 1, ctl);
             if (!ok) break;
             float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = i < left ? __bfloat162float(vs[i * x.rows]) : 0.f;
+            load_rows(v, vs, x.rows, left);
             ok = warp_wait(&B.y, ph, ctl);
             if (!ok) break;
             tc_fence_after();
@@ -415,6 +423,8 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
                 put_terms<2>(t0 + C::R + 16 * s, f);
             }
             warp_done(&B.r, lane);
+            // while the products run: the state that enters the chunk
+            store_half_row<HS>(p.sb + (u * p.dv + r) * DK + half * HS, S);
             ok = warp_wait(&B.z, ph, ctl);
             if (!ok) break;
             tc_fence_after();
@@ -455,8 +465,7 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
             warp_done(&B.w, lane);
             const float gl = sc[kScG * kGdC + kGdC - 1];
             float d[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) d[i] = i < left ? __bfloat162float(ds[i * x.rows]) : 0.f;
+            load_rows(d, ds, x.rows, left);
 #pragma unroll
             for (int i = 0; i < 32; ++i) vs[i * x.rows] = __float2bfloat16_rn(v[i]);
             fence_async_smem();
@@ -465,6 +474,7 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
                 mbar_arrive(&B.staged[ph]);
                 mbar_arrive(&B.empty[ph]);                   // scalars, V and dO are read
             }
+            if (c > 0 && (c & 1) == 0) keep(p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32) + lane * 4);
             ok = warp_wait(&B.ds, ph, ctl);
             if (!ok) break;
             tc_fence_after();
@@ -612,9 +622,8 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int t = 16 * b + 2 * j;
-                    const uint32_t lo = t < left ? __bfloat16_as_ushort(ds[t * x.rows]) : 0;
-                    const uint32_t hi = t + 1 < left ? __bfloat16_as_ushort(ds[(t + 1) * x.rows]) : 0;
-                    w[j] = lo | (hi << 16);
+                    const uint32_t lo = __bfloat16_as_ushort(ds[t * x.rows]), hi = __bfloat16_as_ushort(ds[(t + 1) * x.rows]);
+                    w[j] = (t < left ? lo : 0u) | (t + 1 < left ? hi << 16 : 0u);
                 }
                 tmem_st8(t0 + C::X + (i & 1) * 32 + half * 16 + 8 * b, w);
             }
@@ -635,9 +644,19 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             const __nv_bfloat16* ds = reinterpret_cast<const __nv_bfloat16*>(x.slice(1, ph)) + at;
             const int left = x.len - c * kGdC - half * 32;
             // while the first products run: <E, state leaving> (the sum of da's
-            // terms over all later tokens), E rounded, and y from the forward
+            // terms over all later tokens; after every second chunk), E rounded,
+            // and y from the forward; the next step's into L2
+            if (i + 1 < x.nc) {
+                const int64_t un = u - p.seqs.H;
+                const char* a = reinterpret_cast<const char*>(p.yn + ((un * nwr + wr) * 2 + half) * (32 * 32));
+                prefetch_l2(a + lane * 128);
+                if ((c & 1) == 0) {
+                    const char* b = reinterpret_cast<const char*>(p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32));
+                    for (int k = lane; k < HS; k += 32) prefetch_l2(b + k * 128);
+                }
+            }
             float dot = 0.f;
-            if (i > 0 || p.ds_final) {
+            if (i > 0 ? (c & 1) == 1 : p.ds_final != nullptr) {
                 const float* sn = (i > 0 ? p.sn + (((u + p.seqs.H) * nwr + wr) * 2 + half) * (HS * 32)
                                          : p.sn_last + ((x.nh * nwr + wr) * 2 + half) * (HS * 32)) + lane * 4;
 #pragma unroll
@@ -673,8 +692,10 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 put16(t0 + C::PO + 16 * s, f);
                 load16(q, sc + kScPd * kGdC + 16 * s);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    f[j] = 16 * b + j < left ? fmaf(g[j] * q[j], __bfloat162float(ds[(16 * b + j) * x.rows]), f[j]) : 0.f;
+                for (int j = 0; j < 16; ++j) {
+                    const float dO = __bfloat162float(ds[(16 * b + j) * x.rows]);
+                    f[j] = 16 * b + j < left ? fmaf(g[j] * q[j], dO, f[j]) : 0.f;
+                }
                 put_terms<2>(t0 + C::Y + 16 * s, f);
             }
             warp_done(&B.r, lane);
@@ -700,14 +721,15 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                     const bool in = t < left;
                     const float4 y4 = yn[t >> 2];
                     const float y = (t & 3) == 0 ? y4.x : (t & 3) == 1 ? y4.y : (t & 3) == 2 ? y4.z : y4.w;
-                    const float z = in ? __bfloat162float(vs[t * x.rows]) - y : 0.f;
-                    const float dO = in ? __bfloat162float(ds[t * x.rows]) : 0.f;
+                    const float v = __bfloat162float(vs[t * x.rows]), d = __bfloat162float(ds[t * x.rows]);
+                    const float z = in ? v - y : 0.f, dO = in ? d : 0.f;
                     const float full = fmaf(g[j] * q[j], dO, f[j]);
                     s1[t] = fmaf(full, y, f[j] * z);
                     s2[t] = full * z;
                     f[j] = full;
-                    if (in) vs[t * x.rows] = __float2bfloat16_rn(full);
                 }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) vs[(16 * b + j) * x.rows] = __float2bfloat16_rn(f[j]);
                 load16(g, sc + kScG * kGdC + 16 * s);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) f[j] *= -g[j];
