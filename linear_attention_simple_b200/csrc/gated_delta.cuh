@@ -162,8 +162,10 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 //           (k 0-7, k 8-15), r2, r3 of n 8-15.
 //   rows_k: the same from a tile stored [k][n], with ldsm4_t.
 //   rows_a: a left operand of 16 rows from a tile stored [m][k].
+//   rows_at: the same from a tile stored [k][m], with ldsm4_t.
 __device__ __forceinline__ int rows_n(int lane, int ld) { return ((lane & 7) + ((lane >> 4) << 3)) * ld + (((lane >> 3) & 1) << 3); }
 __device__ __forceinline__ int rows_k(int lane, int ld) { return ((lane & 7) + (((lane >> 3) & 1) << 3)) * ld + ((lane >> 4) << 3); }
+__device__ __forceinline__ int rows_at(int lane, int ld) { return ((lane & 7) + ((lane >> 4) << 3)) * ld + (((lane >> 3) & 1) << 3); }
 __device__ __forceinline__ int rows_a(int lane, int ld) { return (lane & 15) * ld + ((lane >> 4) << 3); }
 
 // 2^x for the decay factors: x <= 0 here (0 -> 1, very negative -> 0).

@@ -10,14 +10,16 @@
 //
 // One CTA of 4 warps per (chunk, q/k head), 16 token rows to a warp; the
 // value heads that share the q/k head are summed in its accumulators.  A
-// first pass over dv (32 columns a stage, two stages) gives A, A^T, B and
-// B^T, each warp its own rows, the tiles on the masked side left out; they
-// become left operands in place (bf16) and multiply K and Q; a second pass
-// adds the three products with the states.  Both transposes are computed
-// rather than exchanged: 64 x 64 tiles over dv cost less than a trip through
-// shared memory.  dq and dk leave in bf16, so every operand is one bf16
-// rounding of its value; the sums behind da and dbeta come in fp32 from the
-// sweeps.
+// first pass over dv (32 columns a stage, two stages) gives A and B, each warp
+// its own rows, the tiles above the diagonal left out; they are rounded to
+// bf16, multiply K from the registers and, from shared memory, transposed, Q
+// and K; a second pass adds the three products with the states.  dq and dk
+// leave in bf16, so every operand is one bf16 rounding of its value; the sums
+// behind da and dbeta come in fp32 from the sweeps.
+//
+// Latency bounds it (three CTAs an SM, 12 warps): where a value head has a
+// q/k head of its own (ONE), the accumulators of dq and dk start only after
+// the first pass, which leaves 168 registers a thread enough.
 #include "gated_delta.cuh"
 
 namespace gla {
@@ -32,8 +34,13 @@ struct GradSmem {
     static constexpr int KS = DK + kGdPad;
     static constexpr int tok = kGdC * kVs;             // one staged token slice
     static constexpr int st = kSl * KS;                // one staged state slice
-    static constexpr int stage = 3 * tok + 2 * st;
-    static constexpr int bytes = (2 * kGdC * KS + 2 * stage) * 2 + kGdSc * kGdC * 4;
+    static constexpr int stage1 = 3 * tok, stage2 = 3 * tok + 2 * st;
+    // elements: the first pass's stages, later A and B; then K and Q; the
+    // second pass's stages over all of them
+    static constexpr int ab = kGdC * (kGdC + kGdPad);
+    static constexpr int kq = 2 * stage1;
+    static constexpr int all = kq + 2 * kGdC * KS > 2 * stage2 ? kq + 2 * kGdC * KS : 2 * stage2;
+    static constexpr int bytes = all * 2 + kGdSc * kGdC * 4;
 };
 
 struct Src {
@@ -61,14 +68,6 @@ __device__ __forceinline__ void load_slice(__nv_bfloat16* st, const Src& x, int 
     }
 }
 
-// The left operand of two neighbouring accumulator tiles, rounded to bf16.
-__device__ __forceinline__ void to_a(uint32_t (&r)[4], const float (&a)[4], const float (&b)[4])
-{
-    r[0] = pack_bf16(a[0], a[1]);
-    r[1] = pack_bf16(a[2], a[3]);
-    r[2] = pack_bf16(b[0], b[1]);
-    r[3] = pack_bf16(b[2], b[3]);
-}
 // A left operand's rows g and g + 8 times f0 and f1.
 __device__ __forceinline__ void scale_a(uint32_t (&r)[4], float f0, float f1)
 {
@@ -79,16 +78,17 @@ __device__ __forceinline__ void scale_a(uint32_t (&r)[4], float f0, float f1)
     }
 }
 
-template <int DK>
-__global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
+template <int DK, bool ONE>
+__global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams p)
 {
     using M = GradSmem<DK>;
     constexpr int KS = M::KS, NT = DK / 8;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    __nv_bfloat16* sk = reinterpret_cast<__nv_bfloat16*>(smem_raw);
+    constexpr int AS = kGdC + kGdPad;                      // row stride of A and B
+    __nv_bfloat16* sst = reinterpret_cast<__nv_bfloat16*>(smem_raw);
+    __nv_bfloat16* sk = sst + M::kq;
     __nv_bfloat16* sq = sk + kGdC * KS;
-    __nv_bfloat16* sst = sq + kGdC * KS;
-    float* sc = reinterpret_cast<float*>(sst + 2 * M::stage);
+    float* sc = reinterpret_cast<float*>(sst + M::all);
 
     const int64_t slot = blockIdx.x;
     const int hk = blockIdx.y;
@@ -105,16 +105,15 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, c2 = (lane & 3) * 2;
     const int nst = p.dv / kSl, wtot = p.dv >> 5;
 
-    gd_load_rows(sk, KS, p.k + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
-    gd_load_rows(sq, KS, p.q + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
-
     float dq[NT][4], dk[NT][4];
+    if (!ONE) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dq[t][e] = dk[t][e] = 0.f;
+            for (int e = 0; e < 4; ++e) dq[t][e] = dk[t][e] = 0.f;
+    }
 
-    for (int j = 0; j < group; ++j) {
+    for (int j = 0; j < (ONE ? 1 : group); ++j) {
         const int h = hk * group + j;
         const int64_t u = slot * H + h;
         Src x{p.dO + row * p.ld_do + static_cast<int64_t>(h) * p.dv, p.dvv + row * H * p.dv + static_cast<int64_t>(h) * p.dv,
@@ -124,53 +123,43 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
         const float* src_sc = reinterpret_cast<const float*>(p.rec + u * GdRec<DK, true>::BYTES + GdRec<DK, true>::SC);
         for (int i = tid; i < kGdSc * kGdC; i += kThreads) sc[i] = src_sc[i];
         load_slice<DK>(sst, x, 0, false, tid);
+        gd_load_rows(sk, KS, p.k + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
+        gd_load_rows(sq, KS, p.q + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
         cp_async_commit();
 
-        // pass 1: products over dv of 16 rows with the 64 tokens, before the masks
-        float fa[8][4], fat[8][4], fb[8][4], fbt[8][4];
+        // pass 1: products over dv of 16 rows with the tokens up to them, before the masks
+        float fa[8][4], fb[8][4];
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) fa[t][e] = fat[t][e] = fb[t][e] = fbt[t][e] = 0.f;
+            for (int e = 0; e < 4; ++e) fa[t][e] = fb[t][e] = 0.f;
         for (int i = 0; i < nst; ++i) {
             cp_async_wait<0>();
             __syncthreads();
-            if (i + 1 < nst) load_slice<DK>(sst + ((i + 1) & 1) * M::stage, x, (i + 1) * kSl, false, tid);
+            if (i + 1 < nst) load_slice<DK>(sst + ((i + 1) & 1) * M::stage1, x, (i + 1) * kSl, false, tid);
             cp_async_commit();
-            const __nv_bfloat16* st = sst + (i & 1) * M::stage;
+            const __nv_bfloat16* st = sst + (i & 1) * M::stage1;
             const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
-            const uint32_t br = smem_u32(st + rows_n(lane, kVs));
+            const uint32_t br = smem_u32(st + 2 * M::tok + rows_n(lane, kVs));
             constexpr int tk = M::tok * 2, rp = 16 * kVs * 2;
 #pragma unroll
             for (int s = 0; s < kSl / 16; ++s) {
-                uint32_t d[4], y[4], v[4];
+                uint32_t d[4], y[4];
                 ldsm4(d, ar + s * 32);
                 ldsm4(y, ar + tk + s * 32);
-                ldsm4(v, ar + 2 * tk + s * 32);
 #pragma unroll
                 for (int np = 0; np < 4; ++np) {
+                    if (np > w) continue;
                     uint32_t b[4];
-                    if (np <= w) {
-                        ldsm4(b, br + 2 * tk + np * rp + s * 32);
-                        mma_bf16(fa[2 * np], d, b[0], b[1]);
-                        mma_bf16(fa[2 * np + 1], d, b[2], b[3]);
-                        mma_bf16(fb[2 * np], y, b[0], b[1]);
-                        mma_bf16(fb[2 * np + 1], y, b[2], b[3]);
-                    }
-                    if (np >= w) {
-                        ldsm4(b, br + np * rp + s * 32);
-                        mma_bf16(fat[2 * np], v, b[0], b[1]);
-                        mma_bf16(fat[2 * np + 1], v, b[2], b[3]);
-                        ldsm4(b, br + tk + np * rp + s * 32);
-                        mma_bf16(fbt[2 * np], v, b[0], b[1]);
-                        mma_bf16(fbt[2 * np + 1], v, b[2], b[3]);
-                    }
+                    ldsm4(b, br + np * rp + s * 32);
+                    mma_bf16(fa[2 * np], d, b[0], b[1]);
+                    mma_bf16(fa[2 * np + 1], d, b[2], b[3]);
+                    mma_bf16(fb[2 * np], y, b[0], b[1]);
+                    mma_bf16(fb[2 * np + 1], y, b[2], b[3]);
                 }
             }
         }
         __syncthreads();                   // both stages are read
-        load_slice<DK>(sst, x, 0, true, tid);
-        cp_async_commit();
 
         // da and dbeta of this head: one warp, two tokens a lane
         if (w == (j & 3)) {
@@ -220,64 +209,91 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
             }
         }
 
-        // masks and decays; A and B by rows i = this warp's, A^T and B^T by rows j
-        const float bh0 = sc[kScBh * kGdC + 16 * w + g], bl0 = sc[kScBl * kGdC + 16 * w + g];
-        const float bh1 = sc[kScBh * kGdC + 16 * w + g + 8], bl1 = sc[kScBl * kGdC + 16 * w + g + 8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 16 * w + g + 8 * (e >> 1), q = 8 * t + c2 + (e & 1);
-                const float diff = ((e >> 1 ? bh1 : bh0) - sc[kScBh * kGdC + q]) + ((e >> 1 ? bl1 : bl0) - sc[kScBl * kGdC + q]);
-                const float d = gd_exp2(-fabsf(diff));          // D between the earlier and the later token
-                const float ds = d * p.scale;
-                fa[t][e] = q <= r ? fa[t][e] * ds : 0.f;
-                fb[t][e] = q < r ? -fb[t][e] * d : 0.f;
-                fat[t][e] = q >= r ? fat[t][e] * ds : 0.f;
-                fbt[t][e] = q > r ? -fbt[t][e] * d : 0.f;
-            }
-        }
-        // dq += A K; dk += A^T Q + (B + B^T) K: B + B^T has one rounding, both halves in place
+        // masks and decays; A and B as left operands, and to shared memory
+        uint32_t pa[4][4], pb[4][4];
         {
-            const uint32_t kt = smem_u32(sk + rows_k(lane, KS)), qt = smem_u32(sq + rows_k(lane, KS));
+            const float bh0 = sc[kScBh * kGdC + 16 * w + g], bl0 = sc[kScBl * kGdC + 16 * w + g];
+            const float bh1 = sc[kScBh * kGdC + 16 * w + g + 8], bl1 = sc[kScBl * kGdC + 16 * w + g + 8];
+            uint32_t* sa = reinterpret_cast<uint32_t*>(sst + (16 * w + g) * AS + c2);
+            uint32_t* sb = reinterpret_cast<uint32_t*>(sst + M::ab + (16 * w + g) * AS + c2);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                uint32_t a[4], at[4], bb[4];
-                to_a(a, fa[2 * s], fa[2 * s + 1]);
-                to_a(at, fat[2 * s], fat[2 * s + 1]);
+            for (int t = 0; t < 8; ++t) {
+                if ((t >> 1) > w) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) pa[t >> 1][2 * (t & 1) + e] = pb[t >> 1][2 * (t & 1) + e] = 0u;
+                    continue;
+                }
+                const float2 qh = *reinterpret_cast<const float2*>(sc + kScBh * kGdC + 8 * t + c2);
+                const float2 ql = *reinterpret_cast<const float2*>(sc + kScBl * kGdC + 8 * t + c2);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    fb[2 * s][e] += fbt[2 * s][e];
-                    fb[2 * s + 1][e] += fbt[2 * s + 1][e];
+                    const int r = 16 * w + g + 8 * (e >> 1), q = 8 * t + c2 + (e & 1);
+                    const float diff = ((e >> 1 ? bh1 : bh0) - (e & 1 ? qh.y : qh.x)) + ((e >> 1 ? bl1 : bl0) - (e & 1 ? ql.y : ql.x));
+                    const float d = q <= r ? gd_exp2(diff) : 0.f;
+                    fa[t][e] *= d * p.scale;
+                    fb[t][e] = q < r ? -fb[t][e] * d : 0.f;
                 }
-                to_a(bb, fb[2 * s], fb[2 * s + 1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t a = pack_bf16(fa[t][2 * e], fa[t][2 * e + 1]), b = pack_bf16(fb[t][2 * e], fb[t][2 * e + 1]);
+                    pa[t >> 1][2 * (t & 1) + e] = a;
+                    pb[t >> 1][2 * (t & 1) + e] = b;
+                    sa[(8 * e * AS + 8 * t) / 2] = a;
+                    sb[(8 * e * AS + 8 * t) / 2] = b;
+                }
+            }
+        }
+        __syncthreads();
+        // dq += A K; dk += A^T Q + B K + B^T K
+        {
+            if (ONE) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dq[t][e] = dk[t][e] = 0.f;
+            }
+            const uint32_t kt = smem_u32(sk + rows_k(lane, KS)), qt = smem_u32(sq + rows_k(lane, KS));
+            const uint32_t ta = smem_u32(sst + 16 * w + rows_at(lane, AS)), tb = ta + M::ab * 2;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                uint32_t at[4], bt[4];
+                if (s >= w) {
+                    ldsm4_t(at, ta + s * 16 * AS * 2);
+                    ldsm4_t(bt, tb + s * 16 * AS * 2);
+                }
 #pragma unroll
                 for (int np = 0; np < DK / 16; ++np) {
                     uint32_t kf[4], qf[4];
                     ldsm4_t(kf, kt + s * 16 * KS * 2 + np * 32);
                     if (s <= w) {
-                        mma_bf16(dq[2 * np], a, kf[0], kf[1]);
-                        mma_bf16(dq[2 * np + 1], a, kf[2], kf[3]);
+                        mma_bf16(dq[2 * np], pa[s], kf[0], kf[1]);
+                        mma_bf16(dq[2 * np + 1], pa[s], kf[2], kf[3]);
+                        mma_bf16(dk[2 * np], pb[s], kf[0], kf[1]);
+                        mma_bf16(dk[2 * np + 1], pb[s], kf[2], kf[3]);
                     }
-                    mma_bf16(dk[2 * np], bb, kf[0], kf[1]);
-                    mma_bf16(dk[2 * np + 1], bb, kf[2], kf[3]);
                     if (s >= w) {
                         ldsm4_t(qf, qt + s * 16 * KS * 2 + np * 32);
+                        mma_bf16(dk[2 * np], bt, kf[0], kf[1]);
+                        mma_bf16(dk[2 * np + 1], bt, kf[2], kf[3]);
                         mma_bf16(dk[2 * np], at, qf[0], qf[1]);
                         mma_bf16(dk[2 * np + 1], at, qf[2], qf[3]);
                     }
                 }
             }
         }
+        __syncthreads();                   // K, Q, A and B are read
+        load_slice<DK>(sst, x, 0, true, tid);
+        cp_async_commit();
+
         // pass 2: dq += G X S^T, dk += G Y S^T + R V' E^T
         const float G0 = sc[kScG * kGdC + 16 * w + g], G1 = sc[kScG * kGdC + 16 * w + g + 8];
         const float R0 = sc[kScR * kGdC + 16 * w + g], R1 = sc[kScR * kGdC + 16 * w + g + 8];
         for (int i = 0; i < nst; ++i) {
             cp_async_wait<0>();
             __syncthreads();
-            if (i + 1 < nst) load_slice<DK>(sst + ((i + 1) & 1) * M::stage, x, (i + 1) * kSl, true, tid);
+            if (i + 1 < nst) load_slice<DK>(sst + ((i + 1) & 1) * M::stage2, x, (i + 1) * kSl, true, tid);
             cp_async_commit();
-            const __nv_bfloat16* st = sst + (i & 1) * M::stage;
+            const __nv_bfloat16* st = sst + (i & 1) * M::stage2;
             const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
             const uint32_t sr = smem_u32(st + 3 * M::tok + rows_k(lane, KS));
             constexpr int tk = M::tok * 2;
@@ -327,17 +343,23 @@ __global__ void __launch_bounds__(kThreads, 2) gd_grad_kernel(GdParams p)
     }
 }
 
-template <int DK>
+template <int DK, bool ONE>
 gla_status launch(const GdParams& p, cudaStream_t st)
 {
     constexpr int smem = GradSmem<DK>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(gd_grad_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(gd_grad_kernel<DK, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
     trace_begin(st);
-    gd_grad_kernel<DK><<<dim3(static_cast<unsigned>(p.slots), static_cast<unsigned>(p.seqs.Hk)), kThreads, smem, st>>>(p);
+    gd_grad_kernel<DK, ONE><<<dim3(static_cast<unsigned>(p.slots), static_cast<unsigned>(p.seqs.Hk)), kThreads, smem, st>>>(p);
     trace_end(st, "gd_grad_kernel");
     count_launch();
     return check_launch("gd_grad_kernel");
+}
+
+template <int DK>
+gla_status pick(const GdParams& p, cudaStream_t st)
+{
+    return p.seqs.H == p.seqs.Hk ? launch<DK, true>(p, st) : launch<DK, false>(p, st);
 }
 
 }  // namespace
@@ -346,9 +368,9 @@ gla_status gd_launch_grad(const GdParams& p, cudaStream_t st)
 {
     if (p.slots == 0) return GLA_OK;
     switch (p.dk) {
-    case 64: return launch<64>(p, st);
-    case 96: return launch<96>(p, st);
-    default: return launch<128>(p, st);
+    case 64: return pick<64>(p, st);
+    case 96: return pick<96>(p, st);
+    default: return pick<128>(p, st);
     }
 }
 

@@ -37,7 +37,7 @@ gla_status gd_check(int N, int T, int Hk, int H, int dk, int dv, int64_t ld_qkv,
     if (!(scale > 0.f) || !std::isfinite(scale)) return GLA_ERR_INVALID_ARG;
     if (H > 0 && (Hk == 0 || H % Hk != 0)) return GLA_ERR_INVALID_ARG;
     if (!gd_dims_ok(dk, dv)) return GLA_ERR_UNSUPPORTED;
-    if (H > 65535 || static_cast<int64_t>(N) * H > 0x7FFFFFFF) return GLA_ERR_UNSUPPORTED;
+    if (H > 65535 || static_cast<int64_t>(N) * H > 0x3FFFFFFF) return GLA_ERR_UNSUPPORTED;
     const int64_t pq = static_cast<int64_t>(Hk) * dk, pv = static_cast<int64_t>(H) * dv;
     if (ld_qkv == 0) {
         *ld_qk = pq;

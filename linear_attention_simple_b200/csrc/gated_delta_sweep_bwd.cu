@@ -79,11 +79,13 @@ struct Cta {
 };
 
 template <int DK>
-__device__ __forceinline__ bool setup(Cta& x, Bars& B, const GdParams& p, int sw, unsigned char* raw)
+__device__ __forceinline__ bool setup(Cta& x, Bars& B, const GdParams& p, int sw, int nslices, unsigned char* raw)
 {
     using Rec = GdRec<DK, true>;
-    x.n = blockIdx.x / p.seqs.H;
-    x.h = blockIdx.x - x.n * p.seqs.H;
+    // the slices of a (sequence, head) side by side, so that they share its records in L2
+    const int pair = blockIdx.x / nslices;
+    x.n = pair / p.seqs.H;
+    x.h = pair - x.n * p.seqs.H;
     p.seqs.span(x.n, x.row0, x.len);
     if (x.len < 0) {
         if (threadIdx.x == 0) record_status(p.status, GLA_ERR_INVALID_ARG);
@@ -92,7 +94,7 @@ __device__ __forceinline__ bool setup(Cta& x, Bars& B, const GdParams& p, int sw
     x.smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     x.slices = x.smem + Smem<DK>::V;
     x.sw = sw;
-    x.w0 = blockIdx.y * sw;
+    x.w0 = (blockIdx.x - pair * nslices) * sw;
     x.rows = min(sw, p.dv - x.w0);
     x.nc = (x.len + kGdC - 1) / kGdC;
     x.nh = static_cast<int64_t>(x.n) * p.seqs.H + x.h;
@@ -277,7 +279,7 @@ __device__ __forceinline__ void store_half_row(__nv_bfloat16* dst, const float (
 template <int DK>
 __global__ void __launch_bounds__(kGdThreads, 1)
 gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __grid_constant__ GdMap map_d,
-                     const __grid_constant__ GdMap map_vp, int sw, WaitCtl ctl)
+                     const __grid_constant__ GdMap map_vp, int sw, int nslices, WaitCtl ctl)
 {
     using C = FwdCols<DK>;
     using M = Smem<DK>;
@@ -285,7 +287,7 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Bars B;
     Cta x;
-    if (!setup<DK>(x, B, p, sw, smem_raw)) return;
+    if (!setup<DK>(x, B, p, sw, nslices, smem_raw)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t tm = B.tmem;
 
@@ -515,7 +517,7 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
 template <int DK>
 __global__ void __launch_bounds__(kGdThreads, 1)
 gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __grid_constant__ GdMap map_d,
-                    const __grid_constant__ GdMap map_dv, int sw, WaitCtl ctl)
+                    const __grid_constant__ GdMap map_dv, int sw, int nslices, WaitCtl ctl)
 {
     using C = RevCols<DK>;
     using M = Smem<DK>;
@@ -523,7 +525,7 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Bars B;
     Cta x;
-    if (!setup<DK>(x, B, p, sw, smem_raw)) return;
+    if (!setup<DK>(x, B, p, sw, nslices, smem_raw)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t tm = B.tmem;
 
@@ -779,7 +781,7 @@ gla_status start(K kernel, const char* name, const GdParams& p, int smem, const 
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
     trace_begin(st);
-    kernel<<<dim3(static_cast<unsigned>(p.seqs.N) * p.seqs.H, sl.n), kGdThreads, smem, st>>>(p, v, d, o, sl.width, ctl);
+    kernel<<<static_cast<unsigned>(p.seqs.N) * p.seqs.H * sl.n, kGdThreads, smem, st>>>(p, v, d, o, sl.width, sl.n, ctl);
     trace_end(st, name);
     count_launch();
     return check_launch(name);

@@ -59,7 +59,7 @@ struct Smem {
 
 template <int DK>
 __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v,
-                                                                                  const __grid_constant__ GdMap map_o, int sw, WaitCtl ctl)
+                                                                                  const __grid_constant__ GdMap map_o, int sw, int nslices, WaitCtl ctl)
 {
     using C = Cols<DK>;
     using M = Smem<DK>;
@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars B;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n = blockIdx.x / p.seqs.H, h = blockIdx.x - n * p.seqs.H;
+    // the slices of a (sequence, head) side by side, so that they share its records in L2
+    const int pair = blockIdx.x / nslices, n = pair / p.seqs.H, h = pair - n * p.seqs.H;
     int64_t row0;
     int len;
     p.seqs.span(n, row0, len);
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
         if (tid == 0) record_status(p.status, GLA_ERR_INVALID_ARG);
         return;
     }
-    const int w0 = blockIdx.y * sw, rows = min(sw, p.dv - w0);      // this CTA's dv rows
+    const int w0 = (blockIdx.x - pair * nslices) * sw, rows = min(sw, p.dv - w0);      // this CTA's dv rows
     const int nc = (len + kGdC - 1) / kGdC;
     const unsigned char* rec = p.rec + (p.seqs.slot0(n, row0) * p.seqs.H + h) * Rec::BYTES;
     const int64_t rec_step = static_cast<int64_t>(p.seqs.H) * Rec::BYTES;
@@ -384,8 +385,8 @@ gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
     cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
     trace_begin(st);
-    gd_sweep_fwd_kernel<DK><<<dim3(static_cast<unsigned>(p.seqs.N) * p.seqs.H, sl.n), kGdThreads, smem, st>>>(p, v, o, sl.width,
-                                                                                                            ctl);
+    gd_sweep_fwd_kernel<DK><<<static_cast<unsigned>(p.seqs.N) * p.seqs.H * sl.n, kGdThreads, smem, st>>>(p, v, o, sl.width, sl.n,
+                                                                                                       ctl);
     trace_end(st, "gd_sweep_fwd_kernel");
     count_launch();
     return check_launch("gd_sweep_fwd_kernel");
