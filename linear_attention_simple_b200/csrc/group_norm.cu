@@ -15,7 +15,7 @@
 // sums are a few shuffles, every row is read once and no lane idles (d = 192:
 // 8 lanes of 3 vectors).  The forward walks neighbouring groups of a row with
 // neighbouring lanes and loads its next row while it works on this one.  In
-// the backward a CTA stays with one group: weight and bias sit in shared
+// the backward a CTA stays with its groups: weight and bias sit in shared
 // memory, the sums over rows in registers until they are added up within the
 // CTA, and one partial row per CTA goes to the workspace; a second kernel adds
 // those in a fixed order.
@@ -27,7 +27,9 @@ namespace gla {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBwdThreads = 128;
 constexpr int kSms = 148;
+constexpr int bwd_ctas(int nv) { return nv > 2 ? 3 : 4; }      // of an SM, all resident
 
 struct NormParams {
     const void* x;
@@ -36,7 +38,7 @@ struct NormParams {
     __nv_bfloat16* y;
     void* dx;
     __nv_bfloat16* dgate;
-    float* part;                           // [CTAs of a group][2][G d]
+    float* part;                           // [CTAs of a block of groups][2][G d]
     int64_t ld_x, ld_gate;
     int M, G, d, shared_w, center, act, walkers;
     float eps;
@@ -50,14 +52,11 @@ struct Raw<__nv_bfloat16> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&f)[8]) const
+    __device__ __forceinline__ void get(f2 (&f)[4]) const
     {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = bf16_lo(w[i]);
-            f[2 * i + 1] = bf16_hi(w[i]);
-        }
+        for (int i = 0; i < 4; ++i) f[i] = f2_from_bf16x2(w[i]);
     }
 };
 template <>
@@ -69,80 +68,91 @@ struct Raw<float> {
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&f)[8]) const
+    __device__ __forceinline__ void get(f2 (&f)[4]) const
     {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        f[0] = f2_make(a.x, a.y);
+        f[1] = f2_make(a.z, a.w);
+        f[2] = f2_make(b.x, b.y);
+        f[3] = f2_make(b.z, b.w);
     }
 };
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8])
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const f2 (&f)[4])
 {
     *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        make_uint4(f2_to_bf16x2(f[0]), f2_to_bf16x2(f[1]), f2_to_bf16x2(f[2]), f2_to_bf16x2(f[3]));
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8])
+__device__ __forceinline__ void store8(float* p, const f2 (&f)[4])
 {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 a = f2_get(f[2 * i]), b = f2_get(f[2 * i + 1]);
+        reinterpret_cast<float4*>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
+    }
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ float lanes_sum(float v, int lanes)
 {
     for (int o = lanes >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-// The fast exponential and quotient are good to a few 2^-22 here, far below
-// the bf16 rounding of y and the fp32 sums; 1 + e^-z past 2^126 gives 0.
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// Sigmoids of a pair, by the hardware's exponential and reciprocal: good to a
+// few 2^-22, far below the bf16 rounding of y and the sums' own; e^-z past the
+// largest fp32 gives 0.
+__device__ __forceinline__ f2 sigmoid2(f2 z)
+{
+    const float2 t = f2_get(f2_mul(z, f2_splat(-1.4426950408889634f)));
+    float a, b;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(t.y));
+    const float2 u = f2_get(f2_add(f2_make(a, b), f2_splat(1.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(u.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(u.y));
+    return f2_make(a, b);
+}
 
 // x^ in place of x (zeros behind d), and rstd of the group.
 template <int NV>
-__device__ __forceinline__ float normalise(float (&x)[NV][8], int lane, int lanes, const NormParams& p)
+__device__ __forceinline__ float normalise(f2 (&x)[NV][4], int lane, int lanes, const NormParams& p)
 {
     const float inv = 1.f / static_cast<float>(p.d);
     if (p.center) {
-        float sum = 0.f;
+        f2 sum = f2_splat(0.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum += x[j][e];
-        const float mean = lanes_sum(sum, lanes) * inv;
+            for (int e = 0; e < 4; ++e) sum = f2_add(sum, x[j][e]);
+        const float2 t = f2_get(sum);
+        const float mean = lanes_sum(t.x + t.y, lanes) * inv;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const float m = (j * lanes + lane) * 8 < p.d ? mean : 0.f;
+            const f2 m = f2_splat((j * lanes + lane) * 8 < p.d ? mean : 0.f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[j][e] -= m;
+            for (int e = 0; e < 4; ++e) x[j][e] = f2_sub(x[j][e], m);
         }
     }
-    float sq = 0.f;
+    f2 sq = f2_splat(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq = fmaf(x[j][e], x[j][e], sq);
-    const float rstd = rsqrtf(lanes_sum(sq, lanes) * inv + p.eps);
+        for (int e = 0; e < 4; ++e) sq = f2_fma(x[j][e], x[j][e], sq);
+    const float2 t = f2_get(sq);
+    const float rstd = rsqrtf(lanes_sum(t.x + t.y, lanes) * inv + p.eps);
+    const f2 rs = f2_splat(rstd);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[j][e] *= rstd;
+        for (int e = 0; e < 4; ++e) x[j][e] = f2_mul(x[j][e], rs);
     return rstd;
 }
 
 template <int NV, class T, bool GATE>
-__global__ void __launch_bounds__(kThreads) group_norm_silu_kernel(NormParams p, int lanes)
+__global__ void __launch_bounds__(kThreads, NV > 2 ? 2 : 3) group_norm_silu_kernel(NormParams p, int lanes)
 {
     const int64_t seat = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / lanes;
     const int lane = threadIdx.x & (lanes - 1), g = static_cast<int>(seat % p.G);
     const int64_t walker = seat / p.G;
     const int c0 = lane * 8, cstep = lanes * 8;
-    float w[NV][8], b[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = c0 + j * cstep, at = (p.shared_w ? 0 : g * p.d) + c;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[j][e] = p.weight && c < p.d ? p.weight[at + e] : 1.f;
-            b[j][e] = p.bias && c < p.d ? p.bias[at + e] : 0.f;
-        }
-    }
+    const int at = (p.shared_w ? 0 : g * p.d) + c0;
     const T* px = static_cast<const T*>(p.x) + g * p.d + c0;
     const __nv_bfloat16* pg = p.gate + g * p.d + c0;
     Raw<T> rx[NV];
@@ -164,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) group_norm_silu_kernel(NormParams p,
     for (int64_t r0 = 0; r0 < p.M; r0 += p.walkers) {
         const int64_t r = r0 + walker;
         const bool on = walker < p.walkers && r < p.M;
-        float f[NV][8], z[NV][8];
+        f2 f[NV][4], z[NV][4];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             rx[j].get(f[j]);
@@ -176,12 +186,30 @@ __global__ void __launch_bounds__(kThreads) group_norm_silu_kernel(NormParams p,
         for (int j = 0; j < NV; ++j) {
             const int c = c0 + j * cstep;
             if (!on || c >= p.d) continue;
+            // weight and bias stay in L1: held in registers they cost half of the warps
+            if (p.weight) {
+                Raw<float> t;
+                f2 w[4];
+                t.load(p.weight + at + j * cstep);
+                t.get(w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float n = fmaf(f[j][e], w[j][e], b[j][e]);
-                const float a = GATE ? z[j][e] : n;
-                const float s = p.act ? a * sigmoid_f(a) : a;
-                f[j][e] = GATE ? n * s : s;
+                for (int e = 0; e < 4; ++e) f[j][e] = f2_mul(f[j][e], w[e]);
+            }
+            if (p.bias) {
+                Raw<float> t;
+                f2 b[4];
+                t.load(p.bias + at + j * cstep);
+                t.get(b);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[j][e] = f2_add(f[j][e], b[e]);
+            }
+            if (GATE) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[j][e] = f2_mul(f[j][e], z[j][e]);
+            }
+            if (p.act) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[j][e] = f2_mul(f[j][e], sigmoid2(GATE ? z[j][e] : f[j][e]));
             }
             store8(p.y + (r * p.G + g) * p.d + c, f[j]);
         }
@@ -189,30 +217,35 @@ __global__ void __launch_bounds__(kThreads) group_norm_silu_kernel(NormParams p,
 }
 
 template <int NV, class T, bool GATE>
-__global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : 2) group_norm_silu_bwd_kernel(NormParams p, int lanes)
+__global__ void __launch_bounds__(kBwdThreads, bwd_ctas(NV)) group_norm_silu_bwd_kernel(NormParams p, int lanes)
 {
-    extern __shared__ __align__(16) float smem[];          // weight, bias [2][d]; later the warps' sums [8][2][d]
-    const int lane = threadIdx.x & (lanes - 1), g = blockIdx.x % p.G;
-    const int64_t walker = static_cast<int64_t>(blockIdx.x / p.G) * (kThreads / lanes) + threadIdx.x / lanes;
+    extern __shared__ __align__(16) float smem[];          // weight, bias [S][2][d]; later the warps' sums [4][S][2][d]
+    // a warp has S neighbouring groups of one row, a CTA the same groups of its warps' rows
+    const int S = 32 / lanes, blocks = (p.G + S - 1) / S, g0 = (blockIdx.x % blocks) * S;
+    const int lane = threadIdx.x & (lanes - 1), seat = (threadIdx.x & 31) / lanes, g = g0 + seat;
+    const int64_t walker = static_cast<int64_t>(blockIdx.x / blocks) * (kBwdThreads / 32) + (threadIdx.x >> 5);
     const int c0 = lane * 8, cstep = lanes * 8;
-    for (int i = threadIdx.x; i < p.d; i += kThreads) {
-        const int at = (p.shared_w ? 0 : g * p.d) + i;
-        smem[i] = p.weight ? p.weight[at] : 1.f;
-        smem[p.d + i] = p.bias ? p.bias[at] : 0.f;
-    }
+    for (int k = 0; k < S; ++k)
+        for (int i = threadIdx.x; i < p.d; i += kBwdThreads) {
+            const int at = (p.shared_w ? 0 : (g0 + k) * p.d) + i;
+            const bool in = g0 + k < p.G;
+            smem[k * 2 * p.d + i] = p.weight && in ? p.weight[at] : 1.f;
+            smem[k * 2 * p.d + p.d + i] = p.bias && in ? p.bias[at] : 0.f;
+        }
     __syncthreads();
-    float sw[NV][8], sb[NV][8];
+    const float* params = smem + seat * 2 * p.d;
+    f2 sw[NV][4], sb[NV][4];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sw[j][e] = sb[j][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sw[j][e] = sb[j][e] = f2_splat(0.f);
     const T* px = static_cast<const T*>(p.x) + g * p.d + c0;
     const __nv_bfloat16* pg = p.gate + g * p.d + c0;
     const float inv = 1.f / static_cast<float>(p.d);
     Raw<T> rx[NV];
     Raw<__nv_bfloat16> rz[NV], rd[NV];
     auto fetch = [&](int64_t r) {
-        const bool on = r < p.M;
+        const bool on = g < p.G && r < p.M;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             rx[j].zero();
@@ -225,91 +258,105 @@ __global__ void __launch_bounds__(kThreads, NV > 2 ? 1 : 2) group_norm_silu_bwd_
             }
         }
     };
-    fetch(walker);
     for (int64_t r0 = 0; r0 < p.M; r0 += p.walkers) {
         const int64_t r = r0 + walker;
-        const bool on = r < p.M;
+        const bool on = g < p.G && r < p.M;
         const int64_t at = (r * p.G + g) * p.d;
-        float f[NV][8], z[NV][8], dn[NV][8];
+        f2 f[NV][4], dn[NV][4];
+        fetch(r);
+        // the next row into L2, a line per lane (its registers are not to be had)
+        if (g < p.G && r + p.walkers < p.M) {
+            const int64_t rn = r + p.walkers;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            rx[j].get(f[j]);
-            rd[j].get(dn[j]);
-            if (GATE) rz[j].get(z[j]);
+            for (int j = 0; j < NV; ++j) {
+                if ((lane & 7) != 0 || c0 + j * cstep >= p.d) continue;
+                prefetch_l2(px + rn * p.ld_x + j * cstep);
+                prefetch_l2(p.dy + (rn * p.G + g) * p.d + c0 + j * cstep);
+                if (GATE) prefetch_l2(pg + rn * p.ld_gate + j * cstep);
+            }
         }
-        if (r0 + p.walkers < p.M) fetch(r + p.walkers);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) rx[j].get(f[j]);
         const float rstd = normalise<NV>(f, lane, lanes, p);
-        float s1 = 0.f, s2 = 0.f;
+        f2 s1 = f2_splat(0.f), s2 = s1;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = c0 + j * cstep;
             if (c >= p.d) continue;
-            float w[8], b[8];
+            f2 w[4], n[4], z[4], slope[4];
+            Raw<float> t;
+            t.a = *reinterpret_cast<const float4*>(params + c);
+            t.b = *reinterpret_cast<const float4*>(params + c + 4);
+            t.get(w);
+            t.a = *reinterpret_cast<const float4*>(params + p.d + c);
+            t.b = *reinterpret_cast<const float4*>(params + p.d + c + 4);
+            t.get(n);
+            rd[j].get(dn[j]);
+            if (GATE) rz[j].get(z);
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                *reinterpret_cast<float4*>(w + e) = *reinterpret_cast<const float4*>(smem + c + e);
-                *reinterpret_cast<float4*>(b + e) = *reinterpret_cast<const float4*>(smem + p.d + c + e);
+            for (int e = 0; e < 4; ++e) n[e] = f2_fma(f[j][e], w[e], n[e]);
+            // val: act of the gate or of n; slope: its derivative
+            f2 val[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                val[e] = GATE ? z[e] : n[e];
+                slope[e] = f2_splat(1.f);
             }
+            if (p.act) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float n = fmaf(f[j][e], w[e], b[e]);
-                const float a = GATE ? z[j][e] : n;
-                float val = a, slope = 1.f;
-                if (p.act) {
-                    const float sg = sigmoid_f(a);
-                    val = a * sg;
-                    slope = sg * fmaf(a, 1.f - sg, 1.f);
+                for (int e = 0; e < 4; ++e) {
+                    const f2 a = val[e], sg = sigmoid2(a);
+                    val[e] = f2_mul(a, sg);
+                    slope[e] = f2_fma(f2_sub(a, val[e]), sg, sg);    // sg (1 + a (1 - sg))
                 }
-                const float dy = dn[j][e];
-                dn[j][e] = dy * (GATE ? val : slope);
-                z[j][e] = dy * n * slope;
-                sw[j][e] = fmaf(dn[j][e], f[j][e], sw[j][e]);
-                sb[j][e] += dn[j][e];
-                dn[j][e] *= w[e];
-                s1 += dn[j][e];
-                s2 = fmaf(dn[j][e], f[j][e], s2);
             }
-            if (GATE && on) store8(p.dgate + at + c, z[j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f2 d = f2_mul(dn[j][e], GATE ? val[e] : slope[e]);
+                if (GATE) z[e] = f2_mul(f2_mul(dn[j][e], n[e]), slope[e]);
+                sw[j][e] = f2_fma(d, f[j][e], sw[j][e]);
+                sb[j][e] = f2_add(sb[j][e], d);
+                dn[j][e] = f2_mul(d, w[e]);
+                s1 = f2_add(s1, dn[j][e]);
+                s2 = f2_fma(dn[j][e], f[j][e], s2);
+            }
+            if (GATE && on) store8(p.dgate + at + c, z);
         }
-        s1 = p.center ? lanes_sum(s1, lanes) * inv : 0.f;
-        s2 = lanes_sum(s2, lanes) * inv;
+        const float2 t1 = f2_get(s1), t2 = f2_get(s2);
+        const float m1 = p.center ? lanes_sum(t1.x + t1.y, lanes) * inv : 0.f;
+        const float m2 = lanes_sum(t2.x + t2.y, lanes) * inv;
+        const f2 a1 = f2_splat(-rstd * m1), a2 = f2_splat(-rstd * m2), rs = f2_splat(rstd);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = c0 + j * cstep;
             if (!on || c >= p.d) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[j][e] = rstd * (dn[j][e] - fmaf(f[j][e], s2, s1));
+            for (int e = 0; e < 4; ++e) f[j][e] = f2_fma(rs, dn[j][e], f2_fma(a2, f[j][e], a1));
             store8(static_cast<T*>(p.dx) + at + c, f[j]);
         }
     }
     if (!p.part) return;
-    // the seats of a warp, then the warps, in a fixed order
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            for (int o = lanes; o < 32; o <<= 1) {
-                sw[j][e] += __shfl_xor_sync(0xFFFFFFFFu, sw[j][e], o);
-                sb[j][e] += __shfl_xor_sync(0xFFFFFFFFu, sb[j][e], o);
-            }
+    // the warps, in a fixed order
     __syncthreads();
-    float* mine = smem + (threadIdx.x >> 5) * 2 * p.d;
-    if ((threadIdx.x & 31) < lanes) {
+    float* mine = smem + ((threadIdx.x >> 5) * S + seat) * 2 * p.d;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = c0 + j * cstep;
-            if (c >= p.d) continue;
-            store8(mine + c, sw[j]);
-            store8(mine + p.d + c, sb[j]);
+    for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * cstep;
+        if (c >= p.d) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            *reinterpret_cast<float2*>(mine + c + 2 * e) = f2_get(sw[j][e]);
+            *reinterpret_cast<float2*>(mine + p.d + c + 2 * e) = f2_get(sb[j][e]);
         }
     }
     __syncthreads();
-    float* part = p.part + static_cast<int64_t>(blockIdx.x / p.G) * 2 * p.G * p.d + g * p.d;
-    for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
-        float v = 0.f;
-        for (int k = 0; k < kThreads / 32; ++k) v += smem[k * 2 * p.d + i];
-        part[i < p.d ? i : p.G * p.d + i - p.d] = v;
-    }
+    float* part = p.part + static_cast<int64_t>(blockIdx.x / blocks) * 2 * p.G * p.d;
+    for (int k = 0; k < S && g0 + k < p.G; ++k)
+        for (int i = threadIdx.x; i < 2 * p.d; i += kBwdThreads) {
+            float v = 0.f;
+            for (int q = 0; q < kBwdThreads / 32; ++q) v += smem[(q * S + k) * 2 * p.d + i];
+            part[(i < p.d ? 0 : p.G * p.d - p.d) + (g0 + k) * p.d + i] = v;
+        }
 }
 
 // dweight, dbias [C]: the partial rows, and with a shared weight the groups,
@@ -362,14 +409,15 @@ void shape_for(int d, int* lanes, int* nv)
     }
 }
 
-// The backward's CTAs of a group: about four a SM over all groups, no more
-// than the rows need.
-int ctas_of_group(int M, int G, int d)
+// The backward's CTAs of a block of neighbouring groups: all that fit the GPU
+// at once over all blocks, no more than the rows need.
+int ctas_of_block(int M, int G, int d, int* blocks)
 {
     int lanes, nv;
     shape_for(d, &lanes, &nv);
-    const int seats = kThreads / lanes;
-    const int want = (4 * kSms + G - 1) / G, need = (M + seats - 1) / seats;
+    const int S = 32 / lanes, warps = kBwdThreads / 32;
+    *blocks = (G + S - 1) / S;
+    const int fit = bwd_ctas(nv) * kSms / *blocks, want = fit > 0 ? fit : 1, need = (M + warps - 1) / warps;
     return want < need ? want : (need > 0 ? need : 1);
 }
 
@@ -378,13 +426,8 @@ gla_status start(const NormParams& p, int lanes, int blocks, cudaStream_t st)
 {
     trace_begin(st);
     if (BWD) {
-        const int smem = (kThreads / 32) * 2 * p.d * 4;      // 64 KB at most
-        cudaError_t e = cudaSuccess;
-        if (smem > 48 * 1024)
-            e = cudaFuncSetAttribute(group_norm_silu_bwd_kernel<NV, T, GATE>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return status_of(e);
-        group_norm_silu_bwd_kernel<NV, T, GATE><<<blocks, kThreads, smem, st>>>(p, lanes);
+        const int smem = (kBwdThreads / 32) * (32 / lanes) * 2 * p.d * 4;      // 32 KB at most
+        group_norm_silu_bwd_kernel<NV, T, GATE><<<blocks, kBwdThreads, smem, st>>>(p, lanes);
     } else {
         group_norm_silu_kernel<NV, T, GATE><<<blocks, kThreads, 0, st>>>(p, lanes);
     }
@@ -401,9 +444,10 @@ gla_status run(const NormParams& q, cudaStream_t st)
     shape_for(p.d, &lanes, &nv);
     int64_t blocks;
     if (BWD) {
-        const int per = ctas_of_group(p.M, p.G, p.d);
-        p.walkers = per * (kThreads / lanes);
-        blocks = static_cast<int64_t>(per) * p.G;
+        int n;
+        const int per = ctas_of_block(p.M, p.G, p.d, &n);
+        p.walkers = per * (kBwdThreads / 32);
+        blocks = static_cast<int64_t>(per) * n;
     } else {
         const int64_t w = static_cast<int64_t>(kSms) * 8 * kThreads / lanes / p.G;
         p.walkers = static_cast<int>(w < 1 ? 1 : (w < p.M ? w : p.M));
@@ -428,7 +472,8 @@ gla_status run_any(const NormParams& p, bool f32, cudaStream_t st)
 
 size_t group_norm_bwd_workspace_bytes(int M, int G, int d)
 {
-    return static_cast<size_t>(ctas_of_group(M, G, d)) * 2 * G * d * 4;
+    int blocks;
+    return static_cast<size_t>(ctas_of_block(M, G, d, &blocks)) * 2 * G * d * 4;
 }
 
 gla_status launch_group_norm(const void* x, bool f32, const void* gate, const float* weight, const float* bias, void* y,
@@ -481,9 +526,10 @@ gla_status launch_group_norm_bwd(const void* x, bool f32, const void* gate, cons
         if (s != GLA_OK || !p.part) return s;
     }
     if (!dweight && !dbias) return GLA_OK;
+    int blocks;
     const int C = shared_w ? d : G * d;
     trace_begin(st);
-    group_norm_reduce_kernel<<<(C + 31) / 32, 256, 0, st>>>(ws, dweight, dbias, M > 0 ? ctas_of_group(M, G, d) : 0, G, d, shared_w);
+    group_norm_reduce_kernel<<<(C + 31) / 32, 256, 0, st>>>(ws, dweight, dbias, M > 0 ? ctas_of_block(M, G, d, &blocks) : 0, G, d, shared_w);
     trace_end(st, "group_norm_reduce_kernel");
     count_launch();
     return check_launch("group_norm_reduce_kernel");
