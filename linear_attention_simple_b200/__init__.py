@@ -658,18 +658,36 @@ def conv1d_silu_decode_step(x, w, conv_state, slot_idx=None, apply_ln=True, ln_g
 
 # ---- gated delta rule, group norm with an activation
 
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, first.device))
+def _fit(x, name, dtype, shape, device):
+    """Check a contiguous tensor (None passes): one test when it is right, the
+    reason when it is not."""
+    if x is None or (x.dtype is dtype and x.shape == shape and x.device == device and x.is_contiguous()):
+        return
+    _need(x, name, dtype, shape)
+    raise ValueError("%s is on %s, expected %s" % (name, x.device, device))
 
 
-def _call_on(t, fn, *args, stream=None):
-    """Call the C entry point `fn` with t's device current, on `stream` or that
+def _workspace(ws, need, device):
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _fit(ws, "ws", torch.uint8, (ws.numel(),), device)
+    return ws
+
+
+def _call_on(device, fn, *args, stream=None):
+    """Call the C entry point `fn` with `device` current, on `stream` or that
     device's current stream."""
-    with torch.cuda.device(t.device):
-        s = stream if stream is not None else torch.cuda.current_stream(t.device)
-        _check(fn, getattr(lib(), fn)(*args, ctypes.c_void_p(s.cuda_stream)))
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call_on(device, fn, *args, stream=stream)
+    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    status = getattr(lib(), fn)(*args, s)
+    if status != 0:
+        _check(fn, status)
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
 
 
 def _rows_stride(x, name):
@@ -692,42 +710,54 @@ def _rows_stride(x, name):
     return ld
 
 
-def _gated_delta_args(fn, q, k, v, a, beta, cu_seqlens, types):
-    """Check the shared arguments; returns (N, T, Hk, H, dk, dv, ld_qkv)."""
-    lead = q.shape[:-2]
-    if len(lead) != (1 if cu_seqlens is not None else 2):
-        raise ValueError("%s: q must be [%s, Hk, dk]" % (fn, "T" if cu_seqlens is not None else "N, T"))
+def _gated_delta_args(fn, q, k, v, a, beta, lead, cu_seqlens, types):
+    """Check the shared arguments, whose leading dims are `lead`; returns (Hk, H,
+    dk, dv, ld_qkv)."""
     if q.dtype not in types:
         raise TypeError("%s takes %s q, k, v, got %s" % (fn, " or ".join(map(str, types)), q.dtype))
     Hk, dk = q.shape[-2:]
     H, dv = v.shape[-2:]
-    _need(q, "q", q.dtype, contiguous=False)
-    _need(k, "k", q.dtype, lead + (Hk, dk), contiguous=False)
-    _need(v, "v", q.dtype, lead + (H, dv), contiguous=False)
-    _need(a, "a", torch.float32, lead + (H,))
-    _need(beta, "beta", torch.float32, lead + (H,))
-    _same_device(q, k=k, v=v, a=a, beta=beta, cu_seqlens=cu_seqlens)
-    if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", torch.int32)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError("cu_seqlens must have N + 1 entries")
-        N, T = cu_seqlens.numel() - 1, lead[0]
-    else:
-        N, T = lead
-    ld = [_rows_stride(x, name) for x, name in ((q, "q"), (k, "k"), (v, "v"))]
-    if q.numel() == 0 or v.numel() == 0 or ld == [Hk * dk, Hk * dk, H * dv]:
-        return N, T, Hk, H, dk, dv, 0
+    dev = q.device
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    _fit(a, "a", torch.float32, lead + (H,), dev)
+    _fit(beta, "beta", torch.float32, lead + (H,), dev)
+    ld, packed = [], True
+    for x, name, h, d in ((q, "q", Hk, dk), (k, "k", Hk, dk), (v, "v", H, dv)):
+        if x.is_contiguous():
+            _fit(x, name, q.dtype, lead + (h, d), dev)
+            ld.append(h * d)
+        else:
+            _need(x, name, q.dtype, lead + (h, d), contiguous=False)
+            if x.device != dev:
+                raise ValueError("%s is on %s, expected %s" % (name, x.device, dev))
+            ld.append(_rows_stride(x, name))
+            packed = packed and ld[-1] == h * d
+    if packed:
+        return Hk, H, dk, dv, 0
     if not ld[0] == ld[1] == ld[2]:
         raise ValueError("q, k and v must share one token stride when not packed (got %d, %d, %d)" % tuple(ld))
-    return N, T, Hk, H, dk, dv, ld[0]
+    return Hk, H, dk, dv, ld[0]
 
 
-def _new(t, name, like, shape, dtype):
-    """`t` checked against shape and type, or a new tensor on like's device."""
+def _sequences(fn, q, v, cu_seqlens):
+    """(leading dims, N, T) of a chunked call."""
+    lead = tuple(q.shape[:-2])
+    if len(lead) != (1 if cu_seqlens is not None else 2) or v.dim() != q.dim():
+        raise ValueError("%s: q must be [%s, Hk, dk]" % (fn, "T" if cu_seqlens is not None else "N, T"))
+    if cu_seqlens is None:
+        return lead, lead[0], lead[1]
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must have N + 1 entries")
+    _fit(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, q.device)
+    return lead, cu_seqlens.numel() - 1, lead[0]
+
+
+def _new(t, name, shape, dtype, device):
+    """`t` checked against shape and type, or a new tensor."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _need(t, name, dtype, shape)
-    _same_device(like, **{name: t})
+        return torch.empty(shape, dtype=dtype, device=device)
+    _fit(t, name, dtype, shape, device)
     return t
 
 
@@ -744,20 +774,18 @@ def gated_delta_chunk_fwd(q, k, v, a, beta, s0=None, cu_seqlens=None, o=None, s_
     beta [N,T,H] fp32; with cu_seqlens [N+1] int32 (on the device) the N
     sequences are packed and the leading dims are [T].  Returns (o in v's
     shape, s_final [N,H,dk,dv] fp32 or None)."""
-    N, T, Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_fwd", q, k, v, a, beta, cu_seqlens,
-                                                (torch.bfloat16,))
-    _need(s0, "s0", torch.float32, (N, H, dk, dv))
-    _same_device(q, s0=s0, ws=ws)
-    o = _new(o, "o", q, tuple(v.shape), torch.bfloat16)
+    lead, N, T = _sequences("gated_delta_chunk_fwd", q, v, cu_seqlens)
+    Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_fwd", q, k, v, a, beta, lead, cu_seqlens,
+                                          (torch.bfloat16,))
+    dev = q.device
+    _fit(s0, "s0", torch.float32, (N, H, dk, dv), dev)
+    o = _new(o, "o", lead + (H, dv), torch.bfloat16, dev)
     if s_final is not None or want_final_state:
-        s_final = _new(s_final, "s_final", q, (N, H, dk, dv), torch.float32)
-    if ws is None:
-        need = gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _need(ws, "ws", torch.uint8)
-    _call_on(q, "gated_delta_chunk_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(cu_seqlens), _ptr(s0),
-             _ptr(o), _ptr(s_final), _ptr(ws), ws.numel(), N, T, Hk, H, dk, dv, ld,
-             float(dk ** -0.5 if scale is None else scale), GLA_BF16, stream=stream)
+        s_final = _new(s_final, "s_final", (N, H, dk, dv), torch.float32, dev)
+    ws = _workspace(ws, gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None), dev)
+    _call_on(dev, "gated_delta_chunk_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), beta.data_ptr(),
+             _data(cu_seqlens), _data(s0), o.data_ptr(), _data(s_final), ws.data_ptr(), ws.numel(), N, T, Hk, H, dk, dv,
+             ld, dk ** -0.5 if scale is None else scale, GLA_BF16, stream=stream)
     return o, s_final
 
 
@@ -767,28 +795,26 @@ def gated_delta_chunk_bwd(q, k, v, a, beta, dO, s0=None, ds_final=None, cu_seqle
     forward).  dO in v's shape, bf16; ds_final [N,H,dk,dv] fp32 or None.  Returns
     (dq, dk, dv, da, dbeta, ds0): dq, dk, dv bf16 in q, k and v's shapes, da and
     dbeta fp32, ds0 fp32 or None."""
-    N, T, Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_bwd", q, k, v, a, beta, cu_seqlens,
-                                                (torch.bfloat16,))
-    _need(s0, "s0", torch.float32, (N, H, dk, dv))
-    _need(ds_final, "ds_final", torch.float32, (N, H, dk, dv))
-    _need(dO, "dO", torch.bfloat16, tuple(v.shape))
-    _same_device(q, s0=s0, ds_final=ds_final, dO=dO, ws=ws)
+    lead, N, T = _sequences("gated_delta_chunk_bwd", q, v, cu_seqlens)
+    Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_bwd", q, k, v, a, beta, lead, cu_seqlens,
+                                          (torch.bfloat16,))
+    dev, f32, bf16 = q.device, torch.float32, torch.bfloat16
+    _fit(s0, "s0", f32, (N, H, dk, dv), dev)
+    _fit(ds_final, "ds_final", f32, (N, H, dk, dv), dev)
+    _fit(dO, "dO", bf16, lead + (H, dv), dev)
     gq, gk, gv, ga, gb, gs = grads if grads is not None else (None,) * 6
-    gq = _new(gq, "grad_q", q, tuple(q.shape), torch.bfloat16)
-    gk = _new(gk, "grad_k", q, tuple(k.shape), torch.bfloat16)
-    gv = _new(gv, "grad_v", q, tuple(v.shape), torch.bfloat16)
-    ga = _new(ga, "grad_a", q, tuple(a.shape), torch.float32)
-    gb = _new(gb, "grad_beta", q, tuple(a.shape), torch.float32)
+    gq = _new(gq, "grad_q", lead + (Hk, dk), bf16, dev)
+    gk = _new(gk, "grad_k", lead + (Hk, dk), bf16, dev)
+    gv = _new(gv, "grad_v", lead + (H, dv), bf16, dev)
+    ga = _new(ga, "grad_a", lead + (H,), f32, dev)
+    gb = _new(gb, "grad_beta", lead + (H,), f32, dev)
     if gs is not None or (want_grad_s0 and grads is None):
-        gs = _new(gs, "grad_s0", q, (N, H, dk, dv), torch.float32)
-    if ws is None:
-        need = gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None, True)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _need(ws, "ws", torch.uint8)
-    _call_on(q, "gated_delta_chunk_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(cu_seqlens), _ptr(s0),
-             _ptr(dO), _ptr(ds_final), _ptr(gq), _ptr(gk), _ptr(gv), _ptr(ga), _ptr(gb), _ptr(gs), _ptr(ws),
-             ws.numel(), N, T, Hk, H, dk, dv, ld, float(dk ** -0.5 if scale is None else scale), GLA_BF16,
-             stream=stream)
+        gs = _new(gs, "grad_s0", (N, H, dk, dv), f32, dev)
+    ws = _workspace(ws, gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None, True), dev)
+    _call_on(dev, "gated_delta_chunk_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), beta.data_ptr(),
+             _data(cu_seqlens), _data(s0), dO.data_ptr(), _data(ds_final), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
+             ga.data_ptr(), gb.data_ptr(), _data(gs), ws.data_ptr(), ws.numel(), N, T, Hk, H, dk, dv, ld,
+             dk ** -0.5 if scale is None else scale, GLA_BF16, stream=stream)
     return gq, gk, gv, ga, gb, gs
 
 
@@ -797,38 +823,54 @@ def gated_delta_decode_step(state, q, k, v, a, beta, o=None, slot_idx=None, scal
     [n_slots,H,dk,dv] fp32; q, k [N,Hk,dk] and v [N,H,dv] (one token), or
     [N,T,Hk,dk] and [N,T,H,dv] (T tokens in order), bf16 or fp32; a, beta [N,H]
     or [N,T,H] fp32; slot_idx [N] int32 or None.  Returns o in v's shape, fp32."""
-    one = q.dim() == 3
-    xs = [x.unsqueeze(1) if one else x for x in (q, k, v, a, beta)]
-    N, T, Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_decode_step", *xs, None,
-                                                (torch.bfloat16, torch.float32))
-    _need(state, "state", torch.float32)
-    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dk, dv):
+    lead = tuple(q.shape[:-2])
+    if len(lead) not in (1, 2) or v.dim() != q.dim():
+        raise ValueError("gated_delta_decode_step: q must be [N, Hk, dk] or [N, T, Hk, dk]")
+    N, T = lead if len(lead) == 2 else (lead[0], 1)
+    Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_decode_step", q, k, v, a, beta, lead, None,
+                                          (torch.bfloat16, torch.float32))
+    dev = q.device
+    if state.dim() != 4 or state.shape[1:] != (H, dk, dv):
         raise ValueError("state must be [n_slots, %d, %d, %d]" % (H, dk, dv))
-    _need(slot_idx, "slot_idx", torch.int32, (N,))
+    _fit(state, "state", torch.float32, state.shape, dev)
+    _fit(slot_idx, "slot_idx", torch.int32, (N,), dev)
     if slot_idx is None and state.shape[0] != N:
         raise ValueError("without slot_idx the state must have N slots")
-    _same_device(q, state=state, slot_idx=slot_idx)
-    o = _new(o, "o", q, tuple(v.shape), torch.float32)
-    _call_on(q, "gated_delta_decode_step", _ptr(state), _ptr(slot_idx), state.shape[0], *map(_ptr, xs), _ptr(o), N, T,
-             Hk, H, dk, dv, ld, float(dk ** -0.5 if scale is None else scale), _dt(q), stream=stream)
+    o = _new(o, "o", lead + (H, dv), torch.float32, dev)
+    _call_on(dev, "gated_delta_decode_step", state.data_ptr(), _data(slot_idx), state.shape[0], q.data_ptr(),
+             k.data_ptr(), v.data_ptr(), a.data_ptr(), beta.data_ptr(), o.data_ptr(), N, T, Hk, H, dk, dv, ld,
+             dk ** -0.5 if scale is None else scale, _dt(q), stream=stream)
     return o
+
+
+def _norm_rows(x, name, dtype, shape, device):
+    """Row stride of x or gate (0: contiguous)."""
+    if x is None or x.is_contiguous():
+        _fit(x, name, dtype, shape, device)
+        return 0
+    _need(x, name, dtype, shape, contiguous=False)
+    if x.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, x.device, device))
+    return _rows_stride(x, name) if x.numel() else 0
 
 
 def _norm_args(x, weight, bias, gate):
     """Check group_norm_silu's tensors; returns (M, G, d, ld_x, ld_gate, shared)."""
     if x.dim() < 2:
         raise ValueError("x must be [..., G, d]")
-    G, d = x.shape[-2:]
-    _need(x, "x", x.dtype, contiguous=False)
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
     _dt(x)
-    _need(gate, "gate", torch.bfloat16, tuple(x.shape), contiguous=False)
+    shape, dev = x.shape, x.device
+    G, d = shape[-2:]
     first = weight if weight is not None else bias
     shared = first is not None and first.dim() == 1
-    _need(weight, "weight", torch.float32, (d,) if shared else (G, d))
-    _need(bias, "bias", torch.float32, (d,) if shared else (G, d))
-    _same_device(x, weight=weight, bias=bias, gate=gate)
+    params = (d,) if shared else (G, d)
+    _fit(weight, "weight", torch.float32, params, dev)
+    _fit(bias, "bias", torch.float32, params, dev)
     M = x.numel() // (G * d) if G * d else 0
-    return M, G, d, _rows_stride(x, "x") if M else 0, _rows_stride(gate, "gate") if gate is not None and M else 0, shared
+    return (M, G, d, _norm_rows(x, "x", x.dtype, shape, dev), _norm_rows(gate, "gate", torch.bfloat16, shape, dev),
+            int(shared))
 
 
 def group_norm_silu(x, weight=None, bias=None, gate=None, center=True, act=True, eps=1e-5, y=None, stream=None):
@@ -839,9 +881,9 @@ def group_norm_silu(x, weight=None, bias=None, gate=None, center=True, act=True,
     n * silu(gate), or silu(n) without a gate (act=False: the identity in
     silu's place), bf16 in x's shape."""
     M, G, d, ldx, ldg, shared = _norm_args(x, weight, bias, gate)
-    y = _new(y, "y", x, tuple(x.shape), torch.bfloat16)
-    _call_on(x, "group_norm_silu", _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y), M, G, d, ldx, ldg,
-             int(shared), int(center), int(act), float(eps), _dt(x), stream=stream)
+    y = _new(y, "y", x.shape, torch.bfloat16, x.device)
+    _call_on(x.device, "group_norm_silu", x.data_ptr(), _data(gate), _data(weight), _data(bias), y.data_ptr(), M, G, d,
+             ldx, ldg, shared, int(center), int(act), eps, _dt(x), stream=stream)
     return y
 
 
@@ -855,19 +897,18 @@ def group_norm_silu_bwd(x, dy, weight=None, bias=None, gate=None, center=True, a
     type, dgate bf16 or None, dweight, dbias in the shapes of weight and bias,
     fp32, or None)."""
     M, G, d, ldx, ldg, shared = _norm_args(x, weight, bias, gate)
-    _need(dy, "dy", torch.bfloat16, tuple(x.shape))
-    _same_device(x, dy=dy, ws=ws)
+    dev, f32 = x.device, torch.float32
+    _fit(dy, "dy", torch.bfloat16, x.shape, dev)
     gx, gg, gw, gb = grads if grads is not None else (None,) * 4
-    gx = _new(gx, "grad_x", x, tuple(x.shape), x.dtype)
-    gg = _new(gg, "grad_gate", x, tuple(x.shape), torch.bfloat16) if gate is not None else None
-    gw = _new(gw, "grad_weight", x, tuple(weight.shape), torch.float32) if weight is not None else None
-    gb = _new(gb, "grad_bias", x, tuple(bias.shape), torch.float32) if bias is not None else None
-    if ws is None and (gw is not None or gb is not None):
-        ws = torch.empty(group_norm_silu_bwd_workspace_bytes(M, G, d), dtype=torch.uint8, device=x.device)
-    _need(ws, "ws", torch.uint8)
-    _call_on(x, "group_norm_silu_bwd", _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(gx), _ptr(gg),
-             _ptr(gw), _ptr(gb), _ptr(ws), 0 if ws is None else ws.numel(), M, G, d, ldx, ldg, int(shared),
-             int(center), int(act), float(eps), _dt(x), stream=stream)
+    gx = _new(gx, "grad_x", x.shape, x.dtype, dev)
+    gg = _new(gg, "grad_gate", x.shape, torch.bfloat16, dev) if gate is not None else None
+    gw = _new(gw, "grad_weight", weight.shape, f32, dev) if weight is not None else None
+    gb = _new(gb, "grad_bias", bias.shape, f32, dev) if bias is not None else None
+    if ws is not None or gw is not None or gb is not None:
+        ws = _workspace(ws, group_norm_silu_bwd_workspace_bytes(M, G, d), dev)
+    _call_on(dev, "group_norm_silu_bwd", x.data_ptr(), _data(gate), _data(weight), _data(bias), dy.data_ptr(),
+             gx.data_ptr(), _data(gg), _data(gw), _data(gb), _data(ws), 0 if ws is None else ws.numel(), M, G, d, ldx, ldg,
+             shared, int(center), int(act), eps, _dt(x), stream=stream)
     return gx, gg, gw, gb
 
 

@@ -39,12 +39,14 @@ struct StepParams {
     int* status;
 };
 
+// Sixteen rows a thread: 64 registers of state, and room for the rest below 96,
+// so that two CTAs share an SM at 192 columns.
 template <int DK>
-constexpr int row_groups() { return DK == 128 ? 8 : 4; }
+constexpr int row_groups() { return DK / 16; }
 constexpr int kMaxQuads = 64;              // float4 column groups of a CTA (dv <= 256)
 
 template <int DK, class Tin>
-__global__ void __launch_bounds__(row_groups<DK>() * kMaxQuads, DK == 128 ? 1 : 2) gd_step_kernel(StepParams p)
+__global__ void __maxnreg__(96) gd_step_kernel(StepParams p)
 {
     constexpr int RG = row_groups<DK>(), R = DK / RG;
     __shared__ float2 s_kq[2][DK];
@@ -60,10 +62,14 @@ __global__ void __launch_bounds__(row_groups<DK>() * kMaxQuads, DK == 128 ? 1 : 
         if (t == 0) record_status(p.status, GLA_ERR_INVALID_ARG);
         return;
     }
-    float* S = p.state + (slot * p.H + h) * DK * p.dv + col;
+    float* S = p.state + ((slot * p.H + h) * DK + rg) * p.dv + col;
+    const int step = RG * p.dv;                    // elements between a thread's rows
     float4 s[R];
+    {
+        const float* at = S;
 #pragma unroll
-    for (int i = 0; i < R; ++i) s[i] = __ldcs(reinterpret_cast<const float4*>(S + static_cast<int64_t>(rg + RG * i) * p.dv));
+        for (int i = 0; i < R; ++i, at += step) s[i] = __ldcs(reinterpret_cast<const float4*>(at));
+    }
 
     const Tin* q = static_cast<const Tin*>(p.q) + static_cast<int64_t>(n) * p.T * p.ld_qk + hk * DK;
     const Tin* k = static_cast<const Tin*>(p.k) + static_cast<int64_t>(n) * p.T * p.ld_qk + hk * DK;
@@ -126,8 +132,9 @@ __global__ void __launch_bounds__(row_groups<DK>() * kMaxQuads, DK == 128 ? 1 : 
                 make_float4(p.scale * fmaf(d, u.x, zq.x), p.scale * fmaf(d, u.y, zq.y), p.scale * fmaf(d, u.z, zq.z),
                             p.scale * fmaf(d, u.w, zq.w));
     }
+    asm volatile("" : "+l"(S));                    // the rows' addresses are formed anew, not kept in registers
 #pragma unroll
-    for (int i = 0; i < R; ++i) __stcs(reinterpret_cast<float4*>(S + static_cast<int64_t>(rg + RG * i) * p.dv), s[i]);
+    for (int i = 0; i < R; ++i, S += step) __stcs(reinterpret_cast<float4*>(S), s[i]);
 }
 
 template <int DK>
