@@ -202,51 +202,6 @@ __device__ void copies(const Cta& x, Bars& B, const GdParams& p, const CUtensorM
     if (pp > 0) mbar_wait(&B.fp, (pp - 1) & 1, ctl);
 }
 
-// Sixteen fp32 values as NT bf16 terms of 8 columns, at taddr, + 8, + 16.
-template <int NT>
-__device__ __forceinline__ void put_terms(uint32_t taddr, float (&x)[16])
-{
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-            if (n + 1 < NT) {
-                x[2 * i] -= bf16_lo(w[i]);
-                x[2 * i + 1] -= bf16_hi(w[i]);
-            }
-        }
-        tmem_st8(taddr + 8 * n, w);
-    }
-}
-__device__ __forceinline__ void put16(uint32_t taddr, const float (&x)[16])
-{
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i]);
-    tmem_st16(taddr, w);
-}
-// This row's 32 tokens of a slice, zeros from `left` on (what lies there is
-// not the sequence's).  The loads do not wait for the comparison.
-__device__ __forceinline__ void load_rows(float (&f)[32], const __nv_bfloat16* s, int stride, int left)
-{
-#pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = __bfloat162float(s[i * stride]);
-    if (left < 32) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = i < left ? f[i] : 0.f;
-    }
-}
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-// Arrive for this warp once its tensor-memory accesses are done.
-__device__ __forceinline__ void warp_done(uint64_t* bar, int lane)
-{
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-}
 // Sums of 32 values over the 32 lanes: lane t has the total of value t.
 __device__ __forceinline__ float lane_sums(float (&v)[32], int lane)
 {
@@ -264,16 +219,26 @@ __device__ __forceinline__ float lane_sums(float (&v)[32], int lane)
 }
 // A thread's state columns, rounded to bf16, to its half row of [dv][dk].
 template <int HS>
-__device__ __forceinline__ void store_half_row(__nv_bfloat16* dst, const float (&S)[HS])
+__device__ __forceinline__ void store_half_row(__nv_bfloat16* dst, const f2 (&S)[HS / 2])
 {
 #pragma unroll
     for (int k = 0; k < HS / 16; ++k) {
         uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack_bf16(S[16 * k + 2 * i], S[16 * k + 2 * i + 1]);
+        for (int i = 0; i < 8; ++i) w[i] = f2_to_bf16x2(S[8 * k + i]);
         st_global_v8(dst + 16 * k, w);
     }
 }
+__device__ __forceinline__ void split_pairs(float (&f)[32], int b, const Cols16& x)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 t = f2_get(x.p[i]);
+        f[16 * b + 2 * i] = t.x;
+        f[16 * b + 2 * i + 1] = t.y;
+    }
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---------------------------------------------------------------- forward
 template <int DK>
@@ -373,24 +338,17 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
         const int half = warp >> 2, r = x.w0 + (warp & 3) * 32 + lane, wr = r >> 5, nwr = p.dv >> 5;
         const uint32_t t0 = tm + (static_cast<uint32_t>(warp & 3) << 21);
         constexpr int HS = DK / 2;
-        float S[HS];
-        const float* s0 = p.s0 ? p.s0 + (x.nh * DK + half * HS) * p.dv + r : nullptr;
-#pragma unroll
-        for (int i = 0; i < HS; ++i) S[i] = s0 ? s0[static_cast<int64_t>(i) * p.dv] : 0.f;
+        f2 S[HS / 2];
+        load_state<HS>(S, p.s0 ? p.s0 + (x.nh * DK + half * HS) * p.dv + r : nullptr, p.dv);
         auto put_state = [&]() {
 #pragma unroll
-            for (int k = 0; k < HS / 16; ++k) {
-                float f[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = S[16 * k + i];
-                put_terms<2>(t0 + C::S + half * HS + 16 * k, f);
-            }
+            for (int k = 0; k < HS / 16; ++k) put_terms<2>(t0 + C::S + half * HS + 16 * k, cols_of<HS>(S, k));
         };
         // the state in fp32, as this thread holds it
         auto keep = [&](float* dst) {
 #pragma unroll
-            for (int i = 0; i < HS; i += 4)
-                *reinterpret_cast<float4*>(dst + i * 32) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+            for (int i = 0; i < HS / 2; i += 2)
+                *reinterpret_cast<ulonglong2*>(dst + 2 * i * 32) = make_ulonglong2(S[i].v, S[i + 1].v);
         };
         if (x.nc > 0) {
             put_state();
@@ -398,31 +356,27 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
         }
         bool ok = true;
         for (int c = 0; c < x.nc; ++c) {
-            const int ph = c & 1;
+            const int ph = c & 1, s = 2 * half;              // this thread's steps of 16 tokens: s and s + 1
             const int64_t u = x.u0 + static_cast<int64_t>(c) * p.seqs.H;
-            const float* sc = reinterpret_cast<const float*>(x.smem + ph * M::KSC + Rec::SC);
-            __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(x.slice(0, ph)) + half * 32 * x.rows + (warp & 3) * 32 + lane;
-            const __nv_bfloat16* ds = reinterpret_cast<const __nv_bfloat16*>(x.slice(1, ph)) + (vs - reinterpret_cast<__nv_bfloat16*>(x.slice(0, ph)));
-            const int left = x.len - c * kGdC - half * 32;
+            const float* sc = reinterpret_cast<const float*>(x.smem + ph * M::KSC + Rec::SC) + 16 * s;
+            const int at = 16 * s * x.rows + (warp & 3) * 32 + lane;          // this row's 32 tokens in a slice
+            __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(x.slice(0, ph)) + at;
+            const __nv_bfloat16* ds = reinterpret_cast<const __nv_bfloat16*>(x.slice(1, ph)) + at;
+            const int left = x.len - c * kGdC - 16 * s;
             ok = warp_wait(&B.full[ph], (c >> 1) & 1, ctl);
             if (!ok) break;
-            float v[32];
-            load_rows(v, vs, x.rows, left);
+            Cols16 v[2], y[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) v[b] = load_row16(vs + 16 * b * x.rows, x.rows, left - 16 * b);
             ok = warp_wait(&B.y, ph, ctl);
             if (!ok) break;
             tc_fence_after();
+            get16x2(y[0], y[1], t0 + C::Y + 16 * s, t0 + C::Y + 16 * s + 16);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int s = half * 2 + b;
-                float f[16], G[16];
-                load16(G, sc + kScG * kGdC + 16 * s);
-                get16(f, t0 + C::Y + 16 * s);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] *= G[i];
-                put16(t0 + C::Y + 16 * s, f);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] -= v[16 * b + i];
-                put_terms<2>(t0 + C::R + 16 * s, f);
+                y[b] = y[b] * load16(sc + kScG * kGdC + 16 * b);
+                put16(t0 + C::Y + 16 * (s + b), y[b]);
+                put_terms<2>(t0 + C::R + 16 * (s + b), y[b] - v[b]);
             }
             warp_done(&B.r, lane);
             // while the products run: the state that enters the chunk
@@ -430,63 +384,39 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
             ok = warp_wait(&B.z, ph, ctl);
             if (!ok) break;
             tc_fence_after();
-            float* yn = p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32) + lane * 4;
+            get16x2(y[0], y[1], t0 + C::Y + 16 * s, t0 + C::Y + 16 * s + 16);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int s = half * 2 + b;
-                float f[16], g[16];
-                get16(f, t0 + C::Y + 16 * s);
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<float4*>(yn + (16 * b + i) * 32) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-                load16(g, sc + kScBeta * kGdC + 16 * s);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    f[i] = g[i] * (v[16 * b + i] - f[i]);
-                    v[16 * b + i] = f[i];                    // V' from here on
-                }
-                load16(g, sc + kScR * kGdC + 16 * s);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) g[i] *= f[i];
-                put_terms<3>(t0 + C::V + 24 * s, f);
-                // the scaled V': terms 0 and 1 over y, term 2 over R
-                {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int n = 0; n < 3; ++n) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            w[i] = pack_bf16(g[2 * i], g[2 * i + 1]);
-                            g[2 * i] -= bf16_lo(w[i]);
-                            g[2 * i + 1] -= bf16_hi(w[i]);
-                        }
-                        tmem_st8(t0 + (n < 2 ? C::Y + 16 * s + 8 * n : C::R + 16 * s), w);
-                    }
-                }
+                v[b] = load16(sc + kScBeta * kGdC + 16 * b) * (v[b] - y[b]);                 // V'
+                put_terms<3>(t0 + C::V + 24 * (s + b), v[b], t0 + C::V + 24 * (s + b) + 16);
+                // scaled: terms 0 and 1 over y, term 2 over R
+                put_terms<3>(t0 + C::Y + 16 * (s + b), v[b] * load16(sc + kScR * kGdC + 16 * b), t0 + C::R + 16 * (s + b));
             }
             warp_done(&B.w, lane);
-            const float gl = sc[kScG * kGdC + kGdC - 1];
-            float d[32];
-            load_rows(d, ds, x.rows, left);
+            const float gl = sc[kScG * kGdC + kGdC - 1 - 16 * s];
+            float* yn = p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32) + lane * 4;
+            Cols16 d[2];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) vs[i * x.rows] = __float2bfloat16_rn(v[i]);
+            for (int b = 0; b < 2; ++b) {
+                d[b] = load_row16(ds + 16 * b * x.rows, x.rows, left - 16 * b);
+                store_row16(vs + 16 * b * x.rows, x.rows, v[b]);
+            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&B.staged[ph]);
                 mbar_arrive(&B.empty[ph]);                   // scalars, V and dO are read
             }
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<ulonglong2*>(yn + (16 * b + 4 * i) * 32) = make_ulonglong2(y[b].p[2 * i].v, y[b].p[2 * i + 1].v);
             if (c > 0 && (c & 1) == 0) keep(p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32) + lane * 4);
             ok = warp_wait(&B.ds, ph, ctl);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < HS / 16; ++k) {
-                float f[16];
-                get16(f, t0 + C::S + half * HS + 16 * k);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) S[16 * k + i] = fmaf(gl, S[16 * k + i], f[i]);
-            }
+            add_cols<HS>(S, t0 + C::S + half * HS, gl);
             if (c + 1 < x.nc) {
                 put_state();
                 warp_done(&B.s, lane);
@@ -494,17 +424,14 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
             ok = warp_wait(&B.out, ph, ctl);
             if (!ok) break;
             tc_fence_after();
-            {
-                uint32_t o[32];
-                tmem_ld32(t0 + C::O + half * 32, o);
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B.o);
+            get16x2(y[0], y[1], t0 + C::O + 16 * s, t0 + C::O + 16 * s + 16);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.o);
+            float od[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) d[i] *= __uint_as_float(o[i]);
-            }
-            p.part[(u * 3 * nwr + wr) * kGdC + half * 32 + lane] = lane_sums(d, lane);
+            for (int b = 0; b < 2; ++b) split_pairs(od, b, d[b] * y[b]);
+            p.part[(u * 3 * nwr + wr) * kGdC + half * 32 + lane] = lane_sums(od, lane);
         }
         if (ok && p.ds_final) keep(p.sn_last + ((x.nh * nwr + wr) * 2 + half) * (HS * 32) + lane * 4);
     }
@@ -600,34 +527,38 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
         const int half = warp >> 2, r = x.w0 + (warp & 3) * 32 + lane, wr = r >> 5, nwr = p.dv >> 5;
         const uint32_t t0 = tm + (static_cast<uint32_t>(warp & 3) << 21);
         constexpr int HS = DK / 2;
-        const int at = half * 32 * x.rows + (warp & 3) * 32 + lane;              // this row's tokens in a slice
-        float E[HS];
-        const float* e0 = p.ds_final ? p.ds_final + (x.nh * DK + half * HS) * p.dv + r : nullptr;
-#pragma unroll
-        for (int i = 0; i < HS; ++i) E[i] = e0 ? e0[static_cast<int64_t>(i) * p.dv] : 0.f;
+        const int s = 2 * half;                              // this thread's steps of 16 tokens: s and s + 1
+        const int at = 16 * s * x.rows + (warp & 3) * 32 + lane;              // this row's 32 tokens in a slice
+        f2 E[HS / 2];
+        load_state<HS>(E, p.ds_final ? p.ds_final + (x.nh * DK + half * HS) * p.dv + r : nullptr, p.dv);
         auto put_grad = [&]() {
 #pragma unroll
             for (int k = 0; k < HS / 16; ++k) {
-                float f[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = E[16 * k + i];
-                put_terms<3>(t0 + C::E + half * (HS / 2 * 3) + 24 * k, f);
+                const uint32_t t = t0 + C::E + half * (HS / 2 * 3) + 24 * k;
+                put_terms<3>(t, cols_of<HS>(E, k), t + 16);
             }
         };
-        // dO of step i into tensor memory
+        // dO of step i into tensor memory, and for this thread
+        uint32_t dw[2][8];
         auto put_dO = [&](int i) {
             const __nv_bfloat16* ds = reinterpret_cast<const __nv_bfloat16*>(x.slice(1, i & 1)) + at;
-            const int left = x.len - (x.nc - 1 - i) * kGdC - half * 32;
+            const int left = x.len - (x.nc - 1 - i) * kGdC - 16 * s;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                uint32_t w[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int t = 16 * b + 2 * j;
                     const uint32_t lo = __bfloat16_as_ushort(ds[t * x.rows]), hi = __bfloat16_as_ushort(ds[(t + 1) * x.rows]);
-                    w[j] = (t < left ? lo : 0u) | (t + 1 < left ? hi << 16 : 0u);
+                    dw[b][j] = lo | (hi << 16);
                 }
-                tmem_st8(t0 + C::X + (i & 1) * 32 + half * 16 + 8 * b, w);
+                if (left < 32) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int t = 16 * b + 2 * j;
+                        dw[b][j] = t + 1 < left ? dw[b][j] : t < left ? dw[b][j] & 0xFFFFu : 0u;
+                    }
+                }
+                tmem_st8(t0 + C::X + (i & 1) * 32 + half * 16 + 8 * b, dw[b]);
             }
             warp_done(&B.x[i & 1], lane);
         };
@@ -641,64 +572,66 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
         for (int i = 0; ok && i < x.nc; ++i) {
             const int ph = i & 1, c = x.nc - 1 - i;
             const int64_t u = x.u0 + static_cast<int64_t>(c) * p.seqs.H;
-            const float* sc = reinterpret_cast<const float*>(x.smem + ph * M::KSC + Rec::SC);
+            const float* sc = reinterpret_cast<const float*>(x.smem + ph * M::KSC + Rec::SC) + 16 * s;
             __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(x.slice(0, ph)) + at;
-            const __nv_bfloat16* ds = reinterpret_cast<const __nv_bfloat16*>(x.slice(1, ph)) + at;
-            const int left = x.len - c * kGdC - half * 32;
+            const int left = x.len - c * kGdC - 16 * s;
             // while the first products run: <E, state leaving> (the sum of da's
             // terms over all later tokens; after every second chunk), E rounded,
             // and y from the forward; the next step's into L2
             if (i + 1 < x.nc) {
                 const int64_t un = u - p.seqs.H;
-                const char* a = reinterpret_cast<const char*>(p.yn + ((un * nwr + wr) * 2 + half) * (32 * 32));
-                prefetch_l2(a + lane * 128);
+                prefetch_l2(p.yn + ((un * nwr + wr) * 2 + half) * (32 * 32) + lane * 32);
                 if ((c & 1) == 0) {
-                    const char* b = reinterpret_cast<const char*>(p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32));
-                    for (int k = lane; k < HS; k += 32) prefetch_l2(b + k * 128);
+                    const float* b = p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32);
+                    for (int k = lane; k < HS; k += 32) prefetch_l2(b + k * 32);
                 }
             }
             float dot = 0.f;
             if (i > 0 ? (c & 1) == 1 : p.ds_final != nullptr) {
                 const float* sn = (i > 0 ? p.sn + (((u + p.seqs.H) * nwr + wr) * 2 + half) * (HS * 32)
                                          : p.sn_last + ((x.nh * nwr + wr) * 2 + half) * (HS * 32)) + lane * 4;
+                f2 sum = f2_splat(0.f);
 #pragma unroll
-                for (int k = 0; k < HS; k += 4) {
-                    const float4 s = __ldcs(reinterpret_cast<const float4*>(sn + k * 32));
-                    dot += E[k] * s.x + E[k + 1] * s.y + E[k + 2] * s.z + E[k + 3] * s.w;
+                for (int k = 0; k < HS / 2; k += 2) {
+                    const ulonglong2 w = __ldcs(reinterpret_cast<const ulonglong2*>(sn + 2 * k * 32));
+                    f2 a, b;
+                    a.v = w.x;
+                    b.v = w.y;
+                    sum = f2_fma(E[k + 1], b, f2_fma(E[k], a, sum));
                 }
+                const float2 t = f2_get(sum);
+                dot = t.x + t.y;
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
             }
             if (lane == 0) p.anch[(u * nwr + wr) * 2 + half] = dot;
             store_half_row<HS>(p.eb + (u * p.dv + r) * DK + half * HS, E);
-            float4 yn[8];
+            Cols16 y[2], d[2];
             const float* yp = p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32) + lane * 4;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) yn[k] = __ldcs(reinterpret_cast<const float4*>(yp + k * 128));
-
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const ulonglong2 w = __ldcs(reinterpret_cast<const ulonglong2*>(yp + (16 * b + 4 * k) * 32));
+                    y[b].p[2 * k].v = w.x;
+                    y[b].p[2 * k + 1].v = w.y;
+                }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const Cols16 f = load16(sc + kScBeta * kGdC + 16 * b) * load16(sc + kScPd * kGdC + 16 * b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[b].p[j] = f2_mul(f.p[j], f2_from_bf16x2(dw[b][j]));       // beta P_ii dO
+            }
             ok = warp_wait(&B.y, ph, ctl);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int s = half * 2 + b;
-                float f[16], g[16], q[16];
-                get16(f, t0 + C::Y + 16 * s);
-                get16(q, t0 + C::PO + 16 * s);
-                load16(g, sc + kScR * kGdC + 16 * s);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = fmaf(g[j], f[j], q[j]);
-                load16(g, sc + kScBeta * kGdC + 16 * s);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] *= g[j];
-                put16(t0 + C::PO + 16 * s, f);
-                load16(q, sc + kScPd * kGdC + 16 * s);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float dO = __bfloat162float(ds[(16 * b + j) * x.rows]);
-                    f[j] = 16 * b + j < left ? fmaf(g[j] * q[j], dO, f[j]) : 0.f;
-                }
-                put_terms<2>(t0 + C::Y + 16 * s, f);
+                Cols16 f, q;
+                get16x2(f, q, t0 + C::Y + 16 * (s + b), t0 + C::PO + 16 * (s + b));
+                f = load16(sc + kScBeta * kGdC + 16 * b) * fma16(load16(sc + kScR * kGdC + 16 * b), f, q);
+                put16(t0 + C::PO + 16 * (s + b), f);
+                put_terms<2>(t0 + C::Y + 16 * (s + b), f + d[b]);
             }
             warp_done(&B.r, lane);
             if (i + 1 < x.nc) {
@@ -712,33 +645,19 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             float s1[32], s2[32];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int s = half * 2 + b;
-                float f[16], g[16], q[16];
-                get16(f, t0 + C::PO + 16 * s);               // dvs
-                load16(g, sc + kScBeta * kGdC + 16 * s);
-                load16(q, sc + kScPd * kGdC + 16 * s);
+                const Cols16 f = get16(t0 + C::PO + 16 * (s + b)), full = f + d[b];              // dvs, dv
+                Cols16 g = load16(sc + kScG * kGdC + 16 * b) * full;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int t = 16 * b + j;
-                    const bool in = t < left;
-                    const float4 y4 = yn[t >> 2];
-                    const float y = (t & 3) == 0 ? y4.x : (t & 3) == 1 ? y4.y : (t & 3) == 2 ? y4.z : y4.w;
-                    const float v = __bfloat162float(vs[t * x.rows]), d = __bfloat162float(ds[t * x.rows]);
-                    const float z = in ? v - y : 0.f, dO = in ? d : 0.f;
-                    const float full = fmaf(g[j] * q[j], dO, f[j]);
-                    s1[t] = fmaf(full, y, f[j] * z);
-                    s2[t] = full * z;
-                    f[j] = full;
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) vs[(16 * b + j) * x.rows] = __float2bfloat16_rn(f[j]);
-                load16(g, sc + kScG * kGdC + 16 * s);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] *= -g[j];
-                put_terms<2>(t0 + C::Y + 16 * s, f);
+                for (int j = 0; j < 8; ++j) g.p[j] = f2_mul(g.p[j], f2_splat(-1.f));
+                put_terms<2>(t0 + C::Y + 16 * (s + b), g);
+                const Cols16 v = load_row16(vs + 16 * b * x.rows, x.rows, left - 16 * b);
+                store_row16(vs + 16 * b * x.rows, x.rows, full);
+                // dv.y + dvs.z = dvs.v + (dv - dvs).y
+                split_pairs(s1, b, fma16(f, v, d[b] * y[b]));
+                split_pairs(s2, b, full * (v - y[b]));
             }
             warp_done(&B.w, lane);
-            const float gl = sc[kScG * kGdC + kGdC - 1];
+            const float gl = sc[kScG * kGdC + kGdC - 1 - 16 * s];
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -751,23 +670,13 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             ok = warp_wait(&B.ds, ph, ctl);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < HS / 16; ++k) {
-                float f[16];
-                get16(f, t0 + C::D + half * HS + 16 * k);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) E[16 * k + j] = fmaf(gl, E[16 * k + j], f[j]);
-            }
+            add_cols<HS>(E, t0 + C::D + half * HS, gl);
             if (i + 1 < x.nc) {
                 put_grad();
                 warp_done(&B.s, lane);
             }
         }
-        if (ok && p.ds0) {
-            float* s = p.ds0 + (x.nh * DK + half * HS) * p.dv + r;
-#pragma unroll
-            for (int i = 0; i < HS; ++i) s[static_cast<int64_t>(i) * p.dv] = E[i];
-        }
+        if (ok && p.ds0) store_state<HS>(E, p.ds0 + (x.nh * DK + half * HS) * p.dv + r, p.dv);
     }
     tc_fence_before();
     __syncthreads();

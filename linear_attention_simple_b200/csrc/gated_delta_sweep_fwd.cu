@@ -247,123 +247,69 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
         const int half = warp >> 2, r = w0 + (warp & 3) * 32 + lane;
         const uint32_t t0 = tm + (static_cast<uint32_t>(warp & 3) << 21);       // lane quarter
         constexpr int HS = DK / 2;                                              // state columns of a thread
-        float S[HS];
-        const float* s0 = p.s0 ? p.s0 + (nh * DK + half * HS) * p.dv + r : nullptr;
-#pragma unroll
-        for (int i = 0; i < HS; ++i) S[i] = s0 ? s0[static_cast<int64_t>(i) * p.dv] : 0.f;
+        f2 S[HS / 2];
+        load_state<HS>(S, p.s0 ? p.s0 + (nh * DK + half * HS) * p.dv + r : nullptr, p.dv);
         auto put_state = [&]() {
 #pragma unroll
-            for (int k = 0; k < HS / 16; ++k) {
-                float x[16];
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = S[16 * k + i];
-                split16(x, hi, lo);
-                tmem_st8(t0 + C::S + half * HS + 16 * k, hi);
-                tmem_st8(t0 + C::S + half * HS + 16 * k + 8, lo);
-            }
-        };
-        auto done = [&](uint64_t* bar) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
+            for (int k = 0; k < HS / 16; ++k) put_terms<2>(t0 + C::S + half * HS + 16 * k, cols_of<HS>(S, k));
         };
         if (nc > 0) {
             put_state();
-            done(&B.s);
+            warp_done(&B.s, lane);
         }
         bool ok = true;
         for (int c = 0; c < nc; ++c) {
-            const int ph = c & 1;
-            const float* sc = reinterpret_cast<const float*>(smem + ph * M::KSC + Rec::SC);
-            __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(smem + M::V) + ph * kGdC * sw + half * 32 * rows +
+            const int ph = c & 1, s = 2 * half;              // this thread's steps of 16 tokens: s and s + 1
+            const float* sc = reinterpret_cast<const float*>(smem + ph * M::KSC + Rec::SC) + 16 * s;
+            __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(smem + M::V) + ph * kGdC * sw + 16 * s * rows +
                                 (warp & 3) * 32 + lane;                       // this row's 32 tokens
-            const int left = len - c * kGdC - half * 32;                      // tokens of those in the sequence
+            const int left = len - c * kGdC - 16 * s;                         // tokens of those in the sequence
             ok = warp_wait(&B.full[ph], (c >> 1) & 1, ctl) && warp_wait(&B.y, ph, ctl);
             if (!ok) break;
             tc_fence_after();
+            Cols16 x[2];
+            get16x2(x[0], x[1], t0 + C::Y + 16 * s, t0 + C::Y + 16 * s + 16);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int s = half * 2 + b;
-                float x[16], G[16];
-                uint32_t hi[8], lo[8];
-                load16(G, sc + kScG * kGdC + 16 * s);
-                get16(x, t0 + C::Y + 16 * s);
-                // rows behind the sequence's end: what lies in the slice is not V
-                if (left >= 32) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = fmaf(-G[i], x[i], __bfloat162float(vs[(16 * b + i) * rows]));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        x[i] = 16 * b + i < left ? fmaf(-G[i], x[i], __bfloat162float(vs[(16 * b + i) * rows])) : 0.f;
-                }
-                split16(x, hi, lo);
-                tmem_st8(t0 + C::Y + 16 * s, hi);
-                tmem_st8(t0 + C::Y + 16 * s + 8, lo);
-            }
-            done(&B.r);
+            for (int b = 0; b < 2; ++b)
+                put_terms<2>(t0 + C::Y + 16 * (s + b),
+                             load_row16(vs + 16 * b * rows, rows, left - 16 * b) - load16(sc + kScG * kGdC + 16 * b) * x[b]);
+            warp_done(&B.r, lane);
             ok = warp_wait(&B.z, ph, ctl);
             if (!ok) break;
             tc_fence_after();
+            get16x2(x[0], x[1], t0 + C::S + 16 * s, t0 + C::S + 16 * s + 16);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int s = half * 2 + b;
-                float x[16], f[16];
-                uint32_t hi[8], lo[8];
-                get16(x, t0 + C::S + 16 * s);
-                load16(f, sc + kScBeta * kGdC + 16 * s);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] *= f[i];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) hi[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-                tmem_st8(t0 + C::V + 8 * s, hi);
-                load16(f, sc + kScR * kGdC + 16 * s);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] *= f[i];
-                split16(x, hi, lo);
-                tmem_st8(t0 + C::Y + 16 * s, hi);
-                tmem_st8(t0 + C::Y + 16 * s + 8, lo);
+                x[b] = x[b] * load16(sc + kScBeta * kGdC + 16 * b);
+                put_terms<1>(t0 + C::V + 8 * (s + b), x[b]);
+                put_terms<2>(t0 + C::Y + 16 * (s + b), x[b] * load16(sc + kScR * kGdC + 16 * b));
             }
-            done(&B.w);
-            const float gl = sc[kScG * kGdC + kGdC - 1];
+            warp_done(&B.w, lane);
+            const float gl = sc[kScG * kGdC + kGdC - 1 - 16 * s];
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.empty[ph]);          // the scalars are read
             ok = warp_wait(&B.ds, ph, ctl);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < HS / 16; ++k) {
-                float x[16];
-                get16(x, t0 + C::S + half * HS + 16 * k);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) S[16 * k + i] = fmaf(gl, S[16 * k + i], x[i]);
-            }
+            add_cols<HS>(S, t0 + C::S + half * HS, gl);
             if (c + 1 < nc) {
                 put_state();
-                done(&B.s);
+                warp_done(&B.s, lane);
             }
             ok = warp_wait(&B.out, ph, ctl);
             if (!ok) break;
             tc_fence_after();
-            uint32_t x[32];
-            tmem_ld32(t0 + C::O + half * 32, x);
-            tmem_ld_wait();
+            get16x2(x[0], x[1], t0 + C::O + 16 * s, t0 + C::O + 16 * s + 16);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) vs[i * rows] = __float2bfloat16_rn(__uint_as_float(x[i]));
+            for (int b = 0; b < 2; ++b) store_row16(vs + 16 * b * rows, rows, x[b]);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.staged[ph]);
         }
-        if (ok && p.s_final) {
-            float* s = p.s_final + (nh * DK + half * HS) * p.dv + r;
-#pragma unroll
-            for (int i = 0; i < HS; ++i) s[static_cast<int64_t>(i) * p.dv] = S[i];
-        }
+        if (ok && p.s_final) store_state<HS>(S, p.s_final + (nh * DK + half * HS) * p.dv + r, p.dv);
     }
     tc_fence_before();
     __syncthreads();
