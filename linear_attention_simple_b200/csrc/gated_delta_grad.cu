@@ -32,9 +32,10 @@ constexpr int kVs = kSl + kGdPad;          // row stride of a staged token slice
 template <int DK>
 struct GradSmem {
     static constexpr int KS = DK + kGdPad;
-    static constexpr int tok = kGdC * kVs;             // one staged token slice
+    static constexpr int tok = kGdC * kVs;             // one staged token slice of dO or dv
+    static constexpr int vt = kSl * (kGdC + kGdPad);   // and of V', which lies transposed
     static constexpr int st = kSl * KS;                // one staged state slice
-    static constexpr int stage1 = 3 * tok, stage2 = 3 * tok + 2 * st;
+    static constexpr int stage1 = 2 * tok + vt, stage2 = stage1 + 2 * st;
     // elements: the first pass's stages, later A and B; then K and Q; the
     // second pass's stages over all of them
     static constexpr int ab = kGdC * (kGdC + kGdPad);
@@ -56,9 +57,12 @@ __device__ __forceinline__ void load_slice(__nv_bfloat16* st, const Src& x, int 
     constexpr int KS = GradSmem<DK>::KS, tok = GradSmem<DK>::tok;
     gd_load_rows(st, kVs, x.d + col, x.ld_do, kSl, x.valid, tid, kThreads);
     gd_load_rows(st + tok, kVs, x.y + col, x.ld_dv, kSl, x.valid, tid, kThreads);
-    gd_load_rows(st + 2 * tok, kVs, x.vp + col, x.dv, kSl, kGdC, tid, kThreads);
+    for (int i = tid; i < kSl * (kGdC / 8); i += kThreads) {
+        const int r = i >> 3, c = (i & 7) * 8;
+        cp_async16(st + 2 * tok + r * (kGdC + kGdPad) + c, x.vp + static_cast<int64_t>(col + r) * kGdC + c, true);
+    }
     if (states) {
-        __nv_bfloat16* ss = st + 3 * tok;
+        __nv_bfloat16* ss = st + GradSmem<DK>::stage1;
         for (int i = tid; i < 2 * kSl * (DK / 8); i += kThreads) {
             const int which = i / (kSl * (DK / 8)), j = i - which * (kSl * (DK / 8));
             const int r = j / (DK / 8), c = (j - r * (DK / 8)) * 8;
@@ -140,8 +144,8 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
             cp_async_commit();
             const __nv_bfloat16* st = sst + (i & 1) * M::stage1;
             const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
-            const uint32_t br = smem_u32(st + 2 * M::tok + rows_n(lane, kVs));
-            constexpr int tk = M::tok * 2, rp = 16 * kVs * 2;
+            const uint32_t br = smem_u32(st + 2 * M::tok + rows_k(lane, AS));
+            constexpr int tk = M::tok * 2;
 #pragma unroll
             for (int s = 0; s < kSl / 16; ++s) {
                 uint32_t d[4], y[4];
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
                 for (int np = 0; np < 4; ++np) {
                     if (np > w) continue;
                     uint32_t b[4];
-                    ldsm4(b, br + np * rp + s * 32);
+                    ldsm4_t(b, br + s * 16 * AS * 2 + np * 32);
                     mma_bf16(fa[2 * np], d, b[0], b[1]);
                     mma_bf16(fa[2 * np + 1], d, b[2], b[3]);
                     mma_bf16(fb[2 * np], y, b[0], b[1]);
@@ -295,14 +299,15 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
             cp_async_commit();
             const __nv_bfloat16* st = sst + (i & 1) * M::stage2;
             const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
-            const uint32_t sr = smem_u32(st + 3 * M::tok + rows_k(lane, KS));
+            const uint32_t vr = smem_u32(st + 2 * M::tok + 16 * w + rows_at(lane, AS));
+            const uint32_t sr = smem_u32(st + M::stage1 + rows_k(lane, KS));
             constexpr int tk = M::tok * 2;
 #pragma unroll
             for (int s = 0; s < kSl / 16; ++s) {
                 uint32_t d[4], y[4], v[4];
                 ldsm4(d, ar + s * 32);
                 ldsm4(y, ar + tk + s * 32);
-                ldsm4(v, ar + 2 * tk + s * 32);
+                ldsm4_t(v, vr + s * 16 * AS * 2);
                 scale_a(d, p.scale * G0, p.scale * G1);
                 scale_a(y, -G0, -G1);
                 scale_a(v, R0, R1);

@@ -52,19 +52,23 @@ constexpr uint32_t kAlloc = 512;
 struct __align__(8) Bars {
     uint64_t full[2], empty[2];                 // K, scalars, V and dO
     uint64_t fq, ft, fp, eq, et, ep;            // Q, T, P
-    uint64_t staged[2];                         // workers -> copies: V' or dv is in the V slice
+    uint64_t staged[2];                         // workers -> copies: dv is in the V slice (reverse)
     uint64_t s, r, w, o, x[2];                  // workers -> issuer
     uint64_t y, z, ds, out, drain;              // issuer -> workers
+    uint64_t yin[kGdWorkers];                   // reverse: this warp's y is in its buffer
     uint32_t tmem;
 };
+
+// y of a warp's 32 rows and 32 tokens: pieces of 4 tokens, [8][32 lanes][4].
+constexpr int kYBytes = 32 * 32 * 4;
 
 template <int DK>
 struct Smem {
     using Rec = GdRec<DK, true>;
     static constexpr int KSC = (Rec::KSC + 1023) / 1024 * 1024;
     static constexpr int Q = 2 * KSC, T = Q + 2 * DK * 128, P = T + 16384, V = P + 16384;
-    // V and dO slices of two stages behind V
-    static constexpr int bytes(int sw) { return V + 4 * kGdC * sw * 2 + 1024; }
+    // V and dO slices of two stages behind V, then y of each worker warp
+    static constexpr int bytes(int sw) { return V + 4 * kGdC * sw * 2 + kGdWorkers * kYBytes + 1024; }
 };
 
 struct Cta {
@@ -110,6 +114,7 @@ __device__ __forceinline__ bool setup(Cta& x, Bars& B, const GdParams& p, int sw
             mbar_init(&B.staged[i], x.active);
             mbar_init(&B.x[i], x.active);
         }
+        for (int i = 0; i < kGdWorkers; ++i) mbar_init(&B.yin[i], 1);
         uint64_t* single[11] = {&B.fq, &B.ft, &B.fp, &B.eq, &B.et, &B.ep, &B.y, &B.z, &B.ds, &B.out, &B.drain};
         for (uint64_t* b : single) mbar_init(b, 1);
         uint64_t* from_workers[4] = {&B.s, &B.r, &B.w, &B.o};
@@ -127,11 +132,10 @@ __device__ __forceinline__ bool setup(Cta& x, Bars& B, const GdParams& p, int sw
 }
 
 // The copy warp's work (one lane): step i = 0 .. nc - 1 is chunk i, or nc - 1 - i
-// in reverse.  What the workers stage in the V slice goes to out, whose row of
-// chunk c is out_row0 + c * out_step; whole: all 64 rows of every chunk leave.
+// in reverse, where the workers leave dv in the V slice for it to take away.
 template <int DK, bool REV>
 __device__ void copies(const Cta& x, Bars& B, const GdParams& p, const CUtensorMap* mv, const CUtensorMap* md,
-                       const CUtensorMap* mo, int64_t out_row0, int64_t out_step, int out_col, const WaitCtl& ctl)
+                       const CUtensorMap* mo, const WaitCtl& ctl)
 {
     using M = Smem<DK>;
     using Rec = GdRec<DK, true>;
@@ -154,13 +158,13 @@ __device__ void copies(const Cta& x, Bars& B, const GdParams& p, const CUtensorM
     auto out = [&](int i) {                                  // false: the wait ran out
         const int st = i & 1, c = chunk(i), valid = x.len - c * kGdC;
         if (!mbar_wait(&B.staged[st], (i >> 1) & 1, ctl)) return false;
-        const int64_t row = out_row0 + c * out_step;
-        if (!REV || valid >= kGdC) {
-            tma_store_2d(mo, x.slice(0, st), out_col, static_cast<int>(row));
+        const int64_t row = x.row0 + static_cast<int64_t>(c) * kGdC;
+        if (valid >= kGdC) {
+            tma_store_2d(mo, x.slice(0, st), col, static_cast<int>(row));
         } else {                                             // the rows behind are another sequence's
             const int64_t ld = static_cast<int64_t>(p.seqs.H) * p.dv;
             for (int r = 0; r < valid; ++r)
-                bulk_store(p.dvv + (row + r) * ld + out_col, x.slice(0, st) + r * x.rows * 2, x.rows * 2);
+                bulk_store(p.dvv + (row + r) * ld + col, x.slice(0, st) + r * x.rows * 2, x.rows * 2);
         }
         tma_store_commit();
         tma_store_wait_read();
@@ -188,12 +192,12 @@ __device__ void copies(const Cta& x, Bars& B, const GdParams& p, const CUtensorM
             ++pp;
         }
         if (i > 0) {
-            ok = out(i - 1) && (i + 1 >= x.nc || mbar_wait(&B.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, ctl));
+            ok = (!REV || out(i - 1)) && (i + 1 >= x.nc || mbar_wait(&B.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, ctl));
             if (!ok) break;
         }
         if (i + 1 < x.nc) first(a++);
     }
-    if (ok && x.nc > 0) out(x.nc - 1);
+    if (REV && ok && x.nc > 0) out(x.nc - 1);
     // no copy may be in flight when the block ends
     tma_store_wait_read();
     for (int i = max(0, a - 2); i < a; ++i) mbar_wait(&B.full[i & 1], (i >> 1) & 1, ctl);
@@ -244,7 +248,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 template <int DK>
 __global__ void __launch_bounds__(kGdThreads, 1)
 gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __grid_constant__ GdMap map_d,
-                     const __grid_constant__ GdMap map_vp, int sw, int nslices, WaitCtl ctl)
+                     const __grid_constant__ GdMap, int sw, int nslices, WaitCtl ctl)
 {
     using C = FwdCols<DK>;
     using M = Smem<DK>;
@@ -255,13 +259,10 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
     if (!setup<DK>(x, B, p, sw, nslices, smem_raw)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t tm = B.tmem;
-
     if (warp == kGdWorkers) {
         if (lane == 0) {
             const bool whole = x.rows == sw;
-            copies<DK, false>(x, B, p, whole ? &map_v.all : &map_v.last, whole ? &map_d.all : &map_d.last,
-                              whole ? &map_vp.all : &map_vp.last, x.u0 * kGdC,
-                              static_cast<int64_t>(p.seqs.H) * kGdC, x.w0, ctl);
+            copies<DK, false>(x, B, p, whole ? &map_v.all : &map_v.last, whole ? &map_d.all : &map_d.last, nullptr, ctl);
         }
     } else if (warp == kGdWorkers + 1) {
         if (lane == 0) {
@@ -281,17 +282,6 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
                     umma_bf16_ts(tm + C::Y, tm + C::S + 16 * k + 8, b, id64, 1);
                 }
                 umma_commit(&B.y);
-                if (c > 0 && !mbar_wait(&B.o, (c - 1) & 1, ctl)) break;
-                if (!mbar_wait(&B.fq, c & 1, ctl)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k) {
-                    const uint64_t hi = desc_add(q_k, (k >> 1) * 4096 + (k & 1) * 32), lo = desc_add(hi, DK * 128);
-                    umma_bf16_ts(tm + C::O, tm + C::S + 16 * k, hi, id64, k > 0);
-                    umma_bf16_ts(tm + C::O, tm + C::S + 16 * k + 8, hi, id64, 1);
-                    umma_bf16_ts(tm + C::O, tm + C::S + 16 * k, lo, id64, 1);
-                }
-                umma_commit(&B.eq);
                 if (!mbar_wait(&B.ft, c & 1, ctl) || !mbar_wait(&B.r, c & 1, ctl)) break;
                 tc_fence_after();
                 // strictly lower triangular: step s reaches tokens 16 s on
@@ -306,6 +296,18 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
                 }
                 umma_commit(&B.z);
                 umma_commit(&B.et);
+                // o' of the state: while the workers turn z into V'
+                if (c > 0 && !mbar_wait(&B.o, (c - 1) & 1, ctl)) break;
+                if (!mbar_wait(&B.fq, c & 1, ctl)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k) {
+                    const uint64_t hi = desc_add(q_k, (k >> 1) * 4096 + (k & 1) * 32), lo = desc_add(hi, DK * 128);
+                    umma_bf16_ts(tm + C::O, tm + C::S + 16 * k, hi, id64, k > 0);
+                    umma_bf16_ts(tm + C::O, tm + C::S + 16 * k + 8, hi, id64, 1);
+                    umma_bf16_ts(tm + C::O, tm + C::S + 16 * k, lo, id64, 1);
+                }
+                umma_commit(&B.eq);
                 if (!mbar_wait(&B.w, c & 1, ctl)) break;
                 tc_fence_after();
 #pragma unroll
@@ -360,7 +362,7 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
             const int64_t u = x.u0 + static_cast<int64_t>(c) * p.seqs.H;
             const float* sc = reinterpret_cast<const float*>(x.smem + ph * M::KSC + Rec::SC) + 16 * s;
             const int at = 16 * s * x.rows + (warp & 3) * 32 + lane;          // this row's 32 tokens in a slice
-            __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(x.slice(0, ph)) + at;
+            const __nv_bfloat16* vs = reinterpret_cast<const __nv_bfloat16*>(x.slice(0, ph)) + at;
             const __nv_bfloat16* ds = reinterpret_cast<const __nv_bfloat16*>(x.slice(1, ph)) + at;
             const int left = x.len - c * kGdC - 16 * s;
             ok = warp_wait(&B.full[ph], (c >> 1) & 1, ctl);
@@ -394,24 +396,23 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
             }
             warp_done(&B.w, lane);
             const float gl = sc[kScG * kGdC + kGdC - 1 - 16 * s];
-            float* yn = p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32) + lane * 4;
             Cols16 d[2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                d[b] = load_row16(ds + 16 * b * x.rows, x.rows, left - 16 * b);
-                store_row16(vs + 16 * b * x.rows, x.rows, v[b]);
-            }
-            fence_async_smem();
+            for (int b = 0; b < 2; ++b) d[b] = load_row16(ds + 16 * b * x.rows, x.rows, left - 16 * b);
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&B.staged[ph]);
-                mbar_arrive(&B.empty[ph]);                   // scalars, V and dO are read
-            }
+            if (lane == 0) mbar_arrive(&B.empty[ph]);        // scalars, V and dO are read
+            float* yn = p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32) + lane * 4;
+            __nv_bfloat16* vp = p.vp + (u * p.dv + r) * kGdC + 16 * s;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < 2; ++b) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = f2_to_bf16x2(v[b].p[i]);
+                st_global_v8(vp + 16 * b, w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<ulonglong2*>(yn + (16 * b + 4 * i) * 32) = make_ulonglong2(y[b].p[2 * i].v, y[b].p[2 * i + 1].v);
+            }
             if (c > 0 && (c & 1) == 0) keep(p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32) + lane * 4);
             ok = warp_wait(&B.ds, ph, ctl);
             if (!ok) break;
@@ -455,12 +456,11 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
     if (!setup<DK>(x, B, p, sw, nslices, smem_raw)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t tm = B.tmem;
-
     if (warp == kGdWorkers) {
         if (lane == 0) {
             const bool whole = x.rows == sw;
             copies<DK, true>(x, B, p, whole ? &map_v.all : &map_v.last, whole ? &map_d.all : &map_d.last,
-                             whole ? &map_dv.all : &map_dv.last, x.row0, kGdC, x.h * p.dv + x.w0, ctl);
+                             whole ? &map_dv.all : &map_dv.last, ctl);
         }
     } else if (warp == kGdWorkers + 1) {
         if (lane == 0) {
@@ -525,6 +525,7 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
         }
     } else if ((warp & 3) * 32 < x.rows) {
         const int half = warp >> 2, r = x.w0 + (warp & 3) * 32 + lane, wr = r >> 5, nwr = p.dv >> 5;
+        unsigned char* ybuf = x.slices + 4 * kGdC * x.sw * 2 + warp * kYBytes;
         const uint32_t t0 = tm + (static_cast<uint32_t>(warp & 3) << 21);
         constexpr int HS = DK / 2;
         const int s = 2 * half;                              // this thread's steps of 16 tokens: s and s + 1
@@ -576,15 +577,15 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(x.slice(0, ph)) + at;
             const int left = x.len - c * kGdC - 16 * s;
             // while the first products run: <E, state leaving> (the sum of da's
-            // terms over all later tokens; after every second chunk), E rounded,
-            // and y from the forward; the next step's into L2
-            if (i + 1 < x.nc) {
-                const int64_t un = u - p.seqs.H;
-                prefetch_l2(p.yn + ((un * nwr + wr) * 2 + half) * (32 * 32) + lane * 32);
-                if ((c & 1) == 0) {
-                    const float* b = p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32);
-                    for (int k = lane; k < HS; k += 32) prefetch_l2(b + k * 32);
-                }
+            // terms over all later tokens; after every second chunk, the next one
+            // into L2) and E rounded; y of the forward is on its way
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&B.yin[warp], kYBytes);
+                bulk_load(ybuf, p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32), kYBytes, &B.yin[warp]);
+            }
+            if (i + 1 < x.nc && (c & 1) == 0) {
+                const float* b = p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32);
+                for (int k = lane; k < HS; k += 32) prefetch_l2(b + k * 32);
             }
             float dot = 0.f;
             if (i > 0 ? (c & 1) == 1 : p.ds_final != nullptr) {
@@ -606,16 +607,7 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             }
             if (lane == 0) p.anch[(u * nwr + wr) * 2 + half] = dot;
             store_half_row<HS>(p.eb + (u * p.dv + r) * DK + half * HS, E);
-            Cols16 y[2], d[2];
-            const float* yp = p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32) + lane * 4;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const ulonglong2 w = __ldcs(reinterpret_cast<const ulonglong2*>(yp + (16 * b + 4 * k) * 32));
-                    y[b].p[2 * k].v = w.x;
-                    y[b].p[2 * k + 1].v = w.y;
-                }
+            Cols16 d[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const Cols16 f = load16(sc + kScBeta * kGdC + 16 * b) * load16(sc + kScPd * kGdC + 16 * b);
@@ -639,7 +631,7 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 if (!ok) break;
                 put_dO(i + 1);
             }
-            ok = warp_wait(&B.z, ph, ctl);
+            ok = warp_wait(&B.yin[warp], i & 1, ctl) && warp_wait(&B.z, ph, ctl);
             if (!ok) break;
             tc_fence_after();
             float s1[32], s2[32];
@@ -652,9 +644,16 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 put_terms<2>(t0 + C::Y + 16 * (s + b), g);
                 const Cols16 v = load_row16(vs + 16 * b * x.rows, x.rows, left - 16 * b);
                 store_row16(vs + 16 * b * x.rows, x.rows, full);
+                Cols16 y;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(ybuf + (4 * b + k) * 512 + lane * 16);
+                    y.p[2 * k].v = w.x;
+                    y.p[2 * k + 1].v = w.y;
+                }
                 // dv.y + dvs.z = dvs.v + (dv - dvs).y
-                split_pairs(s1, b, fma16(f, v, d[b] * y[b]));
-                split_pairs(s2, b, full * (v - y[b]));
+                split_pairs(s1, b, fma16(f, v, d[b] * y));
+                split_pairs(s2, b, full * (v - y));
             }
             warp_done(&B.w, lane);
             const float gl = sc[kScG * kGdC + kGdC - 1 - 16 * s];
@@ -702,15 +701,14 @@ gla_status both(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
     const GdSlices sl(p.dv);
     const int64_t width = static_cast<int64_t>(p.seqs.H) * p.dv;
     const int64_t tokens = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;
-    GdMap v, d, vp, dv;
+    GdMap v, d, dv;
     gla_status s;
     if ((s = gd_slice_map(&v, p.v, width, p.ld_v, tokens, sl.width, sl.last)) != GLA_OK ||
         (s = gd_slice_map(&d, p.dO, width, p.ld_do, tokens, sl.width, sl.last)) != GLA_OK ||
-        (s = gd_slice_map(&vp, p.vp, p.dv, p.dv, p.slots * p.seqs.H * kGdC, sl.width, sl.last)) != GLA_OK ||
         (s = gd_slice_map(&dv, p.dvv, width, width, tokens, sl.width, sl.last)) != GLA_OK)
         return s;
     const int smem = Smem<DK>::bytes(sl.width);
-    if ((s = start(gd_sweep_keep_kernel<DK>, "gd_sweep_keep_kernel", p, smem, v, d, vp, sl, ctl, st)) != GLA_OK) return s;
+    if ((s = start(gd_sweep_keep_kernel<DK>, "gd_sweep_keep_kernel", p, smem, v, d, dv, sl, ctl, st)) != GLA_OK) return s;
     return start(gd_sweep_rev_kernel<DK>, "gd_sweep_rev_kernel", p, smem, v, d, dv, sl, ctl, st);
 }
 

@@ -193,9 +193,13 @@ template <int HS>
 __device__ __forceinline__ void add_cols(f2 (&S)[HS / 2], uint32_t taddr, float f)
 {
     const f2 g = f2_splat(f);
+    uint32_t r[HS / 16][16];
+#pragma unroll
+    for (int k = 0; k < HS / 16; ++k) tmem_ld16(taddr + 16 * k, r[k]);
+    tmem_ld_wait();
 #pragma unroll
     for (int k = 0; k < HS / 16; ++k) {
-        const Cols16 x = get16(taddr + 16 * k);
+        const Cols16 x = cols16(r[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) S[8 * k + i] = f2_fma(g, S[8 * k + i], x.p[i]);
     }
