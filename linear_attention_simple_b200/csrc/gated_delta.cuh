@@ -29,6 +29,7 @@ constexpr int kGdC = 64;                 // tokens per chunk
 constexpr int kGdPad = 8;                // bf16 elements behind each shared-memory row: rows an odd
                                          // multiple of 16 bytes apart, so ldmatrix has no bank conflicts
 constexpr int kGdTP = kGdC + kGdPad;     // row stride of a shared T or P tile
+constexpr int kGdPiece = 32 * 8;         // a piece: 8 values of each of 32 dv rows
 constexpr int kGdSc = 6;                 // per-token scalars of a chunk: G, R, beta, P_ii, b (high, low)
 enum { kScG = 0, kScR = 1, kScBeta = 2, kScPd = 3, kScBh = 4, kScBl = 5 };
 
@@ -184,11 +185,11 @@ struct GdParams {
     // workspace, one entry per chunk slot and value head (u = slot * H + h)
     unsigned char* rec;     // [u]: GdRec
     // backward only; a "half row" is a thread's: one dv row, half of the columns
-    __nv_bfloat16 *sb, *eb; // [u][dv][dk]: the state entering, the gradient of the state leaving
+    __nv_bfloat16 *sb, *eb; // [u][dv / 32][dk / 8][32][8]: the state entering, the gradient of the state leaving
     float* sn;              // [u][dv / 32][2][dk / 8][32 lanes][4]: the state entering in fp32, half rows
     float* sn_last;         // [N H][..]: the final state in the same form
     float* yn;              // [u][dv / 32][2][8][32 lanes][4]: y, half rows
-    __nv_bfloat16* vp;      // [u][dv][64]: V', transposed
+    __nv_bfloat16* vp;      // [u][dv / 32][8][32][8 tokens]: V'
     float* part;            // [u][3][dv / 32][64]: sums over 32 dv rows, per token
     float* anch;            // [u][dv / 32][2]: <gradient of the state leaving, state leaving>
     int64_t slots;

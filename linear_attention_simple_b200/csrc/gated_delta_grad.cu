@@ -26,6 +26,7 @@ namespace gla {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kMaxWarps = 8;               // of 32 dv rows (dv <= 256)
 constexpr int kSl = 32;                    // dv columns per stage
 constexpr int kVs = kSl + kGdPad;          // row stride of a staged token slice
 
@@ -33,8 +34,10 @@ template <int DK>
 struct GradSmem {
     static constexpr int KS = DK + kGdPad;
     static constexpr int tok = kGdC * kVs;             // one staged token slice of dO or dv
-    static constexpr int vt = kSl * (kGdC + kGdPad);   // and of V', which lies transposed
-    static constexpr int st = kSl * KS;                // one staged state slice
+    // V' and the states as they lie in memory, in pieces of 8 values of 32 dv
+    // rows: 16 bytes a row, so that ldmatrix meets every bank once
+    static constexpr int vt = kSl * kGdC;
+    static constexpr int st = kSl * DK;
     static constexpr int stage1 = 2 * tok + vt, stage2 = stage1 + 2 * st;
     // elements: the first pass's stages, later A and B; then K and Q; the
     // second pass's stages over all of them
@@ -57,20 +60,22 @@ __device__ __forceinline__ void load_slice(__nv_bfloat16* st, const Src& x, int 
     constexpr int KS = GradSmem<DK>::KS, tok = GradSmem<DK>::tok;
     gd_load_rows(st, kVs, x.d + col, x.ld_do, kSl, x.valid, tid, kThreads);
     gd_load_rows(st + tok, kVs, x.y + col, x.ld_dv, kSl, x.valid, tid, kThreads);
-    for (int i = tid; i < kSl * (kGdC / 8); i += kThreads) {
-        const int r = i >> 3, c = (i & 7) * 8;
-        cp_async16(st + 2 * tok + r * (kGdC + kGdPad) + c, x.vp + static_cast<int64_t>(col + r) * kGdC + c, true);
-    }
+    __nv_bfloat16* sv = st + 2 * tok;
+    for (int i = tid; i < GradSmem<DK>::vt / 8; i += kThreads)
+        cp_async16(sv + 8 * i, x.vp + static_cast<int64_t>(col) * kGdC + 8 * i, true);
     if (states) {
+        constexpr int n = GradSmem<DK>::st / 8;
         __nv_bfloat16* ss = st + GradSmem<DK>::stage1;
-        for (int i = tid; i < 2 * kSl * (DK / 8); i += kThreads) {
-            const int which = i / (kSl * (DK / 8)), j = i - which * (kSl * (DK / 8));
-            const int r = j / (DK / 8), c = (j - r * (DK / 8)) * 8;
-            cp_async16(ss + which * GradSmem<DK>::st + r * KS + c,
-                       (which ? x.e : x.s) + static_cast<int64_t>(col + r) * DK + c, true);
+        for (int i = tid; i < n; i += kThreads) {
+            cp_async16(ss + 8 * i, x.s + static_cast<int64_t>(col) * DK + 8 * i, true);
+            cp_async16(ss + 8 * (n + i), x.e + static_cast<int64_t>(col) * DK + 8 * i, true);
         }
     }
 }
+
+// The rows_k and rows_at patterns on pieces.
+__device__ __forceinline__ int piece_k(int lane) { return (lane >> 4) * kGdPiece + ((lane & 7) + (((lane >> 3) & 1) << 3)) * 8; }
+__device__ __forceinline__ int piece_at(int lane) { return ((lane >> 3) & 1) * kGdPiece + ((lane & 7) + ((lane >> 4) << 3)) * 8; }
 
 // A left operand's rows g and g + 8 times f0 and f1.
 __device__ __forceinline__ void scale_a(uint32_t (&r)[4], float f0, float f1)
@@ -144,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
             cp_async_commit();
             const __nv_bfloat16* st = sst + (i & 1) * M::stage1;
             const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
-            const uint32_t br = smem_u32(st + 2 * M::tok + rows_k(lane, AS));
+            const uint32_t br = smem_u32(st + 2 * M::tok + piece_k(lane));
             constexpr int tk = M::tok * 2;
 #pragma unroll
             for (int s = 0; s < kSl / 16; ++s) {
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
                 for (int np = 0; np < 4; ++np) {
                     if (np > w) continue;
                     uint32_t b[4];
-                    ldsm4_t(b, br + s * 16 * AS * 2 + np * 32);
+                    ldsm4_t(b, br + s * 256 + np * 4 * kGdPiece);
                     mma_bf16(fa[2 * np], d, b[0], b[1]);
                     mma_bf16(fa[2 * np + 1], d, b[2], b[3]);
                     mma_bf16(fb[2 * np], y, b[0], b[1]);
@@ -173,7 +178,9 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
             const bool between = (c & 1) == 0 && (c + 1) * kGdC < len;
             float2 od = make_float2(0.f, 0.f), s1 = od, s2 = od;
             float tail = 0.f, next = 0.f;
-            for (int t = 0; t < wtot; ++t) {
+#pragma unroll
+            for (int t = 0; t < kMaxWarps; ++t) {          // all loads at once
+                if (t >= wtot) continue;
                 const float2 a = *reinterpret_cast<const float2*>(part + t * kGdC);
                 const float2 b = *reinterpret_cast<const float2*>(part + (wtot + t) * kGdC);
                 const float2 e = *reinterpret_cast<const float2*>(part + (2 * wtot + t) * kGdC);
@@ -299,23 +306,23 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
             cp_async_commit();
             const __nv_bfloat16* st = sst + (i & 1) * M::stage2;
             const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
-            const uint32_t vr = smem_u32(st + 2 * M::tok + 16 * w + rows_at(lane, AS));
-            const uint32_t sr = smem_u32(st + M::stage1 + rows_k(lane, KS));
+            const uint32_t vr = smem_u32(st + 2 * M::tok + 2 * w * kGdPiece + piece_at(lane));
+            const uint32_t sr = smem_u32(st + M::stage1 + piece_k(lane));
             constexpr int tk = M::tok * 2;
 #pragma unroll
             for (int s = 0; s < kSl / 16; ++s) {
                 uint32_t d[4], y[4], v[4];
                 ldsm4(d, ar + s * 32);
                 ldsm4(y, ar + tk + s * 32);
-                ldsm4_t(v, vr + s * 16 * AS * 2);
+                ldsm4_t(v, vr + s * 256);
                 scale_a(d, p.scale * G0, p.scale * G1);
                 scale_a(y, -G0, -G1);
                 scale_a(v, R0, R1);
 #pragma unroll
                 for (int np = 0; np < DK / 16; ++np) {
                     uint32_t sf[4], ef[4];
-                    ldsm4_t(sf, sr + s * 16 * KS * 2 + np * 32);
-                    ldsm4_t(ef, sr + M::st * 2 + s * 16 * KS * 2 + np * 32);
+                    ldsm4_t(sf, sr + s * 256 + np * 4 * kGdPiece);
+                    ldsm4_t(ef, sr + M::st * 2 + s * 256 + np * 4 * kGdPiece);
                     mma_bf16(dq[2 * np], d, sf[0], sf[1]);
                     mma_bf16(dq[2 * np + 1], d, sf[2], sf[3]);
                     mma_bf16(dk[2 * np], y, sf[0], sf[1]);
