@@ -192,6 +192,10 @@ struct GdParams {
     __nv_bfloat16* vp;      // [u][dv / 32][8][32][8 tokens]: V'
     float* part;            // [u][3][dv / 32][64]: sums over 32 dv rows, per token
     float* anch;            // [u][dv / 32][2]: <gradient of the state leaving, state leaving>
+    // forward: segments of seg_chunks chunks, at most nseg of a sequence; per
+    // (sequence, head, segment) the state that enters [dk][dv], and A [dk][dk]
+    int nseg, seg_chunks;
+    float *seg_l, *seg_a;
     int64_t slots;
     int* status;
 };

@@ -24,6 +24,14 @@
 // cycles for each, however short).  Each step waits for the one before, so a CTA is bound by the chain of
 // small products and conversions; two CTAs share an SM (256 columns of tensor
 // memory and about 100 KB each at dk <= 96) and fill each other's gaps.
+//
+// With few (sequence, head) pairs a long sequence is cut into segments that
+// run at once.  A segment is linear in the state that enters it, S_out = A
+// S_in + L, so a pass over all segments but the last finds L (from a state of
+// zeros) and A (the same sweep with V = 0 from the identity: dk more rows), a
+// small fp32 kernel hands the states on from segment to segment, and the sweep
+// proper starts every segment from its own.  One prompt of 16,384 tokens at 16
+// heads of 128 x 128: 768 us in one piece, 331 us so.
 #include "gated_delta_tc.cuh"
 
 namespace gla {
@@ -57,9 +65,12 @@ struct Smem {
     static constexpr int bytes(int sw) { return V + 2 * kGdC * sw * 2 + 1024; }
 };
 
-template <int DK>
-__global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v,
-                                                                                  const __grid_constant__ GdMap map_o, int sw, int nslices, WaitCtl ctl)
+// PRE: the pass that finds L and A of every segment but a sequence's last; its
+// last slice is the identity's.
+template <int DK, bool PRE>
+__global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1)
+gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __grid_constant__ GdMap map_o, int sw, int nslices,
+                    WaitCtl ctl)
 {
     using C = Cols<DK>;
     using M = Smem<DK>;
@@ -68,8 +79,9 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars B;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // the slices of a (sequence, head) side by side, so that they share its records in L2
-    const int pair = blockIdx.x / nslices, n = pair / p.seqs.H, h = pair - n * p.seqs.H;
+    // the slices of a segment side by side, so that they share its records in L2
+    const int piece = blockIdx.x / nslices, slice = blockIdx.x - piece * nslices;
+    const int pair = piece / p.nseg, seg = piece - pair * p.nseg, n = pair / p.seqs.H, h = pair - n * p.seqs.H;
     int64_t row0;
     int len;
     p.seqs.span(n, row0, len);
@@ -77,9 +89,19 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
         if (tid == 0) record_status(p.status, GLA_ERR_INVALID_ARG);
         return;
     }
-    const int w0 = (blockIdx.x - pair * nslices) * sw, rows = min(sw, p.dv - w0);      // this CTA's dv rows
+    int64_t slot0 = p.seqs.slot0(n, row0);
+    const bool last = static_cast<int64_t>(seg + 1) * p.seg_chunks * kGdC >= len;      // the sequence ends here, or before
+    if (p.nseg > 1) {
+        const int64_t first = static_cast<int64_t>(seg) * p.seg_chunks;
+        if ((seg > 0 && first * kGdC >= len) || (PRE && last)) return;
+        len = min(len - static_cast<int>(first) * kGdC, p.seg_chunks * kGdC);
+        row0 += first * kGdC;
+        slot0 += first;
+    }
+    const bool unit = PRE && slice == nslices - 1;
+    const int w0 = unit ? 0 : slice * sw, rows = unit ? DK : min(sw, p.dv - w0);       // this CTA's dv rows
     const int nc = (len + kGdC - 1) / kGdC;
-    const unsigned char* rec = p.rec + (p.seqs.slot0(n, row0) * p.seqs.H + h) * Rec::BYTES;
+    const unsigned char* rec = p.rec + (slot0 * p.seqs.H + h) * Rec::BYTES;
     const int64_t rec_step = static_cast<int64_t>(p.seqs.H) * Rec::BYTES;
     const int64_t nh = static_cast<int64_t>(n) * p.seqs.H + h;
     const int active = 2 * (rows >> 5);                             // worker warps with rows
@@ -119,8 +141,9 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
             // K, scalars and V of chunk c (rows behind the sequence's end are not used)
             auto first = [&](int c) {
                 const int st = c & 1;
-                mbar_arrive_expect_tx(&B.full[st], Rec::KSC + vbytes);
+                mbar_arrive_expect_tx(&B.full[st], Rec::KSC + (unit ? 0u : vbytes));
                 bulk_load(smem + st * M::KSC, rec + c * rec_step, Rec::KSC, &B.full[st]);
+                if (unit) return;
                 tma_load_2d(smem + M::V + st * kGdC * sw * 2, mv, &B.full[st], col,
                             static_cast<int>(row0) + c * kGdC);
             };
@@ -133,16 +156,23 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
             int a = 0, q = 0, t = 0, pp = 0;             // copies issued of each kind
             if (nc > 0) first(a++);
             for (int c = 0; c < nc; ++c) {
-                ok = tile(c, &B.fq, &B.eq, M::Q, Rec::Q, DK * 128);
-                if (!ok) break;
-                ++q;
+                if (!PRE) {
+                    ok = tile(c, &B.fq, &B.eq, M::Q, Rec::Q, DK * 128);
+                    if (!ok) break;
+                    ++q;
+                }
                 ok = tile(c, &B.ft, &B.et, M::T, Rec::T, 16384);
                 if (!ok) break;
                 ++t;
-                ok = tile(c, &B.fp, &B.ep, M::P, Rec::P, 8192);
-                if (!ok) break;
-                ++pp;
-                if (c > 0) {
+                if (!PRE) {
+                    ok = tile(c, &B.fp, &B.ep, M::P, Rec::P, 8192);
+                    if (!ok) break;
+                    ++pp;
+                }
+                if (PRE) {
+                    if (c > 0 && c + 1 < nc) ok = mbar_wait(&B.empty[(c - 1) & 1], ((c - 1) >> 1) & 1, ctl);
+                    if (!ok) break;
+                } else if (c > 0) {
                     // o of the chunk before: out of its slice, which then takes the next chunk's V
                     const int st = (c - 1) & 1;
                     ok = mbar_wait(&B.staged[st], ((c - 1) >> 1) & 1, ctl);
@@ -155,7 +185,7 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
                 }
                 if (c + 1 < nc) first(a++);
             }
-            if (ok && nc > 0) {
+            if (!PRE && ok && nc > 0) {
                 const int c = nc - 1, st = c & 1, valid = len - c * kGdC;
                 const unsigned char* slice = smem + M::V + st * kGdC * sw * 2;
                 if (mbar_wait(&B.staged[st], (c >> 1) & 1, ctl)) {
@@ -199,14 +229,16 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
                     umma_bf16_ts(tm + C::Y, tm + C::S + 16 * k + 8, b, id64, 1);
                 }
                 umma_commit(&B.y);
-                if (c > 0 && !mbar_wait(&B.o, (c - 1) & 1, ctl)) break;
-                if (!mbar_wait(&B.fq, c & 1, ctl)) break;
-                tc_fence_after();
+                if (!PRE) {
+                    if (c > 0 && !mbar_wait(&B.o, (c - 1) & 1, ctl)) break;
+                    if (!mbar_wait(&B.fq, c & 1, ctl)) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < DK / 16; ++k)
-                    umma_bf16_ts(tm + C::O, tm + C::S + 16 * k, desc_add(q_k, (k >> 1) * 4096 + (k & 1) * 32), id64,
-                                 k > 0);
-                umma_commit(&B.eq);
+                    for (int k = 0; k < DK / 16; ++k)
+                        umma_bf16_ts(tm + C::O, tm + C::S + 16 * k, desc_add(q_k, (k >> 1) * 4096 + (k & 1) * 32), id64,
+                                     k > 0);
+                    umma_commit(&B.eq);
+                }
                 if (!mbar_wait(&B.ft, c & 1, ctl)) break;
                 if (!mbar_wait(&B.r, c & 1, ctl)) break;
                 tc_fence_after();
@@ -230,13 +262,15 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
                     umma_bf16_ts(tm + C::S, tm + C::Y + 16 * s + 8, desc_add(k_n, 1024 * s), idDk, 1);
                 }
                 umma_commit(&B.ds);
-                if (!mbar_wait(&B.fp, c & 1, ctl)) break;
+                if (!PRE) {
+                    if (!mbar_wait(&B.fp, c & 1, ctl)) break;
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    umma_bf16_ts(tm + C::O + 16 * s, tm + C::V + 8 * s, desc_add(p_k, 2048 * s + 32 * s),
-                                 idesc_bf16_f32(128, 64 - 16 * s, 0, 0), 1);
-                umma_commit(&B.out);
-                umma_commit(&B.ep);
+                    for (int s = 0; s < 4; ++s)
+                        umma_bf16_ts(tm + C::O + 16 * s, tm + C::V + 8 * s, desc_add(p_k, 2048 * s + 32 * s),
+                                     idesc_bf16_f32(128, 64 - 16 * s, 0, 0), 1);
+                    umma_commit(&B.out);
+                    umma_commit(&B.ep);
+                }
                 umma_commit(&B.empty[c & 1]);
             }
             umma_commit(&B.drain);
@@ -248,7 +282,17 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
         const uint32_t t0 = tm + (static_cast<uint32_t>(warp & 3) << 21);       // lane quarter
         constexpr int HS = DK / 2;                                              // state columns of a thread
         f2 S[HS / 2];
-        load_state<HS>(S, p.s0 ? p.s0 + (nh * DK + half * HS) * p.dv + r : nullptr, p.dv);
+        const int64_t at = nh * p.nseg + seg;                                   // this segment's slot
+        if (PRE) {
+#pragma unroll
+            for (int i = 0; i < HS / 2; ++i) {
+                const int k = half * HS + 2 * i;
+                S[i] = unit ? f2_make(k == r ? 1.f : 0.f, k + 1 == r ? 1.f : 0.f) : f2_splat(0.f);
+            }
+        } else {
+            const float* from = seg > 0 ? p.seg_l + at * DK * p.dv : p.s0 ? p.s0 + nh * DK * p.dv : nullptr;
+            load_state<HS>(S, from ? from + half * HS * p.dv + r : nullptr, p.dv);
+        }
         auto put_state = [&]() {
 #pragma unroll
             for (int k = 0; k < HS / 16; ++k) put_terms<2>(t0 + C::S + half * HS + 16 * k, cols_of<HS>(S, k));
@@ -272,7 +316,8 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
 #pragma unroll
             for (int b = 0; b < 2; ++b)
                 put_terms<2>(t0 + C::Y + 16 * (s + b),
-                             load_row16(vs + 16 * b * rows, rows, left - 16 * b) - load16(sc + kScG * kGdC + 16 * b) * x[b]);
+                             (unit ? zero16() : load_row16(vs + 16 * b * rows, rows, left - 16 * b)) -
+                                 load16(sc + kScG * kGdC + 16 * b) * x[b]);
             warp_done(&B.r, lane);
             ok = warp_wait(&B.z, ph, ctl);
             if (!ok) break;
@@ -281,7 +326,7 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 x[b] = x[b] * load16(sc + kScBeta * kGdC + 16 * b);
-                put_terms<1>(t0 + C::V + 8 * (s + b), x[b]);
+                if (!PRE) put_terms<1>(t0 + C::V + 8 * (s + b), x[b]);
                 put_terms<2>(t0 + C::Y + 16 * (s + b), x[b] * load16(sc + kScR * kGdC + 16 * b));
             }
             warp_done(&B.w, lane);
@@ -296,6 +341,7 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
                 put_state();
                 warp_done(&B.s, lane);
             }
+            if (PRE) continue;
             ok = warp_wait(&B.out, ph, ctl);
             if (!ok) break;
             tc_fence_after();
@@ -309,11 +355,74 @@ __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1) gd_sweep_fwd_ker
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.staged[ph]);
         }
-        if (ok && p.s_final) store_state<HS>(S, p.s_final + (nh * DK + half * HS) * p.dv + r, p.dv);
+        if (PRE) {
+            if (unit) store_state<HS>(S, p.seg_a + (at * DK + half * HS) * DK + r, DK);
+            else store_state<HS>(S, p.seg_l + (at * DK + half * HS) * p.dv + r, p.dv);
+        } else if (ok && last && p.s_final) {
+            store_state<HS>(S, p.s_final + (nh * DK + half * HS) * p.dv + r, p.dv);
+        }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kGdWorkers + 1) tmem_dealloc(tm, C::ALLOC);
+}
+
+// seg_l of segment g: from what the segment adds to the state that enters
+// it, x' = A x + L, into the state that enters it.  A CTA has 16 columns of
+// the state, all its rows in shared memory; a thread 4 columns of DK / 32 rows.
+template <int DK>
+__global__ void __launch_bounds__(128) gd_segments_kernel(GdParams p)
+{
+    constexpr int R = DK / 32, XS = 20;                       // row stride of x: float4 reads of 8 lanes meet all banks
+    __shared__ __align__(16) float x[DK * XS];
+    const int64_t nh = blockIdx.x;
+    const int n = static_cast<int>(nh / p.seqs.H);
+    int64_t row0;
+    int len;
+    p.seqs.span(n, row0, len);
+    const int c = blockIdx.y * 16 + (threadIdx.x & 3) * 4, cx = (threadIdx.x & 3) * 4, r0 = threadIdx.x >> 2;
+    float4 v[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        v[i] = p.s0 ? *reinterpret_cast<const float4*>(p.s0 + (nh * DK + r0 + 32 * i) * p.dv + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; static_cast<int64_t>(g + 1) * p.seg_chunks * kGdC < len; ++g) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(x + (r0 + 32 * i) * XS + cx) = v[i];
+        __syncthreads();
+        float* l = p.seg_l + (nh * p.nseg + g) * DK * p.dv + c;
+        const float* a = p.seg_a + (nh * p.nseg + g) * DK * DK;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float* at = l + static_cast<int64_t>(r0 + 32 * i) * p.dv;
+            const float4 add = *reinterpret_cast<const float4*>(at);
+            *reinterpret_cast<float4*>(at) = v[i];           // the state that enters segment g
+            v[i] = add;
+        }
+#pragma unroll 4
+        for (int k = 0; k < DK; k += 4) {
+            float4 y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(x + (k + j) * XS + cx);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(a + (r0 + 32 * i) * DK + k));
+                const float w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[i].x = fmaf(w[j], y[j].x, v[i].x);
+                    v[i].y = fmaf(w[j], y[j].y, v[i].y);
+                    v[i].z = fmaf(w[j], y[j].z, v[i].z);
+                    v[i].w = fmaf(w[j], y[j].w, v[i].w);
+                }
+            }
+        }
+    }
+    // the last segment's
+    const int g = len > 0 ? (len - 1) / (p.seg_chunks * kGdC) : 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        *reinterpret_cast<float4*>(p.seg_l + ((nh * p.nseg + g) * DK + r0 + 32 * i) * p.dv + c) = v[i];
 }
 
 template <int DK>
@@ -328,11 +437,25 @@ gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
                        (s = gd_slice_map(&o, p.o, width, width, tokens, sl.width, sl.last)) != GLA_OK))
         return s;
     const int smem = Smem<DK>::bytes(sl.width);
-    cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const unsigned pairs = static_cast<unsigned>(p.seqs.N) * p.seqs.H;
+    cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
+    if (p.nseg > 1) {
+        e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return status_of(e);
+        trace_begin(st);
+        gd_sweep_fwd_kernel<DK, true><<<pairs * p.nseg * (sl.n + 1), kGdThreads, smem, st>>>(p, v, o, sl.width, sl.n + 1, ctl);
+        trace_end(st, "gd_sweep_segments_kernel");
+        count_launch();
+        if ((s = check_launch("gd_sweep_segments_kernel")) != GLA_OK) return s;
+        trace_begin(st);
+        gd_segments_kernel<DK><<<dim3(pairs, p.dv / 16), 128, 0, st>>>(p);
+        trace_end(st, "gd_segments_kernel");
+        count_launch();
+        if ((s = check_launch("gd_segments_kernel")) != GLA_OK) return s;
+    }
     trace_begin(st);
-    gd_sweep_fwd_kernel<DK><<<static_cast<unsigned>(p.seqs.N) * p.seqs.H * sl.n, kGdThreads, smem, st>>>(p, v, o, sl.width, sl.n,
-                                                                                                       ctl);
+    gd_sweep_fwd_kernel<DK, false><<<pairs * p.nseg * sl.n, kGdThreads, smem, st>>>(p, v, o, sl.width, sl.n, ctl);
     trace_end(st, "gd_sweep_fwd_kernel");
     count_launch();
     return check_launch("gd_sweep_fwd_kernel");

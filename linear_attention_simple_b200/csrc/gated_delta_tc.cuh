@@ -98,6 +98,13 @@ __device__ __forceinline__ Cols16 fma16(const Cols16& a, const Cols16& b, const 
     for (int i = 0; i < 8; ++i) r.p[i] = f2_fma(a.p[i], b.p[i], c.p[i]);
     return r;
 }
+__device__ __forceinline__ Cols16 zero16()
+{
+    Cols16 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.p[i] = f2_splat(0.f);
+    return r;
+}
 // From shared memory (16-byte aligned), the same for all lanes.
 __device__ __forceinline__ Cols16 load16(const float* p)
 {

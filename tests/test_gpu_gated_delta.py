@@ -107,6 +107,21 @@ def test_chunk_bwd(N, T, Hk, H, dk, dv, with_states):
     check_bwd(d, s0, dO, ds)
 
 
+# few heads and long sequences: the forward cuts them into segments
+LONG = [(1, 1600, 1, 1, 96, 192, None), (2, 2100, 1, 2, 128, 128, None), (1, 1537, 2, 2, 64, 256, None),
+        (1, 1793, 1, 1, 96, 160, None), (1, 0, 1, 2, 96, 192, [700, 0, 1200, 65]), (1, 0, 1, 1, 128, 32, [1, 1700])]
+
+
+@pytest.mark.parametrize("N,T,Hk,H,dk,dv,lens", LONG)
+@pytest.mark.parametrize("decay", ["usual", "slow", "resets"])
+def test_segments(N, T, Hk, H, dk, dv, lens, decay):
+    cu = cu_of(lens) if lens else None
+    N = len(lens) if lens else N
+    d = make((sum(lens),) if lens else (N, T), Hk, H, dk, dv, 50, decay)
+    check_fwd(d, states(N, H, dk, dv, 51), cu)
+    check_fwd(d, None, cu)
+
+
 @pytest.mark.parametrize("decay", ["slow", "none", "strong", "resets"])
 def test_decays(decay):
     d = make((2, 150), 2, 2, 96, 192, 7, decay)
