@@ -31,7 +31,7 @@
 // zeros) and A (the same sweep with V = 0 from the identity: dk more rows), a
 // small fp32 kernel hands the states on from segment to segment, and the sweep
 // proper starts every segment from its own.  One prompt of 16,384 tokens at 16
-// heads of 128 x 128: 768 us in one piece, 331 us so.
+// heads of 128 x 128: 783 us in one piece, 309 us so (169 + 39 + 100).
 #include "gated_delta_tc.cuh"
 
 namespace gla {
@@ -369,60 +369,88 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
 
 // seg_l of segment g: from what the segment adds to the state that enters
 // it, x' = A x + L, into the state that enters it.  A CTA has 16 columns of
-// the state, all its rows in shared memory; a thread 4 columns of DK / 32 rows.
+// the state, all its rows in shared memory; a thread 4 columns of DK / 32 rows
+// and a quarter of the sum (a thread with the whole sum waits four times as
+// long for A: 83 us for 9 segments of 16 heads at dk = 128, 39 so).
 template <int DK>
-__global__ void __launch_bounds__(128) gd_segments_kernel(GdParams p)
+__global__ void __launch_bounds__(512) gd_segments_kernel(GdParams p)
 {
-    constexpr int R = DK / 32, XS = 20;                       // row stride of x: float4 reads of 8 lanes meet all banks
+    constexpr int R = DK / 32, XS = 20, KQ = DK / 4;          // XS: row stride of x, so that float4 reads meet all banks
     __shared__ __align__(16) float x[DK * XS];
+    __shared__ float4 part[3][R][128];
     const int64_t nh = blockIdx.x;
     const int n = static_cast<int>(nh / p.seqs.H);
     int64_t row0;
     int len;
     p.seqs.span(n, row0, len);
-    const int c = blockIdx.y * 16 + (threadIdx.x & 3) * 4, cx = (threadIdx.x & 3) * 4, r0 = threadIdx.x >> 2;
-    float4 v[R];
+    const int t = threadIdx.x & 127, q = threadIdx.x >> 7;
+    const int cx = (t & 3) * 4, c = blockIdx.y * 16 + cx, r0 = t >> 2;
+    if (q == 0) {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        v[i] = p.s0 ? *reinterpret_cast<const float4*>(p.s0 + (nh * DK + r0 + 32 * i) * p.dv + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int g = 0; static_cast<int64_t>(g + 1) * p.seg_chunks * kGdC < len; ++g) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(x + (r0 + 32 * i) * XS + cx) = v[i];
-        __syncthreads();
+        for (int i = 0; i < R; ++i)
+            *reinterpret_cast<float4*>(x + (r0 + 32 * i) * XS + cx) =
+                p.s0 ? *reinterpret_cast<const float4*>(p.s0 + (nh * DK + r0 + 32 * i) * p.dv + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    int g = 0;
+    for (; static_cast<int64_t>(g + 1) * p.seg_chunks * kGdC < len; ++g) {
         float* l = p.seg_l + (nh * p.nseg + g) * DK * p.dv + c;
-        const float* a = p.seg_a + (nh * p.nseg + g) * DK * DK;
+        const float* a = p.seg_a + (nh * p.nseg + g) * DK * DK + q * KQ;
+        float4 v[R], f[R][2];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            float* at = l + static_cast<int64_t>(r0 + 32 * i) * p.dv;
-            const float4 add = *reinterpret_cast<const float4*>(at);
-            *reinterpret_cast<float4*>(at) = v[i];           // the state that enters segment g
-            v[i] = add;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (q == 0) v[i] = *reinterpret_cast<const float4*>(l + static_cast<int64_t>(r0 + 32 * i) * p.dv);
         }
-#pragma unroll 4
-        for (int k = 0; k < DK; k += 4) {
-            float4 y[4];
+        __syncthreads();                                     // x is the state that enters segment g
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(x + (k + j) * XS + cx);
+        for (int k = 0; k < KQ; k += 8) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) f[i][e] = __ldg(reinterpret_cast<const float4*>(a + (r0 + 32 * i) * DK + k) + e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 y = *reinterpret_cast<const float4*>(x + (q * KQ + k + j) * XS + cx);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float4 u = f[i][j >> 2];
+                    const float w = (j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w;
+                    v[i].x = fmaf(w, y.x, v[i].x);
+                    v[i].y = fmaf(w, y.y, v[i].y);
+                    v[i].z = fmaf(w, y.z, v[i].z);
+                    v[i].w = fmaf(w, y.w, v[i].w);
+                }
+            }
+        }
+        if (q > 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) part[q - 1][i][t] = v[i];
+        }
+        __syncthreads();
+        if (q == 0) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(a + (r0 + 32 * i) * DK + k));
-                const float w[4] = {f.x, f.y, f.z, f.w};
+                float4* at = reinterpret_cast<float4*>(x + (r0 + 32 * i) * XS + cx);
+                *reinterpret_cast<float4*>(l + static_cast<int64_t>(r0 + 32 * i) * p.dv) = *at;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[i].x = fmaf(w[j], y[j].x, v[i].x);
-                    v[i].y = fmaf(w[j], y[j].y, v[i].y);
-                    v[i].z = fmaf(w[j], y[j].z, v[i].z);
-                    v[i].w = fmaf(w[j], y[j].w, v[i].w);
+                for (int e = 0; e < 3; ++e) {
+                    const float4 u = part[e][i][t];
+                    v[i].x += u.x;
+                    v[i].y += u.y;
+                    v[i].z += u.z;
+                    v[i].w += u.w;
                 }
+                *at = v[i];
             }
         }
     }
     // the last segment's
-    const int g = len > 0 ? (len - 1) / (p.seg_chunks * kGdC) : 0;
+    if (q == 0) {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        *reinterpret_cast<float4*>(p.seg_l + ((nh * p.nseg + g) * DK + r0 + 32 * i) * p.dv + c) = v[i];
+        for (int i = 0; i < R; ++i)
+            *reinterpret_cast<float4*>(p.seg_l + ((nh * p.nseg + g) * DK + r0 + 32 * i) * p.dv + c) =
+                *reinterpret_cast<const float4*>(x + (r0 + 32 * i) * XS + cx);
+    }
 }
 
 template <int DK>
@@ -449,7 +477,7 @@ gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
         count_launch();
         if ((s = check_launch("gd_sweep_segments_kernel")) != GLA_OK) return s;
         trace_begin(st);
-        gd_segments_kernel<DK><<<dim3(pairs, p.dv / 16), 128, 0, st>>>(p);
+        gd_segments_kernel<DK><<<dim3(pairs, p.dv / 16), 512, 0, st>>>(p);
         trace_end(st, "gd_segments_kernel");
         count_launch();
         if ((s = check_launch("gd_segments_kernel")) != GLA_OK) return s;

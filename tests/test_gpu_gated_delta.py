@@ -193,6 +193,31 @@ def test_rows_outside_every_sequence_stay():
         assert bool((x[:7] == 5).all()) and bool((x[150:] == 5).all())
 
 
+def test_what_is_not_finite_stays_in_its_sequence():
+    """Packed neighbours share tiles' tails: NaN and infinities in one sequence
+    reach no other's outputs, and dense batches' rows keep apart too."""
+    lens = [70, 33, 100, 1, 64]
+    cu = cu_of(lens)
+    d, dO = make((sum(lens),), 1, 2, 96, 192, 60), make((sum(lens),), 1, 2, 96, 192, 61)["v"]
+    s0, ds = states(5, 2, 96, 192, 62), states(5, 2, 96, 192, 63)
+    b, e = int(cu[1]), int(cu[2])
+
+    def run():
+        return gla.gated_delta_chunk_fwd(*args(d), s0=s0, cu_seqlens=cu) + \
+            gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds, cu_seqlens=cu)
+
+    want = run()
+    for n, bad in (("q", float("inf")), ("k", float("nan")), ("v", float("inf")), ("beta", float("nan"))):
+        d[n][b:e] = bad
+    dO[b:e] = float("nan")
+    s0[1], ds[1] = float("nan"), float("inf")
+    for i, (x, y) in enumerate(zip(run(), want)):
+        if i in (1, 7):                                     # states: [sequence, ...]
+            assert all(torch.equal(x[j], y[j]) for j in (0, 2, 3, 4)), i
+        else:
+            assert torch.equal(x[:b], y[:b]) and torch.equal(x[e:], y[e:]), i
+
+
 def test_offsets_outside_the_rows_are_reported():
     d = make((100,), 1, 1, 96, 192, 24)
     gla.gla_get_device_status()
