@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
     if (c < 0 || c * kGdC >= len) return;
     const int valid = min(kGdC, len - static_cast<int>(c) * kGdC);
     const int64_t row = row0 + c * kGdC;
+    [[maybe_unused]] const int64_t rows = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;   // of the checking build
     const int H = p.seqs.H, group = H / p.seqs.Hk;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, c2 = (lane & 3) * 2;
     const int nst = p.dv / kSl, wtot = p.dv >> 5;
@@ -210,11 +211,11 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
             const float after = __shfl_down_sync(0xFFFFFFFFu, s, 1);
             const float later = lane < 31 ? after : 0.f;
             const int64_t at = (row + 2 * lane) * H + h;
-            if (2 * lane < valid) {
+            if (2 * lane < valid && GLA_DCHECK(at >= 0 && at < rows * H, p.status)) {
                 p.da[at] = s + tail;
                 p.dbeta[at] = s2.x / sc[kScBeta * kGdC + 2 * lane];
             }
-            if (2 * lane + 1 < valid) {
+            if (2 * lane + 1 < valid && GLA_DCHECK(at + H < rows * H, p.status)) {
                 p.da[at + H] = later + d1 + tail;
                 p.dbeta[at + H] = s2.y / sc[kScBeta * kGdC + 2 * lane + 1];
             }
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams
     const int64_t ld = static_cast<int64_t>(p.seqs.Hk) * DK;
     for (int i = lane; i < 16 * (DK / 8); i += 32) {
         const int r = 16 * w + i / (DK / 8), cc = (i % (DK / 8)) * 8;
-        if (r < valid) {
+        if (r < valid && GLA_DCHECK(row + r < rows, p.status)) {
             const int64_t at = (row + r) * ld + hk * DK + cc;
             *reinterpret_cast<uint4*>(p.dq + at) = *reinterpret_cast<const uint4*>(sq + r * KS + cc);
             *reinterpret_cast<uint4*>(p.dkk + at) = *reinterpret_cast<const uint4*>(sk + r * KS + cc);

@@ -335,6 +335,7 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
                     umma_bf16_ts(d, a + 8, hi, id, 1);
                     umma_bf16_ts(d, a + 16, hi, id, 1);
                     umma_bf16_ts(d, a, lo, id, 1);
+                    umma_bf16_ts(d, a + 8, lo, id, 1);           // without it da is off by 1e-5
                 }
                 umma_commit(&B.out);
                 umma_commit(&B.ep);

@@ -290,7 +290,8 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 S[i] = unit ? f2_make(k == r ? 1.f : 0.f, k + 1 == r ? 1.f : 0.f) : f2_splat(0.f);
             }
         } else {
-            const float* from = seg > 0 ? p.seg_l + at * DK * p.dv : p.s0 ? p.s0 + nh * DK * p.dv : nullptr;
+            // (in segments the first one's too is a copy: s_final may be s0)
+            const float* from = p.nseg > 1 ? p.seg_l + at * DK * p.dv : p.s0 ? p.s0 + nh * DK * p.dv : nullptr;
             load_state<HS>(S, from ? from + half * HS * p.dv + r : nullptr, p.dv);
         }
         auto put_state = [&]() {

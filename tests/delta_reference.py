@@ -57,5 +57,6 @@ def norm(x, weight, bias, gate, center, act, eps):
 
 def rel(x, ref):
     """Relative 2-norm of the difference (0 when both are 0)."""
-    d, n = float((x.double() - ref.double()).norm()), float(ref.double().norm())
+    x, ref = x.detach().double(), ref.detach().double()
+    d, n = float((x - ref).norm()), float(ref.norm())
     return d / n if n else (0.0 if d == 0.0 else float("inf"))

@@ -218,6 +218,43 @@ def test_what_is_not_finite_stays_in_its_sequence():
             assert torch.equal(x[:b], y[:b]) and torch.equal(x[e:], y[e:]), i
 
 
+@pytest.mark.parametrize("T", [100, 1700])
+def test_states_in_place(T):
+    """s_final may be s0 and grad_s0 ds_final, in one piece and in segments."""
+    d, dO = make((1, T), 1, 1, 96, 192, 64), make((1, T), 1, 1, 96, 192, 65)["v"]
+    s0, ds = states(1, 1, 96, 192, 66), states(1, 1, 96, 192, 67)
+    o, s = gla.gated_delta_chunk_fwd(*args(d), s0=s0)
+    grads = gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds)
+    o2, s2 = gla.gated_delta_chunk_fwd(*args(d), s0=s0.clone(), s_final=(c := s0.clone()))
+    o3, s3 = gla.gated_delta_chunk_fwd(*args(d), s0=c.copy_(s0), s_final=c)
+    again = gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds, grads=[torch.empty_like(x) for x in args(d)] + [ds])
+    for x, y in zip((o, s, o, s) + tuple(grads), (o2, s2, o3, s3) + tuple(again)):
+        assert torch.equal(x, y)
+
+
+def test_offsets_past_32_bits():
+    """A sequence with more than 2^31 values of v, its end against a call on the
+    end alone (a reset before it), and a pool with more than 2^31."""
+    T, H, dv, tail = 150_000, 60, 256, 130
+    d = make((1, T), 1, H, 64, dv, 68)
+    assert d["v"].numel() > 2 ** 31
+    d["a"][:, T - tail] = -1e4
+    end = {n: x[:, T - tail:].contiguous() for n, x in d.items()}
+    o, s = gla.gated_delta_chunk_fwd(*args(d))
+    o2, s2 = gla.gated_delta_chunk_fwd(*args(end))
+    # the chunks begin elsewhere: not the same bits
+    assert rel(o[:, T - tail:], o2) <= TOL_O and rel(s, s2) <= TOL_S
+    del o, s, d
+    slots = 2 ** 31 // (H * 64 * dv) + 5
+    pool = torch.zeros(slots, H, 64, dv, device="cuda")
+    one = make((1, 1), 1, H, 64, dv, 69)
+    pool[-1] = states(1, H, 64, dv, 70)[0]
+    before = pool[-1:].clone()
+    o = gla.gated_delta_decode_step(pool, *args(one), slot_idx=torch.tensor([slots - 1], dtype=torch.int32, device="cuda"))
+    ro, rs = forward(one, before, 64 ** -0.5)
+    assert rel(o, ro) <= 2e-6 and rel(pool[-1:], rs) <= 2e-6
+
+
 def test_offsets_outside_the_rows_are_reported():
     d = make((100,), 1, 1, 96, 192, 24)
     gla.gla_get_device_status()

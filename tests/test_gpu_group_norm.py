@@ -94,6 +94,18 @@ def test_slices_other_stream_and_graph():
         assert torch.equal(p, q) and torch.equal(p, r)
 
 
+def test_offsets_past_32_bits():
+    M, G, d = 70_000, 32, 1024
+    x = torch.zeros(M, G, d, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 2 ** 31
+    end = make(40, G, d, torch.bfloat16, False, False, True, False, 7)
+    x[-40:] = end[0]
+    y = gla.group_norm_silu(x, end[1])
+    assert torch.equal(y[-40:], gla.group_norm_silu(end[0], end[1]))
+    dx = gla.group_norm_silu_bwd(x, x, end[1])[0]
+    assert torch.equal(dx[-40:], gla.group_norm_silu_bwd(end[0], end[0], end[1])[0])
+
+
 def test_gradients_against_differences():
     """fp32 x, identity activation: the loss <n, c> along random directions.
     Central differences with a step of 2^-6 of x's size leave third-order terms
