@@ -7,9 +7,9 @@
 // block of the 64 x 64 tiles per warp, tiles above the diagonal left out.  The
 // inverse is taken in fp32 by halves: the four 16 x 16 diagonal blocks by
 // forward substitution, a warp each and a column per lane; then the blocks
-// below them, -T22 L21 T11, at 16 and at 32 rows, all threads together.
-// (Substitution over all 64 rows, a column per thread, left two of the four
-// warps waiting: 125 us against 69 at 8 x 16 heads x 2,048 tokens.)  The
+// below them, -T22 L21 T11, at 16 and at 32 rows.  (Substitution over all 64
+// rows, a column per thread, left two of the four warps waiting: 125 us
+// against 91 at 8 x 16 heads x 2,048 tokens.)  The
 // running sum of the log-decays is taken in 64 bits, so that the differences
 // behind a strong decay (a reset between documents) keep their precision; a
 // is taken no lower than -10^4, where e^a is 0 in any case.
@@ -44,34 +44,60 @@ __device__ __forceinline__ void put8(unsigned char* hi, unsigned char* lo, const
     if (TWO) *reinterpret_cast<uint4*>(lo) = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// out[R x 4 of a thread] = A B for square blocks of NB rows in fp32 tiles:
-// thread `t` of NB * NB / (4 R) has rows r0 .. r0 + R - 1, columns c0 .. c0 + 3.
-template <int NB, int R>
-__device__ __forceinline__ void block_mul(float (&o)[R][4], const float* a, const float* b, int r0, int c0)
+// Three bf16 terms of a pair.
+__device__ __forceinline__ void terms3(uint32_t (&t)[3], float x, float y)
 {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < NB; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>(b + k * kLs + c0);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float x = a[(r0 + i) * kLs + k];
-            o[i][0] = fmaf(x, y.x, o[i][0]);
-            o[i][1] = fmaf(x, y.y, o[i][1]);
-            o[i][2] = fmaf(x, y.z, o[i][2]);
-            o[i][3] = fmaf(x, y.w, o[i][3]);
-        }
+    for (int n = 0; n < 3; ++n) {
+        t[n] = pack_bf16(x, y);
+        x -= bf16_lo(t[n]);
+        y -= bf16_hi(t[n]);
     }
 }
-template <int R>
-__device__ __forceinline__ void block_put(float* d, const float (&o)[R][4], int r0, int c0, float s)
+// d = f A B for a 16 x 16 block of a warp, A and B rows of fp32 tiles, NB deep:
+// tensor core products of three bf16 terms each (all six of 2^-24 and above),
+// so fp32 but for its last bits.  The same product by fp32 multiply-adds kept
+// the shared-memory pipe busy: eight times the reads.
+template <int NB>
+__device__ __forceinline__ void block_mul(float* d, const float* a, const float* b, float f, int lane)
 {
+    const int g = lane >> 2, c = (lane & 3) * 2;
+    float o[2][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        *reinterpret_cast<float4*>(d + (r0 + i) * kLs + c0) = make_float4(s * o[i][0], s * o[i][1], s * o[i][2], s * o[i][3]);
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NB; k += 16) {
+        uint32_t fa[4][3], fb[2][2][3], at[3][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = *reinterpret_cast<const float2*>(a + (g + 8 * (i & 1)) * kLs + k + c + 8 * (i >> 1));
+            terms3(fa[i], x.x, x.y);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float* y = b + (k + c + 8 * i) * kLs + 8 * t + g;
+                terms3(fb[t][i], y[0], y[kLs]);
+            }
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) at[n][i] = fa[i][n];
+#pragma unroll
+        for (int n = 2; n >= 0; --n)
+#pragma unroll
+            for (int m = 0; m <= n; ++m)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) mma_bf16(o[t], at[m], fb[t][0][n - m], fb[t][1][n - m]);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2*>(d + (g + 8 * e) * kLs + 8 * t + c) = make_float2(f * o[t][2 * e], f * o[t][2 * e + 1]);
 }
 
 template <int DK, bool BWD>
@@ -232,28 +258,24 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
         }
     }
     __syncthreads();
-    // 16-row blocks (1,0) and (3,2), two warps each; L T11 in the other corner
-    {
-        const int blk = tid >> 6, t = tid & 63, r0 = t >> 2, c0 = (t & 3) * 4, o = 32 * blk;
-        float x[1][4];
-        block_mul<16, 1>(x, sl + (o + 16) * kLs + o, tt + o * kLs + o, r0, c0);
-        block_put<1>(tt + o * kLs + o + 16, x, r0, c0, 1.f);
-        __syncthreads();
-        block_mul<16, 1>(x, tt + (o + 16) * kLs + o + 16, tt + o * kLs + o + 16, r0, c0);
-        block_put<1>(tt + (o + 16) * kLs + o, x, r0, c0, -1.f);
-        __syncthreads();
-        *reinterpret_cast<float4*>(tt + (o + r0) * kLs + o + 16 + c0) = make_float4(0.f, 0.f, 0.f, 0.f);
-        __syncthreads();
+    // 16-row blocks (1,0) and (3,2), a warp each; L T11 on the way in the other corner
+    if (w < 2) {
+        const int o = 32 * w;
+        float* corner = tt + o * kLs + o + 16;
+        block_mul<16>(corner, sl + (o + 16) * kLs + o, tt + o * kLs + o, 1.f, lane);
+        __syncwarp();
+        block_mul<16>(tt + (o + 16) * kLs + o, tt + (o + 16) * kLs + o + 16, corner, -1.f, lane);
+        __syncwarp();
+        for (int i = lane; i < 64; i += 32)
+            *reinterpret_cast<float4*>(corner + (i >> 2) * kLs + (i & 3) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // the 32-row block
+    __syncthreads();
+    // the 32-row block, a 16 x 16 quarter a warp
     {
-        const int r0 = (tid >> 3) * 2, c0 = (tid & 7) * 4;
-        float x[2][4];
-        block_mul<32, 2>(x, sl + 32 * kLs, tt, r0, c0);
-        block_put<2>(tt + 32, x, r0, c0, 1.f);
+        const int r0 = (w >> 1) * 16, c0 = (w & 1) * 16;
+        block_mul<32>(tt + r0 * kLs + 32 + c0, sl + (32 + r0) * kLs, tt + c0, 1.f, lane);
         __syncthreads();
-        block_mul<32, 2>(x, tt + 32 * kLs + 32, tt + 32, r0, c0);
-        block_put<2>(tt + 32 * kLs, x, r0, c0, -1.f);
+        block_mul<32>(tt + (32 + r0) * kLs + c0, tt + (32 + r0) * kLs + 32, tt + 32 + c0, -1.f, lane);
     }
     __syncthreads();
     for (int i = tid; i < kGdC * 8; i += kThreads) {
