@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
         put8<BWD>(rec + Rec::Q + at, rec + Rec::QL + at, f);
     }
     const int g = lane >> 2, c2 = (lane & 3) * 2;
+    uint32_t ph[8][2], pl[8][2];                       // P as it leaves, once L's tile is free to carry it
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
 #pragma unroll
@@ -225,11 +226,8 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
                 }
                 *reinterpret_cast<float2*>(sl + i * kLs + j0) = make_float2(l[0], l[1]);
             }
-            const uint32_t hi = pack_bf16(pv[0], pv[1]);
-            const uint32_t at = swz_off(i, t, 128) + (lane & 3) * 4;
-            *reinterpret_cast<uint32_t*>(rec + Rec::P + at) = hi;
-            if (BWD)
-                *reinterpret_cast<uint32_t*>(rec + Rec::PL + at) = pack_bf16(pv[0] - bf16_lo(hi), pv[1] - bf16_hi(hi));
+            ph[t][hf] = pack_bf16(pv[0], pv[1]);
+            if (BWD) pl[t][hf] = pack_bf16(pv[0] - bf16_lo(ph[t][hf]), pv[1] - bf16_hi(ph[t][hf]));
         }
     }
     __syncthreads();
@@ -274,7 +272,16 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
     {
         const int r0 = (w >> 1) * 16, c0 = (w & 1) * 16;
         block_mul<32>(tt + r0 * kLs + 32 + c0, sl + (32 + r0) * kLs, tt + c0, 1.f, lane);
-        __syncthreads();
+        __syncthreads();                               // L is read
+        unsigned char* sp = reinterpret_cast<unsigned char*>(sl);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t at = swz_off(16 * w + g + 8 * hf, t, 128) + (lane & 3) * 4;
+                *reinterpret_cast<uint32_t*>(sp + at) = ph[t][hf];
+                if (BWD) *reinterpret_cast<uint32_t*>(sp + 8192 + at) = pl[t][hf];
+            }
         block_mul<32>(tt + (32 + r0) * kLs + c0, tt + (32 + r0) * kLs + 32, tt + 32 + c0, -1.f, lane);
     }
     __syncthreads();
@@ -289,6 +296,8 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
         const uint32_t at = swz_off(r, i & 7, 128);
         put8<true>(rec + Rec::T + at, rec + Rec::TL + at, f);
     }
+    for (int i = tid; i < (BWD ? 1024 : 512); i += kThreads)
+        reinterpret_cast<uint4*>(rec + Rec::P)[i] = reinterpret_cast<const uint4*>(sl)[i];
     for (int i = tid; i < kGdSc * kGdC / 4; i += kThreads)
         reinterpret_cast<float4*>(rec + Rec::SC)[i] = reinterpret_cast<const float4*>(&sc[0][0])[i];
 }
@@ -298,6 +307,7 @@ gla_status launch(const GdParams& p, cudaStream_t st)
 {
     constexpr int smem = 2 * kGdC * (DK + kGdPad) * 2 + kGdC * kLs * 4;
     static_assert(2 * kGdC * (DK + kGdPad) * 2 >= kGdC * kLs * 4, "T takes the place of K and Q");
+    static_assert(kGdC * kLs * 4 >= 16384, "P takes the place of L");
     cudaError_t e = cudaFuncSetAttribute(gd_chunks_kernel<DK, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
     trace_begin(st);
