@@ -74,7 +74,9 @@ unsigned long long gla_launch_count(void);
  *   - scans the inputs of every chunk, segment and decode call before its
  *     kernels run: a_t <= 0 and finite, q/k/v/dO and fp32 states finite;
  *   - checks the index of each direct global store in its kernels against
- *     the tensor it writes, and skips a store that would fall outside;
+ *     the tensor it writes, and skips a store that would fall outside (the
+ *     gated delta rule: its gradients' kernel only, the others write whole
+ *     tiles and states; the group norm: none);
  * and records GLA_ERR_INVALID_ARG in the device status word on a violation
  * (read it with gla_get_device_status).  The scans cost one extra read of
  * the inputs per call. */
@@ -401,6 +403,8 @@ gla_status conv1d_silu_decode_step(const void* x, const int32_t* slot_idx, int n
  *     S_t  = S'_t + k_t^T beta_t (v_t - k_t S'_t)      S: dk x dv, fp32
  *     o_t  = scale q_t S_t
  *
+ * a_t may be as low as -infinity, which starts the state anew (taken as -1e4;
+ * the checking build reports it, as it is not finite).
  * The keys are meant to have unit length and beta to lie in 0 .. 1 (0 .. 2
  * keeps the state bounded too); neither is checked, nor normalised here.
  *

@@ -107,7 +107,7 @@ def test_chunk_bwd(N, T, Hk, H, dk, dv, with_states):
     check_bwd(d, s0, dO, ds)
 
 
-# few heads and long sequences: the forward cuts them into segments
+# few heads and long sequences: both directions cut them into segments
 LONG = [(1, 1600, 1, 1, 96, 192, None), (2, 2100, 1, 2, 128, 128, None), (1, 1537, 2, 2, 64, 256, None),
         (1, 1793, 1, 1, 96, 160, None), (1, 0, 1, 2, 96, 192, [700, 0, 1200, 65]), (1, 0, 1, 1, 128, 32, [1, 1700])]
 
@@ -120,6 +120,17 @@ def test_segments(N, T, Hk, H, dk, dv, lens, decay):
     d = make((sum(lens),) if lens else (N, T), Hk, H, dk, dv, 50, decay)
     check_fwd(d, states(N, H, dk, dv, 51), cu)
     check_fwd(d, None, cu)
+
+
+@pytest.mark.parametrize("N,T,Hk,H,dk,dv,lens", LONG)
+@pytest.mark.parametrize("decay,with_states", [("usual", True), ("usual", False), ("slow", True), ("resets", True)])
+def test_segments_bwd(N, T, Hk, H, dk, dv, lens, decay, with_states):
+    cu = cu_of(lens) if lens else None
+    N = len(lens) if lens else N
+    lead = (sum(lens),) if lens else (N, T)
+    d, dO = make(lead, Hk, H, dk, dv, 52, decay), make(lead, Hk, H, dk, dv, 53)["v"]
+    s0, ds = (states(N, H, dk, dv, 54), states(N, H, dk, dv, 55)) if with_states else (None, None)
+    check_bwd(d, s0, dO, ds, cu, da_of_terms=decay == "resets")
 
 
 @pytest.mark.parametrize("decay", ["slow", "none", "strong", "resets"])
@@ -136,6 +147,14 @@ def test_a_minus_infinity_is_a_reset():
     o, s = gla.gated_delta_chunk_fwd(*args(d))
     ro, rs = forward(d, torch.zeros(1, 1, 96, 192, device="cuda"), 96 ** -0.5)
     assert rel(o, ro) <= TOL_O and rel(s, rs) <= TOL_S
+
+
+def test_a_nan_decay_is_not_taken_for_a_reset():
+    d = make((2, 200), 1, 1, 96, 192, 11)
+    d["a"][0, 40] = float("nan")
+    o, s = gla.gated_delta_chunk_fwd(*args(d))
+    assert bool(o[0, 40:].isnan().all()) and bool(s[0].isnan().all())
+    assert bool(o[1].isfinite().all()) and bool(s[1].isfinite().all())
 
 
 @pytest.mark.parametrize("beta", [0.0, 1.0, 2.0])
