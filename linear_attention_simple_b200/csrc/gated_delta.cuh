@@ -1,6 +1,6 @@
 // gated_delta.cuh -- shared by the gated delta rule's kernels: the sequence
-// geometry, the workspace layout, warp-level matrix products on bf16
-// fragments and the splitting of fp32 values into bf16 terms.
+// geometry, the records and the workspace, warp-level matrix products on bf16
+// fragments.
 //
 // Chunks have 64 tokens.  With b the running sum of the log-decays inside a
 // chunk, G_i = e^{b_i}, R_i = e^{b_63 - b_i}, D_ij = e^{b_i - b_j} and S the
@@ -12,11 +12,10 @@
 //   o  = scale G Q S + P V',   P = tril(scale Q K^T . D)
 //   S' = G_63 S + K^T (R V')
 //
-// States are held transposed, [dv][dk], with 16 dv rows to a warp: a warp's
-// rows never meet another's, so the whole recurrence of its rows stays in its
-// registers, an accumulator of one product becomes the left operand of the
-// next without a shuffle, and only the chunk's shared operands (K, Q, T, P)
-// pass through shared memory.
+// The all-chunks kernel (gated_delta_chunks.cu) finds T and P; the sweeps
+// (gated_delta_sweep_fwd.cu, gated_delta_sweep_bwd.cu) walk the chunks with the
+// state transposed, [dv][dk], its rows on the lanes of tensor memory: rows of
+// the state never meet, so a slice of them is a CTA's own.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,7 +27,6 @@ namespace gla {
 constexpr int kGdC = 64;                 // tokens per chunk
 constexpr int kGdPad = 8;                // bf16 elements behind each shared-memory row: rows an odd
                                          // multiple of 16 bytes apart, so ldmatrix has no bank conflicts
-constexpr int kGdTP = kGdC + kGdPad;     // row stride of a shared T or P tile
 constexpr int kGdPiece = 32 * 8;         // a piece: 8 values of each of 32 dv rows
 constexpr int kGdSc = 6;                 // per-token scalars of a chunk: G, R, beta, P_ii, b (high, low)
 enum { kScG = 0, kScR = 1, kScBeta = 2, kScPd = 3, kScBh = 4, kScBl = 5 };
@@ -192,16 +190,19 @@ struct GdParams {
     __nv_bfloat16* vp;      // [u][dv / 32][8][32][8 tokens]: V'
     float* part;            // [u][3][dv / 32][64]: sums over 32 dv rows, per token
     float* anch;            // [u][dv / 32][2]: <gradient of the state leaving, state leaving>
-    // forward: segments of seg_chunks chunks, at most nseg of a sequence; per
-    // (sequence, head, segment) the state that enters [dk][dv], and A [dk][dk]
+    // segments of seg_chunks chunks, at most nseg of a sequence; per (sequence,
+    // head, segment) the state that enters [dk][dv], A [dk][dk] and (backward)
+    // the gradient of the state that leaves [dk][dv]
     int nseg, seg_chunks;
-    float *seg_l, *seg_a;
+    float *seg_l, *seg_a, *seg_e;
     int64_t slots;
     int* status;
 };
 
 gla_status gd_launch_chunks(const GdParams& p, bool bwd, cudaStream_t st);
 gla_status gd_launch_sweep_fwd(const GdParams& p, const WaitCtl& ctl, cudaStream_t st);
+gla_status gd_launch_segment_states(const GdParams& p, const WaitCtl& ctl, cudaStream_t st);
+gla_status gd_launch_segment_grads(const GdParams& p, cudaStream_t st);
 gla_status gd_launch_sweeps_bwd(const GdParams& p, const WaitCtl& ctl, cudaStream_t st);
 gla_status gd_launch_grad(const GdParams& p, cudaStream_t st);
 

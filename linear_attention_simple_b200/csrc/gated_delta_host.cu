@@ -54,18 +54,21 @@ gla_status gd_check(int N, int T, int Hk, int H, int dk, int dv, int64_t ld_qkv,
     return GLA_OK;
 }
 
-// The forward's segments (gated_delta_sweep_fwd.cu): as many as fill the SMs
-// once (two CTAs each, one at dk = 128), of at least 8 chunks.  The pass over
-// the segments and their hand-over cost about what the sweep itself does, so
-// two would gain nothing.
-void gd_segments(GdParams& p)
+// Segments of long sequences: as many as fill the SMs once (two CTAs each in
+// the forward up to dk = 96, else one), of at least 8 chunks.  The passes over
+// the segments and their hand-over cost about what the sweeps themselves do, so
+// two would gain nothing (three did: both sides' times are with the sweeps).
+// The backward's have an even number of chunks: it keeps the state after every
+// second one.
+void gd_segments(GdParams& p, bool bwd)
 {
     const int64_t chunks = (static_cast<int64_t>(p.seqs.T) + kGdC - 1) / kGdC;
     const int64_t ctas = static_cast<int64_t>(p.seqs.N) * p.seqs.H * ((p.dv + 127) / 128);
-    int64_t n = ctas > 0 ? 148 * (p.dk <= 96 ? 2 : 1) / ctas : 1;
+    int64_t n = ctas > 0 ? 148 * (p.dk <= 96 && !bwd ? 2 : 1) / ctas : 1;
     if (n > chunks / 8) n = chunks / 8;
     if (n < 3) n = 1;
     p.seg_chunks = static_cast<int>((chunks + n - 1) / n);
+    if (bwd) p.seg_chunks += p.seg_chunks & 1;
     if (p.seg_chunks < 1) p.seg_chunks = 1;
     p.nseg = static_cast<int>((chunks + p.seg_chunks - 1) / p.seg_chunks);
     if (p.nseg < 1) p.nseg = 1;
@@ -83,12 +86,11 @@ size_t gd_layout(GdParams& p, bool bwd, unsigned char* base)
         return q;
     };
     p.rec = take(u * gd_rec_bytes(p.dk, bwd));
-    if (!bwd) {
-        gd_segments(p);
-        const size_t segs = p.nseg > 1 ? static_cast<size_t>(p.seqs.N) * p.seqs.H * p.nseg : 0;
-        p.seg_l = reinterpret_cast<float*>(take(segs * dk * dv * 4));
-        p.seg_a = reinterpret_cast<float*>(take(segs * dk * dk * 4));
-    }
+    gd_segments(p, bwd);
+    const size_t segs = p.nseg > 1 ? static_cast<size_t>(p.seqs.N) * p.seqs.H * p.nseg : 0;
+    p.seg_l = reinterpret_cast<float*>(take(segs * dk * dv * 4));
+    p.seg_a = reinterpret_cast<float*>(take(segs * dk * dk * 4));
+    if (bwd) p.seg_e = reinterpret_cast<float*>(take(segs * dk * dv * 4));
     if (bwd) {
         p.sb = reinterpret_cast<__nv_bfloat16*>(take(u * dk * dv * 2));
         p.eb = reinterpret_cast<__nv_bfloat16*>(take(u * dk * dv * 2));
@@ -250,6 +252,7 @@ gla_status gated_delta_chunk_bwd(const void* q, const void* k, const void* v, co
     gd_layout(p, true, static_cast<unsigned char*>(ws));
     if ((s = gd_scan(p, stream)) != GLA_OK) return s;
     if ((s = gd_launch_chunks(p, true, stream)) != GLA_OK) return s;
+    if (p.nseg > 1 && (s = gd_launch_segment_states(p, ctl, stream)) != GLA_OK) return s;
     if ((s = gd_launch_sweeps_bwd(p, ctl, stream)) != GLA_OK) return s;
     return gd_launch_grad(p, stream);
 }

@@ -20,12 +20,21 @@
 // through P, which cancels exactly, is left out of both (o', dvs); and what
 // the state receives and gives back is taken in three bf16 terms (24 bits) so
 // that both sides of the rest see the same numbers: V' and its scaled form
-// forward, E in reverse.  With two terms everywhere da was off by 9e-6 (by
-// 4e-5 under strong decays) against 4e-6 so.  Everything else has two terms
+// forward, E in reverse.  With two terms everywhere da was off by 1e-5 (by
+// 4e-5 under strong decays) against 5e-6 so.  Everything else has two terms
 // against operands exact in bf16 (K, dO), or two against two (T, P, scale G Q).
 //
-// A CTA is bound by the chain of products and conversions, some 5,500 cycles a
-// chunk; it takes most of tensor memory, so an SM holds one.
+// A CTA is bound by the chain of products and conversions, some 7,500 cycles a
+// chunk forward and 8,500 in reverse; it takes most of tensor memory, so an SM
+// holds one.
+//
+// Long sequences with few heads are therefore cut into segments that run at
+// once, as in the forward: the states that enter them come from the same pass
+// (on this direction's records); the gradients of the states that leave them
+// from a reverse pass from zeros and a hand-over with A^T.  Whole backward of
+// 16,384 tokens, in one piece and so: 4 heads of 96 x 192 2,283 us, 524 us; 16
+// heads 2,561, 1,448; 48 heads of 128 x 128 (three segments) 4,030, 2,994; of
+// 2,048 tokens and 8 heads of 64 x 64 (four segments of 8 chunks) 317, 197.
 #include "gated_delta_tc.cuh"
 
 namespace gla {
@@ -76,18 +85,22 @@ struct Cta {
     const unsigned char* rec;
     int64_t rec_step, row0, nh, u0;
     int n, h, len, nc, w0, rows, sw, active;
+    int64_t at;             // this segment's slot
+    int c0;                 // its first chunk, an even one
+    bool last;              // the sequence ends in it
     __device__ __forceinline__ unsigned char* slice(int which, int st) const     // 0: V, 1: dO
     {
         return slices + (st * 2 + which) * kGdC * sw * 2;
     }
 };
 
+// seg0: the first segment that has work here.
 template <int DK>
-__device__ __forceinline__ bool setup(Cta& x, Bars& B, const GdParams& p, int sw, int nslices, unsigned char* raw)
+__device__ __forceinline__ bool setup(Cta& x, Bars& B, const GdParams& p, int sw, int nslices, int seg0, unsigned char* raw)
 {
     using Rec = GdRec<DK, true>;
-    // the slices of a (sequence, head) side by side, so that they share its records in L2
-    const int pair = blockIdx.x / nslices;
+    // the slices of a segment side by side, so that they share its records in L2
+    const int piece = blockIdx.x / nslices, pair = piece / p.nseg, seg = piece - pair * p.nseg;
     x.n = pair / p.seqs.H;
     x.h = pair - x.n * p.seqs.H;
     p.seqs.span(x.n, x.row0, x.len);
@@ -98,11 +111,18 @@ __device__ __forceinline__ bool setup(Cta& x, Bars& B, const GdParams& p, int sw
     x.smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     x.slices = x.smem + Smem<DK>::V;
     x.sw = sw;
-    x.w0 = (blockIdx.x - pair * nslices) * sw;
+    x.w0 = (blockIdx.x - piece * nslices) * sw;
     x.rows = min(sw, p.dv - x.w0);
+    const int64_t slot0 = p.seqs.slot0(x.n, x.row0), first = static_cast<int64_t>(seg) * p.seg_chunks;
+    if (seg < seg0 || (seg > 0 && first * kGdC >= x.len)) return false;
+    x.c0 = static_cast<int>(first);
+    x.last = p.nseg == 1 || (first + p.seg_chunks) * kGdC >= x.len;
+    if (p.nseg > 1) x.len = min(x.len - x.c0 * kGdC, p.seg_chunks * kGdC);
+    x.row0 += first * kGdC;
     x.nc = (x.len + kGdC - 1) / kGdC;
     x.nh = static_cast<int64_t>(x.n) * p.seqs.H + x.h;
-    x.u0 = p.seqs.slot0(x.n, x.row0) * p.seqs.H + x.h;
+    x.at = x.nh * p.nseg + seg;
+    x.u0 = (slot0 + first) * p.seqs.H + x.h;
     x.rec = p.rec + x.u0 * Rec::BYTES;
     x.rec_step = static_cast<int64_t>(p.seqs.H) * Rec::BYTES;
     x.active = 2 * (x.rows >> 5);
@@ -133,7 +153,7 @@ __device__ __forceinline__ bool setup(Cta& x, Bars& B, const GdParams& p, int sw
 
 // The copy warp's work (one lane): step i = 0 .. nc - 1 is chunk i, or nc - 1 - i
 // in reverse, where the workers leave dv in the V slice for it to take away.
-template <int DK, bool REV>
+template <int DK, bool REV, bool PRE>
 __device__ void copies(const Cta& x, Bars& B, const GdParams& p, const CUtensorMap* mv, const CUtensorMap* md,
                        const CUtensorMap* mo, const WaitCtl& ctl)
 {
@@ -144,9 +164,9 @@ __device__ void copies(const Cta& x, Bars& B, const GdParams& p, const CUtensorM
     auto chunk = [&](int i) { return REV ? x.nc - 1 - i : i; };
     auto first = [&](int i) {
         const int st = i & 1, c = chunk(i), row = static_cast<int>(x.row0) + c * kGdC;
-        mbar_arrive_expect_tx(&B.full[st], Rec::KSC + 2 * slice);
+        mbar_arrive_expect_tx(&B.full[st], Rec::KSC + (PRE ? 1 : 2) * slice);
         bulk_load(x.smem + st * M::KSC, x.rec + c * x.rec_step, Rec::KSC, &B.full[st]);
-        tma_load_2d(x.slice(0, st), mv, &B.full[st], col, row);
+        if (!PRE) tma_load_2d(x.slice(0, st), mv, &B.full[st], col, row);
         tma_load_2d(x.slice(1, st), md, &B.full[st], col, row);
     };
     auto tile = [&](int i, uint64_t* full, uint64_t* empty, int at, int from, uint32_t bytes) {
@@ -192,12 +212,12 @@ __device__ void copies(const Cta& x, Bars& B, const GdParams& p, const CUtensorM
             ++pp;
         }
         if (i > 0) {
-            ok = (!REV || out(i - 1)) && (i + 1 >= x.nc || mbar_wait(&B.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, ctl));
+            ok = (!REV || PRE || out(i - 1)) && (i + 1 >= x.nc || mbar_wait(&B.empty[(i - 1) & 1], ((i - 1) >> 1) & 1, ctl));
             if (!ok) break;
         }
         if (i + 1 < x.nc) first(a++);
     }
-    if (REV && ok && x.nc > 0) out(x.nc - 1);
+    if (REV && !PRE && ok && x.nc > 0) out(x.nc - 1);
     // no copy may be in flight when the block ends
     tma_store_wait_read();
     for (int i = max(0, a - 2); i < a; ++i) mbar_wait(&B.full[i & 1], (i >> 1) & 1, ctl);
@@ -263,13 +283,13 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Bars B;
     Cta x;
-    if (!setup<DK>(x, B, p, sw, nslices, smem_raw)) return;
+    if (!setup<DK>(x, B, p, sw, nslices, 0, smem_raw)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t tm = B.tmem;
     if (warp == kGdWorkers) {
         if (lane == 0) {
             const bool whole = x.rows == sw;
-            copies<DK, false>(x, B, p, whole ? &map_v.all : &map_v.last, whole ? &map_d.all : &map_d.last, nullptr, ctl);
+            copies<DK, false, false>(x, B, p, whole ? &map_v.all : &map_v.last, whole ? &map_d.all : &map_d.last, nullptr, ctl);
         }
     } else if (warp == kGdWorkers + 1) {
         if (lane == 0) {
@@ -349,7 +369,8 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
         const uint32_t t0 = tm + (static_cast<uint32_t>(warp & 3) << 21);
         constexpr int HS = DK / 2;
         f2 S[HS / 2];
-        load_state<HS>(S, p.s0 ? p.s0 + (x.nh * DK + half * HS) * p.dv + r : nullptr, p.dv);
+        const float* from = p.nseg > 1 ? p.seg_l + x.at * DK * p.dv : p.s0 ? p.s0 + x.nh * DK * p.dv : nullptr;
+        load_state<HS>(S, from ? from + half * HS * p.dv + r : nullptr, p.dv);
         auto put_state = [&]() {
 #pragma unroll
             for (int k = 0; k < HS / 16; ++k) put_terms<2>(t0 + C::S + half * HS + 16 * k, cols_of<HS>(S, k));
@@ -418,7 +439,7 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<ulonglong2*>(yn + (16 * b + 4 * i) * 32) = make_ulonglong2(y[b].p[2 * i].v, y[b].p[2 * i + 1].v);
             }
-            if (c > 0 && (c & 1) == 0) keep(p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32) + lane * 4);
+            if (x.c0 + c > 0 && (c & 1) == 0) keep(p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32) + lane * 4);
             ok = warp_wait(&B.ds, ph, ctl);
             if (!ok) break;
             tc_fence_after();
@@ -439,7 +460,7 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
             for (int b = 0; b < 2; ++b) split_pairs(od, b, d[b] * y[b]);
             p.part[(u * 3 * nwr + wr) * kGdC + half * 32 + lane] = lane_sums(od, lane);
         }
-        if (ok && p.ds_final) keep(p.sn_last + ((x.nh * nwr + wr) * 2 + half) * (HS * 32) + lane * 4);
+        if (ok && x.last && p.ds_final) keep(p.sn_last + ((x.nh * nwr + wr) * 2 + half) * (HS * 32) + lane * 4);
     }
     tc_fence_before();
     __syncthreads();
@@ -447,7 +468,9 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
 }
 
 // ---------------------------------------------------------------- reverse
-template <int DK>
+// PRE: over all segments but the first, from a gradient of zeros, for what a
+// segment itself gives its entering state's gradient; nothing else leaves.
+template <int DK, bool PRE>
 __global__ void __launch_bounds__(kGdThreads, 1)
 gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __grid_constant__ GdMap map_d,
                     const __grid_constant__ GdMap map_dv, int sw, int nslices, WaitCtl ctl)
@@ -458,14 +481,14 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Bars B;
     Cta x;
-    if (!setup<DK>(x, B, p, sw, nslices, smem_raw)) return;
+    if (!setup<DK>(x, B, p, sw, nslices, PRE ? 1 : 0, smem_raw)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t tm = B.tmem;
     if (warp == kGdWorkers) {
         if (lane == 0) {
             const bool whole = x.rows == sw;
-            copies<DK, true>(x, B, p, whole ? &map_v.all : &map_v.last, whole ? &map_d.all : &map_d.last,
-                             whole ? &map_dv.all : &map_dv.last, ctl);
+            copies<DK, true, PRE>(x, B, p, whole ? &map_v.all : &map_v.last, whole ? &map_d.all : &map_d.last,
+                                  whole ? &map_dv.all : &map_dv.last, ctl);
         }
     } else if (warp == kGdWorkers + 1) {
         if (lane == 0) {
@@ -536,7 +559,11 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
         const int s = 2 * half;                              // this thread's steps of 16 tokens: s and s + 1
         const int at = 16 * s * x.rows + (warp & 3) * 32 + lane;              // this row's 32 tokens in a slice
         f2 E[HS / 2];
-        load_state<HS>(E, p.ds_final ? p.ds_final + (x.nh * DK + half * HS) * p.dv + r : nullptr, p.dv);
+        const float* from = PRE          ? nullptr
+                            : p.nseg > 1 ? p.seg_e + x.at * DK * p.dv
+                            : p.ds_final ? p.ds_final + x.nh * DK * p.dv
+                                         : nullptr;
+        load_state<HS>(E, from ? from + half * HS * p.dv + r : nullptr, p.dv);
         auto put_grad = [&]() {
 #pragma unroll
             for (int k = 0; k < HS / 16; ++k) {
@@ -584,34 +611,36 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             // while the first products run: <E, state leaving> (the sum of da's
             // terms over all later tokens; after every second chunk, the next one
             // into L2) and E rounded; y of the forward is on its way
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&B.yin[warp], kYBytes);
-                bulk_load(ybuf, p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32), kYBytes, &B.yin[warp]);
-            }
-            if (i + 1 < x.nc && (c & 1) == 0) {
-                const float* b = p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32);
-                for (int k = lane; k < HS; k += 32) prefetch_l2(b + k * 32);
-            }
-            float dot = 0.f;
-            if (i > 0 ? (c & 1) == 1 : p.ds_final != nullptr) {
-                const float* sn = (i > 0 ? p.sn + (((u + p.seqs.H) * nwr + wr) * 2 + half) * (HS * 32)
-                                         : p.sn_last + ((x.nh * nwr + wr) * 2 + half) * (HS * 32)) + lane * 4;
-                f2 sum = f2_splat(0.f);
-#pragma unroll
-                for (int k = 0; k < HS / 2; k += 2) {
-                    const ulonglong2 w = __ldcs(reinterpret_cast<const ulonglong2*>(sn + 2 * k * 32));
-                    f2 a, b;
-                    a.v = w.x;
-                    b.v = w.y;
-                    sum = f2_fma(E[k + 1], b, f2_fma(E[k], a, sum));
+            if (!PRE) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&B.yin[warp], kYBytes);
+                    bulk_load(ybuf, p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32), kYBytes, &B.yin[warp]);
                 }
-                const float2 t = f2_get(sum);
-                dot = t.x + t.y;
+                if (i + 1 < x.nc && (c & 1) == 0) {
+                    const float* b = p.sn + ((u * nwr + wr) * 2 + half) * (HS * 32);
+                    for (int k = lane; k < HS; k += 32) prefetch_l2(b + k * 32);
+                }
+                float dot = 0.f;
+                if (i > 0 || !x.last ? (c & 1) == 1 : p.ds_final != nullptr) {
+                    const float* sn = (i > 0 || !x.last ? p.sn + (((u + p.seqs.H) * nwr + wr) * 2 + half) * (HS * 32)
+                                                        : p.sn_last + ((x.nh * nwr + wr) * 2 + half) * (HS * 32)) + lane * 4;
+                    f2 sum = f2_splat(0.f);
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+                    for (int k = 0; k < HS / 2; k += 2) {
+                        const ulonglong2 w = __ldcs(reinterpret_cast<const ulonglong2*>(sn + 2 * k * 32));
+                        f2 a, b;
+                        a.v = w.x;
+                        b.v = w.y;
+                        sum = f2_fma(E[k + 1], b, f2_fma(E[k], a, sum));
+                    }
+                    const float2 t = f2_get(sum);
+                    dot = t.x + t.y;
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+                }
+                if (lane == 0) p.anch[(u * nwr + wr) * 2 + half] = dot;
+                store_half_row<HS>(p.eb + u * p.dv * DK + wr * 32 * DK + half * (HS / 8) * kGdPiece + lane * 8, E);
             }
-            if (lane == 0) p.anch[(u * nwr + wr) * 2 + half] = dot;
-            store_half_row<HS>(p.eb + u * p.dv * DK + wr * 32 * DK + half * (HS / 8) * kGdPiece + lane * 8, E);
             Cols16 d[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -636,7 +665,7 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 if (!ok) break;
                 put_dO(i + 1);
             }
-            ok = warp_wait(&B.yin[warp], i & 1, ctl) && warp_wait(&B.z, ph, ctl);
+            ok = (PRE || warp_wait(&B.yin[warp], i & 1, ctl)) && warp_wait(&B.z, ph, ctl);
             if (!ok) break;
             tc_fence_after();
             float s1[32], s2[32];
@@ -647,6 +676,7 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
 #pragma unroll
                 for (int j = 0; j < 8; ++j) g.p[j] = f2_mul(g.p[j], f2_splat(-1.f));
                 put_terms<2>(t0 + C::Y + 16 * (s + b), g);
+                if (PRE) continue;
                 const Cols16 v = load_row16(vs + 16 * b * x.rows, x.rows, left - 16 * b);
                 store_row16(vs + 16 * b * x.rows, x.rows, full);
                 Cols16 y;
@@ -668,9 +698,11 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 mbar_arrive(&B.staged[ph]);
                 mbar_arrive(&B.empty[ph]);
             }
-            float* part = p.part + ((u * 3 + 1) * nwr + wr) * kGdC + half * 32 + lane;
-            part[0] = lane_sums(s1, lane);
-            part[static_cast<int64_t>(nwr) * kGdC] = lane_sums(s2, lane);
+            if (!PRE) {
+                float* part = p.part + ((u * 3 + 1) * nwr + wr) * kGdC + half * 32 + lane;
+                part[0] = lane_sums(s1, lane);
+                part[static_cast<int64_t>(nwr) * kGdC] = lane_sums(s2, lane);
+            }
             ok = warp_wait(&B.ds, ph, ctl);
             if (!ok) break;
             tc_fence_after();
@@ -680,7 +712,8 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 warp_done(&B.s, lane);
             }
         }
-        if (ok && p.ds0) store_state<HS>(E, p.ds0 + (x.nh * DK + half * HS) * p.dv + r, p.dv);
+        if (PRE) store_state<HS>(E, p.seg_e + (x.at * DK + half * HS) * p.dv + r, p.dv);
+        else if (ok && x.c0 == 0 && p.ds0) store_state<HS>(E, p.ds0 + (x.nh * DK + half * HS) * p.dv + r, p.dv);
     }
     tc_fence_before();
     __syncthreads();
@@ -694,7 +727,7 @@ gla_status start(K kernel, const char* name, const GdParams& p, int smem, const 
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
     trace_begin(st);
-    kernel<<<static_cast<unsigned>(p.seqs.N) * p.seqs.H * sl.n, kGdThreads, smem, st>>>(p, v, d, o, sl.width, sl.n, ctl);
+    kernel<<<static_cast<unsigned>(p.seqs.N) * p.seqs.H * p.nseg * sl.n, kGdThreads, smem, st>>>(p, v, d, o, sl.width, sl.n, ctl);
     trace_end(st, name);
     count_launch();
     return check_launch(name);
@@ -714,7 +747,12 @@ gla_status both(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
         return s;
     const int smem = Smem<DK>::bytes(sl.width);
     if ((s = start(gd_sweep_keep_kernel<DK>, "gd_sweep_keep_kernel", p, smem, v, d, dv, sl, ctl, st)) != GLA_OK) return s;
-    return start(gd_sweep_rev_kernel<DK>, "gd_sweep_rev_kernel", p, smem, v, d, dv, sl, ctl, st);
+    if (p.nseg > 1) {
+        if ((s = start(gd_sweep_rev_kernel<DK, true>, "gd_sweep_rev_segments_kernel", p, smem, v, d, dv, sl, ctl, st)) != GLA_OK ||
+            (s = gd_launch_segment_grads(p, st)) != GLA_OK)
+            return s;
+    }
+    return start(gd_sweep_rev_kernel<DK, false>, "gd_sweep_rev_kernel", p, smem, v, d, dv, sl, ctl, st);
 }
 
 }  // namespace

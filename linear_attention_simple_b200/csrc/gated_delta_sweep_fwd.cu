@@ -1,4 +1,4 @@
-// gated_delta_sweep_tc.cu -- the forward sweep of the gated delta rule over a
+// gated_delta_sweep_fwd.cu -- the forward sweep of the gated delta rule over a
 // sequence's chunks: outputs and final state.
 //
 // The state is held transposed, [dv][dk], dv rows on the lanes of tensor
@@ -21,9 +21,10 @@
 // V is read from a shared [token][row] slice and o leaves through the same
 // one, two stages, each a single tensor copy (a bulk copy per token row was
 // measured at twice the whole kernel's time: the copy unit takes some 80
-// cycles for each, however short).  Each step waits for the one before, so a CTA is bound by the chain of
-// small products and conversions; two CTAs share an SM (256 columns of tensor
-// memory and about 100 KB each at dk <= 96) and fill each other's gaps.
+// cycles for each, however short).  Each step waits for the one before, so a
+// CTA is bound by the chain of small products and conversions; two CTAs share
+// an SM (256 columns of tensor memory and about 100 KB each at dk <= 96) and
+// fill each other's gaps.
 //
 // With few (sequence, head) pairs a long sequence is cut into segments that
 // run at once.  A segment is linear in the state that enters it, S_out = A
@@ -65,16 +66,19 @@ struct Smem {
     static constexpr int bytes(int sw) { return V + 2 * kGdC * sw * 2 + 1024; }
 };
 
-// PRE: the pass that finds L and A of every segment but a sequence's last; its
-// last slice is the identity's.
-template <int DK, bool PRE>
+// What a launch does: the sweep; or the pass that finds L of every segment but
+// a sequence's last, and A (its last slice is the identity's), on the forward's
+// records or on the backward's, where A of the last segment is wanted too.
+enum { kSweep = 0, kSegments = 1, kSegmentsBwd = 2 };
+template <int DK, int MODE>
 __global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1)
 gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __grid_constant__ GdMap map_o, int sw, int nslices,
                     WaitCtl ctl)
 {
     using C = Cols<DK>;
     using M = Smem<DK>;
-    using Rec = GdRec<DK, false>;
+    using Rec = GdRec<DK, MODE == kSegmentsBwd>;
+    constexpr bool PRE = MODE != kSweep;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars B;
@@ -93,7 +97,7 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
     const bool last = static_cast<int64_t>(seg + 1) * p.seg_chunks * kGdC >= len;      // the sequence ends here, or before
     if (p.nseg > 1) {
         const int64_t first = static_cast<int64_t>(seg) * p.seg_chunks;
-        if ((seg > 0 && first * kGdC >= len) || (PRE && last)) return;
+        if ((seg > 0 && first * kGdC >= len) || (PRE && last && !(MODE == kSegmentsBwd && slice == nslices - 1))) return;
         len = min(len - static_cast<int>(first) * kGdC, p.seg_chunks * kGdC);
         row0 += first * kGdC;
         slot0 += first;
@@ -248,7 +252,7 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                     const uint32_t id = idesc_bf16_f32(128, 64 - 16 * s, 0, 0);
                     const uint64_t hi = desc_add(t_k, 2048 * s + 32 * s), lo = desc_add(hi, 8192);
                     const uint32_t d = tm + C::S + 16 * s, a = tm + C::Y + 16 * s;
-                    umma_bf16_ts(d, a, hi, id, s > 0);
+                    umma_bf16_ts(d, a, hi, id, MODE == kSegmentsBwd || s > 0);
                     umma_bf16_ts(d, a + 8, hi, id, 1);
                     umma_bf16_ts(d, a, lo, id, 1);
                 }
@@ -315,10 +319,12 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             Cols16 x[2];
             get16x2(x[0], x[1], t0 + C::Y + 16 * s, t0 + C::Y + 16 * s + 16);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-                put_terms<2>(t0 + C::Y + 16 * (s + b),
-                             (unit ? zero16() : load_row16(vs + 16 * b * rows, rows, left - 16 * b)) -
-                                 load16(sc + kScG * kGdC + 16 * b) * x[b]);
+            for (int b = 0; b < 2; ++b) {
+                const Cols16 r = (unit ? zero16() : load_row16(vs + 16 * b * rows, rows, left - 16 * b)) -
+                                 load16(sc + kScG * kGdC + 16 * b) * x[b];
+                put_terms<2>(t0 + C::Y + 16 * (s + b), r);
+                if (MODE == kSegmentsBwd) put16(t0 + C::S + 16 * (s + b), r);         // this record's T lacks its diagonal
+            }
             warp_done(&B.r, lane);
             ok = warp_wait(&B.z, ph, ctl);
             if (!ok) break;
@@ -368,12 +374,15 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
     if (warp == kGdWorkers + 1) tmem_dealloc(tm, C::ALLOC);
 }
 
-// seg_l of segment g: from what the segment adds to the state that enters
-// it, x' = A x + L, into the state that enters it.  A CTA has 16 columns of
-// the state, all its rows in shared memory; a thread 4 columns of DK / 32 rows
-// and a quarter of the sum (a thread with the whole sum waits four times as
-// long for A: 83 us for 9 segments of 16 heads at dk = 128, 39 so).
-template <int DK>
+// Hands the states on: x' = A x + L through seg_l, whose slot of a segment
+// turns from L into the state that enters it; ADJ: from the last segment to the
+// first, x' = A^T x + D through seg_e, whose slot turns from D (what the segment
+// itself gives its entering state's gradient) into the gradient of the state
+// that leaves it.  A CTA has 16 columns of the state, all its rows in shared
+// memory; a thread 4 columns of DK / 32 rows and a quarter of the sum (a thread
+// with the whole sum waits four times as long for A: 83 us for 9 segments of 16
+// heads at dk = 128, so 39).
+template <int DK, bool ADJ>
 __global__ void __launch_bounds__(512) gd_segments_kernel(GdParams p)
 {
     constexpr int R = DK / 32, XS = 20, KQ = DK / 4;          // XS: row stride of x, so that float4 reads meet all banks
@@ -384,42 +393,52 @@ __global__ void __launch_bounds__(512) gd_segments_kernel(GdParams p)
     int64_t row0;
     int len;
     p.seqs.span(n, row0, len);
+    if (len < 0) return;
     const int t = threadIdx.x & 127, q = threadIdx.x >> 7;
     const int cx = (t & 3) * 4, c = blockIdx.y * 16 + cx, r0 = t >> 2;
+    const int last = len > 0 ? (len - 1) / (p.seg_chunks * kGdC) : 0;
+    const float* start = ADJ ? p.ds_final : p.s0;
+    float* slots = ADJ ? p.seg_e : p.seg_l;
     if (q == 0) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
             *reinterpret_cast<float4*>(x + (r0 + 32 * i) * XS + cx) =
-                p.s0 ? *reinterpret_cast<const float4*>(p.s0 + (nh * DK + r0 + 32 * i) * p.dv + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                start ? *reinterpret_cast<const float4*>(start + (nh * DK + r0 + 32 * i) * p.dv + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    int g = 0;
-    for (; static_cast<int64_t>(g + 1) * p.seg_chunks * kGdC < len; ++g) {
-        float* l = p.seg_l + (nh * p.nseg + g) * DK * p.dv + c;
-        const float* a = p.seg_a + (nh * p.nseg + g) * DK * DK + q * KQ;
-        float4 v[R], f[R][2];
+    for (int j = 0; j < last; ++j) {
+        const int g = ADJ ? last - j : j;
+        float* l = slots + (nh * p.nseg + g) * DK * p.dv + c;
+        const float* a = p.seg_a + (nh * p.nseg + g) * DK * DK;
+        float4 v[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (q == 0) v[i] = *reinterpret_cast<const float4*>(l + static_cast<int64_t>(r0 + 32 * i) * p.dv);
         }
-        __syncthreads();                                     // x is the state that enters segment g
+        __syncthreads();                                     // x is the state at this segment
 #pragma unroll
-        for (int k = 0; k < KQ; k += 8) {
+        for (int k = q * KQ; k < (q + 1) * KQ; k += 8) {
+            float w[R][8];
 #pragma unroll
-            for (int i = 0; i < R; ++i)
+            for (int i = 0; i < R; ++i) {
+                if (ADJ) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) f[i][e] = __ldg(reinterpret_cast<const float4*>(a + (r0 + 32 * i) * DK + k) + e);
+                    for (int e = 0; e < 8; ++e) w[i][e] = __ldg(a + (k + e) * DK + r0 + 32 * i);
+                } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float4 y = *reinterpret_cast<const float4*>(x + (q * KQ + k + j) * XS + cx);
+                    for (int e = 0; e < 8; e += 4)
+                        *reinterpret_cast<float4*>(w[i] + e) = __ldg(reinterpret_cast<const float4*>(a + (r0 + 32 * i) * DK + k + e));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float4 y = *reinterpret_cast<const float4*>(x + (k + e) * XS + cx);
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    const float4 u = f[i][j >> 2];
-                    const float w = (j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w;
-                    v[i].x = fmaf(w, y.x, v[i].x);
-                    v[i].y = fmaf(w, y.y, v[i].y);
-                    v[i].z = fmaf(w, y.z, v[i].z);
-                    v[i].w = fmaf(w, y.w, v[i].w);
+                    v[i].x = fmaf(w[i][e], y.x, v[i].x);
+                    v[i].y = fmaf(w[i][e], y.y, v[i].y);
+                    v[i].z = fmaf(w[i][e], y.z, v[i].z);
+                    v[i].w = fmaf(w[i][e], y.w, v[i].w);
                 }
             }
         }
@@ -445,13 +464,39 @@ __global__ void __launch_bounds__(512) gd_segments_kernel(GdParams p)
             }
         }
     }
-    // the last segment's
     if (q == 0) {
+        const int g = ADJ ? 0 : last;
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            *reinterpret_cast<float4*>(p.seg_l + ((nh * p.nseg + g) * DK + r0 + 32 * i) * p.dv + c) =
+            *reinterpret_cast<float4*>(slots + ((nh * p.nseg + g) * DK + r0 + 32 * i) * p.dv + c) =
                 *reinterpret_cast<const float4*>(x + (r0 + 32 * i) * XS + cx);
     }
+}
+
+template <int DK, bool ADJ>
+gla_status hand_on(const GdParams& p, cudaStream_t st)
+{
+    trace_begin(st);
+    gd_segments_kernel<DK, ADJ><<<dim3(static_cast<unsigned>(p.seqs.N) * p.seqs.H, p.dv / 16), 512, 0, st>>>(p);
+    trace_end(st, "gd_segments_kernel");
+    count_launch();
+    return check_launch("gd_segments_kernel");
+}
+
+// The pass over segments and the hand-over of their states.
+template <int DK, int MODE>
+gla_status segments(const GdParams& p, const GdMap& v, const GdMap& o, const GdSlices& sl, const WaitCtl& ctl, cudaStream_t st)
+{
+    const int smem = Smem<DK>::bytes(sl.width);
+    cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return status_of(e);
+    trace_begin(st);
+    gd_sweep_fwd_kernel<DK, MODE><<<static_cast<unsigned>(p.seqs.N) * p.seqs.H * p.nseg * (sl.n + 1), kGdThreads, smem, st>>>(
+        p, v, o, sl.width, sl.n + 1, ctl);
+    trace_end(st, "gd_sweep_segments_kernel");
+    count_launch();
+    const gla_status s = check_launch("gd_sweep_segments_kernel");
+    return s != GLA_OK ? s : hand_on<DK, false>(p, st);
 }
 
 template <int DK>
@@ -467,30 +512,46 @@ gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
         return s;
     const int smem = Smem<DK>::bytes(sl.width);
     const unsigned pairs = static_cast<unsigned>(p.seqs.N) * p.seqs.H;
-    cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK, kSweep>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
-    if (p.nseg > 1) {
-        e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return status_of(e);
-        trace_begin(st);
-        gd_sweep_fwd_kernel<DK, true><<<pairs * p.nseg * (sl.n + 1), kGdThreads, smem, st>>>(p, v, o, sl.width, sl.n + 1, ctl);
-        trace_end(st, "gd_sweep_segments_kernel");
-        count_launch();
-        if ((s = check_launch("gd_sweep_segments_kernel")) != GLA_OK) return s;
-        trace_begin(st);
-        gd_segments_kernel<DK><<<dim3(pairs, p.dv / 16), 512, 0, st>>>(p);
-        trace_end(st, "gd_segments_kernel");
-        count_launch();
-        if ((s = check_launch("gd_segments_kernel")) != GLA_OK) return s;
-    }
+    if (p.nseg > 1 && (s = segments<DK, kSegments>(p, v, o, sl, ctl, st)) != GLA_OK) return s;
     trace_begin(st);
-    gd_sweep_fwd_kernel<DK, false><<<pairs * p.nseg * sl.n, kGdThreads, smem, st>>>(p, v, o, sl.width, sl.n, ctl);
+    gd_sweep_fwd_kernel<DK, kSweep><<<pairs * p.nseg * sl.n, kGdThreads, smem, st>>>(p, v, o, sl.width, sl.n, ctl);
     trace_end(st, "gd_sweep_fwd_kernel");
     count_launch();
     return check_launch("gd_sweep_fwd_kernel");
 }
 
+// The same for the backward's sweeps, which have records of their own.
+template <int DK>
+gla_status states(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
+{
+    const GdSlices sl(p.dv);
+    const int64_t tokens = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;
+    GdMap v{};
+    const gla_status s = gd_slice_map(&v, p.v, static_cast<int64_t>(p.seqs.H) * p.dv, p.ld_v, tokens, sl.width, sl.last);
+    return s != GLA_OK ? s : segments<DK, kSegmentsBwd>(p, v, v, sl, ctl, st);
+}
+
 }  // namespace
+
+gla_status gd_launch_segment_states(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
+{
+    switch (p.dk) {
+    case 64: return states<64>(p, ctl, st);
+    case 96: return states<96>(p, ctl, st);
+    default: return states<128>(p, ctl, st);
+    }
+}
+
+gla_status gd_launch_segment_grads(const GdParams& p, cudaStream_t st)
+{
+    switch (p.dk) {
+    case 64: return hand_on<64, true>(p, st);
+    case 96: return hand_on<96, true>(p, st);
+    default: return hand_on<128, true>(p, st);
+    }
+}
 
 gla_status gd_launch_sweep_fwd(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
 {
