@@ -32,7 +32,7 @@
 // zeros) and A (the same sweep with V = 0 from the identity: dk more rows), a
 // small fp32 kernel hands the states on from segment to segment, and the sweep
 // proper starts every segment from its own.  One prompt of 16,384 tokens at 16
-// heads of 128 x 128: 783 us in one piece, 309 us so (169 + 39 + 100).
+// heads of 128 x 128: 783 us in one piece, 300 us so (169 + 30 + 100).
 #include "gated_delta_tc.cuh"
 
 namespace gla {
@@ -379,15 +379,25 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
 // first, x' = A^T x + D through seg_e, whose slot turns from D (what the segment
 // itself gives its entering state's gradient) into the gradient of the state
 // that leaves it.  A CTA has 16 columns of the state, all its rows in shared
-// memory; a thread 4 columns of DK / 32 rows and a quarter of the sum (a thread
-// with the whole sum waits four times as long for A: 83 us for 9 segments of 16
-// heads at dk = 128, so 39).
+// memory; a thread 4 columns of DK / 32 rows and a quarter of the sum.  A of
+// the next segment is on its way meanwhile.  9 segments of 16 heads at dk = 128:
+// 30 us (38 with A read from L2 as it is used, 83 with whole sums a thread).
+template <int DK>
+struct HandOn {
+    static constexpr int R = DK / 32;                         // rows of a thread
+    static constexpr int AS = DK + 4, XS = 20;                // row strides of A and x: 16-byte reads of 8 rows meet all banks
+    static constexpr int A = DK * AS, X = DK * XS;            // floats
+    static constexpr int bytes = (2 * A + X + 3 * R * 128 * 4) * 4;
+};
 template <int DK, bool ADJ>
 __global__ void __launch_bounds__(512) gd_segments_kernel(GdParams p)
 {
-    constexpr int R = DK / 32, XS = 20, KQ = DK / 4;          // XS: row stride of x, so that float4 reads meet all banks
-    __shared__ __align__(16) float x[DK * XS];
-    __shared__ float4 part[3][R][128];
+    using M = HandOn<DK>;
+    constexpr int R = M::R, XS = M::XS, AS = M::AS, KQ = DK / 4;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    float* sa = reinterpret_cast<float*>(smem_raw);           // A of two segments
+    float* x = sa + 2 * M::A;
+    float4* part = reinterpret_cast<float4*>(x + M::X);       // [3][R][128]
     const int64_t nh = blockIdx.x;
     const int n = static_cast<int>(nh / p.seqs.H);
     int64_t row0;
@@ -396,42 +406,57 @@ __global__ void __launch_bounds__(512) gd_segments_kernel(GdParams p)
     if (len < 0) return;
     const int t = threadIdx.x & 127, q = threadIdx.x >> 7;
     const int cx = (t & 3) * 4, c = blockIdx.y * 16 + cx, r0 = t >> 2;
+    auto row = [&](int i) { return ADJ ? R * r0 + i : r0 + 32 * i; };        // neighbours along A's fast axis
     const int last = len > 0 ? (len - 1) / (p.seg_chunks * kGdC) : 0;
     const float* start = ADJ ? p.ds_final : p.s0;
     float* slots = ADJ ? p.seg_e : p.seg_l;
+    auto segment = [&](int j) { return nh * p.nseg + (ADJ ? last - j : j); };
+    auto fetch = [&](int j) {
+        const float* a = p.seg_a + segment(j) * DK * DK;
+        float* dst = sa + (j & 1) * M::A;
+        for (int i = threadIdx.x; i < DK * DK / 4; i += 512) cp_async16(dst + i / (DK / 4) * AS + i % (DK / 4) * 4, a + 4 * i, true);
+    };
+    if (last > 0) fetch(0);
+    cp_async_commit();
     if (q == 0) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            *reinterpret_cast<float4*>(x + (r0 + 32 * i) * XS + cx) =
-                start ? *reinterpret_cast<const float4*>(start + (nh * DK + r0 + 32 * i) * p.dv + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4*>(x + row(i) * XS + cx) =
+                start ? *reinterpret_cast<const float4*>(start + (nh * DK + row(i)) * p.dv + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int j = 0; j < last; ++j) {
-        const int g = ADJ ? last - j : j;
-        float* l = slots + (nh * p.nseg + g) * DK * p.dv + c;
-        const float* a = p.seg_a + (nh * p.nseg + g) * DK * DK;
-        float4 v[R];
+        if (j + 1 < last) fetch(j + 1);
+        cp_async_commit();
+        float* l = slots + segment(j) * DK * p.dv + c;
+        float4 add[R], v[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (q == 0) v[i] = *reinterpret_cast<const float4*>(l + static_cast<int64_t>(r0 + 32 * i) * p.dv);
+            add[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (q == 0) add[i] = *reinterpret_cast<const float4*>(l + static_cast<int64_t>(row(i)) * p.dv);
         }
-        __syncthreads();                                     // x is the state at this segment
+        cp_async_wait<1>();
+        __syncthreads();                                     // A is there, x is the state at this segment
+        const float* a = sa + (j & 1) * M::A;
 #pragma unroll
-        for (int k = q * KQ; k < (q + 1) * KQ; k += 8) {
-            float w[R][8];
+        for (int k = q * KQ; k < (q + 1) * KQ; k += 4) {
+            float w[R][4];
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                if (ADJ) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[i][e] = __ldg(a + (k + e) * DK + r0 + 32 * i);
+            for (int e = 0; e < (ADJ ? 4 : R); ++e) {
+                if (!ADJ) {
+                    *reinterpret_cast<float4*>(w[e]) = *reinterpret_cast<const float4*>(a + row(e) * AS + k);
+                } else if (R == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(a + (k + e) * AS + 4 * r0);
+                    w[0][e] = y.x;
+                    w[1][e] = y.y;
+                    w[R - 2][e] = y.z;
+                    w[R - 1][e] = y.w;
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; e += 4)
-                        *reinterpret_cast<float4*>(w[i] + e) = __ldg(reinterpret_cast<const float4*>(a + (r0 + 32 * i) * DK + k + e));
+                    for (int i = 0; i < R; ++i) w[i][e] = a[(k + e) * AS + row(i)];
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
                 const float4 y = *reinterpret_cast<const float4*>(x + (k + e) * XS + cx);
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
@@ -444,23 +469,23 @@ __global__ void __launch_bounds__(512) gd_segments_kernel(GdParams p)
         }
         if (q > 0) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) part[q - 1][i][t] = v[i];
+            for (int i = 0; i < R; ++i) part[((q - 1) * R + i) * 128 + t] = v[i];
         }
         __syncthreads();
         if (q == 0) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                float4* at = reinterpret_cast<float4*>(x + (r0 + 32 * i) * XS + cx);
-                *reinterpret_cast<float4*>(l + static_cast<int64_t>(r0 + 32 * i) * p.dv) = *at;
+                float4* at = reinterpret_cast<float4*>(x + row(i) * XS + cx);
+                *reinterpret_cast<float4*>(l + static_cast<int64_t>(row(i)) * p.dv) = *at;
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
-                    const float4 u = part[e][i][t];
+                    const float4 u = part[(e * R + i) * 128 + t];
                     v[i].x += u.x;
                     v[i].y += u.y;
                     v[i].z += u.z;
                     v[i].w += u.w;
                 }
-                *at = v[i];
+                *at = make_float4(v[i].x + add[i].x, v[i].y + add[i].y, v[i].z + add[i].z, v[i].w + add[i].w);
             }
         }
     }
@@ -468,16 +493,19 @@ __global__ void __launch_bounds__(512) gd_segments_kernel(GdParams p)
         const int g = ADJ ? 0 : last;
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            *reinterpret_cast<float4*>(slots + ((nh * p.nseg + g) * DK + r0 + 32 * i) * p.dv + c) =
-                *reinterpret_cast<const float4*>(x + (r0 + 32 * i) * XS + cx);
+            *reinterpret_cast<float4*>(slots + ((nh * p.nseg + g) * DK + row(i)) * p.dv + c) =
+                *reinterpret_cast<const float4*>(x + row(i) * XS + cx);
     }
 }
 
 template <int DK, bool ADJ>
 gla_status hand_on(const GdParams& p, cudaStream_t st)
 {
+    constexpr int smem = HandOn<DK>::bytes;
+    const cudaError_t e = cudaFuncSetAttribute(gd_segments_kernel<DK, ADJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return status_of(e);
     trace_begin(st);
-    gd_segments_kernel<DK, ADJ><<<dim3(static_cast<unsigned>(p.seqs.N) * p.seqs.H, p.dv / 16), 512, 0, st>>>(p);
+    gd_segments_kernel<DK, ADJ><<<dim3(static_cast<unsigned>(p.seqs.N) * p.seqs.H, p.dv / 16), 512, smem, st>>>(p);
     trace_end(st, "gd_segments_kernel");
     count_launch();
     return check_launch("gd_segments_kernel");
