@@ -31,8 +31,9 @@
 // S_in + L, so a pass over all segments but the last finds L (from a state of
 // zeros) and A (the same sweep with V = 0 from the identity: dk more rows), a
 // small fp32 kernel hands the states on from segment to segment, and the sweep
-// proper starts every segment from its own.  One prompt of 16,384 tokens at 16
-// heads of 128 x 128: 783 us in one piece, 300 us so (169 + 30 + 100).
+// proper starts every segment from its own.  The pass needs neither Q, P nor o:
+// two of its CTAs share an SM at dk = 128 too (169 us with one each, 143 so).  One prompt of 16,384 tokens at 16
+// heads of 128 x 128: 783 us in one piece, 273 us so (143 + 30 + 100).
 #include "gated_delta_tc.cuh"
 
 namespace gla {
@@ -45,7 +46,7 @@ struct Cols {
     static constexpr int Y = DK;                     // Y -> R terms -> W terms
     static constexpr int V = DK + 64;                // V', one term
     static constexpr int O = DK + 96;
-    static constexpr int ALLOC = DK + 160 <= 256 ? 256 : 512;
+    static constexpr int alloc(bool pre) { return pre || DK + 160 <= 256 ? 256 : 512; }
 };
 
 struct __align__(8) Bars {
@@ -58,11 +59,11 @@ struct __align__(8) Bars {
 };
 
 // Shared memory of a CTA.
-template <int DK>
+template <int DK, bool PRE>
 struct Smem {
     using Rec = GdRec<DK, false>;
     static constexpr int KSC = (Rec::KSC + 1023) / 1024 * 1024;    // a stage of K and scalars
-    static constexpr int Q = 2 * KSC, T = Q + DK * 128, P = T + 16384, V = P + 8192;
+    static constexpr int T = 2 * KSC, Q = T + 16384, P = Q + DK * 128, V = PRE ? Q : P + 8192;
     static constexpr int bytes(int sw) { return V + 2 * kGdC * sw * 2 + 1024; }
 };
 
@@ -71,14 +72,14 @@ struct Smem {
 // records or on the backward's, where A of the last segment is wanted too.
 enum { kSweep = 0, kSegments = 1, kSegmentsBwd = 2 };
 template <int DK, int MODE>
-__global__ void __launch_bounds__(kGdThreads, DK <= 96 ? 2 : 1)
+__global__ void __launch_bounds__(kGdThreads, DK <= 96 || MODE != kSweep ? 2 : 1)
 gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __grid_constant__ GdMap map_o, int sw, int nslices,
                     WaitCtl ctl)
 {
     using C = Cols<DK>;
-    using M = Smem<DK>;
-    using Rec = GdRec<DK, MODE == kSegmentsBwd>;
     constexpr bool PRE = MODE != kSweep;
+    using M = Smem<DK, PRE>;
+    using Rec = GdRec<DK, MODE == kSegmentsBwd>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars B;
@@ -125,7 +126,7 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
         mbar_init_fence();
     }
     if (warp == kGdWorkers + 1) {
-        tmem_alloc(&B.tmem, C::ALLOC);
+        tmem_alloc(&B.tmem, C::alloc(PRE));
         tmem_relinquish();
     }
     tc_fence_before();
@@ -371,7 +372,7 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kGdWorkers + 1) tmem_dealloc(tm, C::ALLOC);
+    if (warp == kGdWorkers + 1) tmem_dealloc(tm, C::alloc(PRE));
 }
 
 // Hands the states on: x' = A x + L through seg_l, whose slot of a segment
@@ -515,7 +516,7 @@ gla_status hand_on(const GdParams& p, cudaStream_t st)
 template <int DK, int MODE>
 gla_status segments(const GdParams& p, const GdMap& v, const GdMap& o, const GdSlices& sl, const WaitCtl& ctl, cudaStream_t st)
 {
-    const int smem = Smem<DK>::bytes(sl.width);
+    const int smem = Smem<DK, true>::bytes(sl.width);
     cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
     trace_begin(st);
@@ -538,7 +539,7 @@ gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
     if (tokens > 0 && ((s = gd_slice_map(&v, p.v, width, p.ld_v, tokens, sl.width, sl.last)) != GLA_OK ||
                        (s = gd_slice_map(&o, p.o, width, width, tokens, sl.width, sl.last)) != GLA_OK))
         return s;
-    const int smem = Smem<DK>::bytes(sl.width);
+    const int smem = Smem<DK, false>::bytes(sl.width);
     const unsigned pairs = static_cast<unsigned>(p.seqs.N) * p.seqs.H;
     cudaError_t e = cudaFuncSetAttribute(gd_sweep_fwd_kernel<DK, kSweep>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
