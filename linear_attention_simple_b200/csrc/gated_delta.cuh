@@ -27,7 +27,7 @@ namespace gla {
 constexpr int kGdC = 64;                 // tokens per chunk
 constexpr int kGdPad = 8;                // bf16 elements behind each shared-memory row: rows an odd
                                          // multiple of 16 bytes apart, so ldmatrix has no bank conflicts
-constexpr int kGdPiece = 32 * 8;         // a piece: 8 values of each of 32 dv rows
+constexpr int kGdPiece = 32 * 16;        // a piece: 16 values of each of 32 dv rows (32-byte swizzle)
 constexpr int kGdSc = 6;                 // per-token scalars of a chunk: G, R, beta, P_ii, b (high, low)
 enum { kScG = 0, kScR = 1, kScBeta = 2, kScPd = 3, kScBh = 4, kScBl = 5 };
 
@@ -140,13 +140,6 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
                  : "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -155,16 +148,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Address of this lane's row for the three ldmatrix patterns, as an element
-// offset from the tile's origin, `ld` elements a row.
+// Address of this lane's row for ldmatrix, as an element offset from the tile's
+// origin, `ld` elements a row.
 //   rows_n: a 16 x 16 tile stored [n][k]: r0, r1 = the right operand of n 0-7
 //           (k 0-7, k 8-15), r2, r3 of n 8-15.
-//   rows_k: the same from a tile stored [k][n], with ldsm4_t.
 //   rows_a: a left operand of 16 rows from a tile stored [m][k].
-//   rows_at: the same from a tile stored [k][m], with ldsm4_t.
 __device__ __forceinline__ int rows_n(int lane, int ld) { return ((lane & 7) + ((lane >> 4) << 3)) * ld + (((lane >> 3) & 1) << 3); }
-__device__ __forceinline__ int rows_k(int lane, int ld) { return ((lane & 7) + (((lane >> 3) & 1) << 3)) * ld + ((lane >> 4) << 3); }
-__device__ __forceinline__ int rows_at(int lane, int ld) { return ((lane & 7) + ((lane >> 4) << 3)) * ld + (((lane >> 3) & 1) << 3); }
 __device__ __forceinline__ int rows_a(int lane, int ld) { return (lane & 15) * ld + ((lane >> 4) << 3); }
 
 // 2^x for the decay factors: x <= 0 here (0 -> 1, very negative -> 0).
@@ -183,11 +172,11 @@ struct GdParams {
     // workspace, one entry per chunk slot and value head (u = slot * H + h)
     unsigned char* rec;     // [u]: GdRec
     // backward only; a "half row" is a thread's: one dv row, half of the columns
-    __nv_bfloat16 *sb, *eb; // [u][dv / 32][dk / 8][32][8]: the state entering, the gradient of the state leaving
+    __nv_bfloat16 *sb, *eb; // [u][dv / 32][dk / 16][piece]: the state entering, the gradient of the state leaving
     float* sn;              // [u][dv / 32][2][dk / 8][32 lanes][4]: the state entering in fp32, half rows
     float* sn_last;         // [N H][..]: the final state in the same form
     float* yn;              // [u][dv / 32][2][8][32 lanes][4]: y, half rows
-    __nv_bfloat16* vp;      // [u][dv / 32][8][32][8 tokens]: V'
+    __nv_bfloat16* vp;      // [u][dv / 32][4][piece]: V', 16 tokens a piece
     float* part;            // [u][3][dv / 32][64]: sums over 32 dv rows, per token
     float* anch;            // [u][dv / 32][2]: <gradient of the state leaving, state leaving>
     // segments of seg_chunks chunks, at most nseg of a sequence; per (sequence,
@@ -204,6 +193,6 @@ gla_status gd_launch_sweep_fwd(const GdParams& p, const WaitCtl& ctl, cudaStream
 gla_status gd_launch_segment_states(const GdParams& p, const WaitCtl& ctl, cudaStream_t st);
 gla_status gd_launch_segment_grads(const GdParams& p, cudaStream_t st);
 gla_status gd_launch_sweeps_bwd(const GdParams& p, const WaitCtl& ctl, cudaStream_t st);
-gla_status gd_launch_grad(const GdParams& p, cudaStream_t st);
+gla_status gd_launch_grad(const GdParams& p, const WaitCtl& ctl, cudaStream_t st);
 
 }  // namespace gla

@@ -1,389 +1,533 @@
 // gated_delta_grad.cu -- dq, dk, da and dbeta of the gated delta rule, every
-// chunk at once.  With X = scale dO, Y = -dv, the state S that enters the
-// chunk and the gradient E of the state that leaves it:
+// chunk at once.  With X = dO, Y = dv, the state S that enters the chunk and the
+// gradient E of the state that leaves it:
 //
-//   A_ij = X_i . v'_j D_ij (i >= j)      B_ij = Y_i . v'_j D_ij (i > j)
-//   dq = A K + G X S^T
-//   dk = A^T Q + B^T K + B K + G Y S^T + R V' E^T
+//   A_ij = scale X_i . v'_j D_ij (i >= j)      B_ij = -Y_i . v'_j D_ij (i > j)
+//   dq = scale G X S^T + A K
+//   dk = -G Y S^T + R V' E^T + (B + B^T) K + A^T Q
 //   da_t = sum over i >= t of (o.dO - dv.y - dvs.z)_i up to the next <E, S'>
 //          (every 128 tokens), and that
 //
-// One CTA of 4 warps per (chunk, q/k head), 16 token rows to a warp; the
-// value heads that share the q/k head are summed in its accumulators.  A
-// first pass over dv (32 columns a stage, two stages) gives A and B, each warp
-// its own rows, the tiles above the diagonal left out; they are rounded to
-// bf16, multiply K from the registers and, from shared memory, transposed, Q
-// and K; a second pass adds the three products with the states.  dq and dk
-// leave in bf16, so every operand is one bf16 rounding of its value; the sums
-// behind da and dbeta come in fp32 from the sweeps.
+// The 64 rows of X stand over the 64 rows of Y in shared memory, so dq's tokens
+// are lanes 0-63 of tensor memory and dk's lanes 64-127, and every product is
+// one of 128 rows.  Per 64 columns of dv:
 //
-// Latency bounds it (three CTAs an SM, 12 warps): where a value head has a
-// q/k head of its own (ONE), the accumulators of dq and dk start only after
-// the first pass, which leaves 168 registers a thread enough.
-#include "gated_delta.cuh"
+//   D1 += [X; Y] V'^T      D2 += [X; Y] S^T      D3 += [.; V'] E^T
+//
+// ([.; V']: its upper rows are whatever lies before V' in shared memory; what
+// they give is not read).  Workers take scale G D2 and -G D2 + R D3 into their
+// registers, turn D1, masked and decayed, into A over B (bf16, in shared memory),
+// and the tensor core reads those as they stand and transposed:
+//
+//   D4 = [A; B] K + [0; B^T] K + [0; A^T] Q
+//
+// The value heads that share a q/k head are added up in the registers.  dq and
+// dk leave in bf16, so every operand is one bf16 rounding of its value; the sums
+// behind da and dbeta come in fp32 from the sweeps, and a warp of its own adds
+// them up.
+//
+// The states and V' are read as the sweeps left them, in pieces of 16 values of
+// 32 dv rows with the tensor core's 32-byte swizzle.  One CTA an SM walks over
+// (chunk, head): a ring of three stages of 64 dv columns keeps the loads going,
+// and the products of the next unit start as soon as D2 and D3 are read (D1 has
+// two buffers).  Every byte is read once, and HBM bounds it: 8 x 2,048 tokens,
+// 16 heads of 96 x 192, 855 MB in 146 us, 5.9 TB/s.  (With mma.sync, two passes
+// over dv and 12 warps an SM, latency did: 272 us.)
+#include "gated_delta_tc.cuh"
 
 namespace gla {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kMaxWarps = 8;               // of 32 dv rows (dv <= 256)
-constexpr int kSl = 32;                    // dv columns per stage
-constexpr int kVs = kSl + kGdPad;          // row stride of a staged token slice
+constexpr int kSms = 148;
+constexpr int kThreads = (kGdWorkers + 4) * 32;      // + a slice, an issue, a sums and a tile warp
+constexpr int kCols = 64;                            // dv columns of a stage
+constexpr int kStages = 3;
+constexpr int kPieceBytes = kGdPiece * 2;
+constexpr int kMaxWarps = 8;                         // of 32 dv rows (dv <= 256)
 
+// Tensor memory columns.
 template <int DK>
-struct GradSmem {
-    static constexpr int KS = DK + kGdPad;
-    static constexpr int tok = kGdC * kVs;             // one staged token slice of dO or dv
-    // V' and the states as they lie in memory, in pieces of 8 values of 32 dv
-    // rows: 16 bytes a row, so that ldmatrix meets every bank once
-    static constexpr int vt = kSl * kGdC;
-    static constexpr int st = kSl * DK;
-    static constexpr int stage1 = 2 * tok + vt, stage2 = stage1 + 2 * st;
-    // elements: the first pass's stages, later A and B; then K and Q; the
-    // second pass's stages over all of them
-    static constexpr int ab = kGdC * (kGdC + kGdPad);
-    static constexpr int kq = 2 * stage1;
-    static constexpr int all = kq + 2 * kGdC * KS > 2 * stage2 ? kq + 2 * kGdC * KS : 2 * stage2;
-    static constexpr int bytes = all * 2 + kGdSc * kGdC * 4;
+struct Cols {
+    static constexpr int D1 = 0, D2 = 128, D3 = D2 + DK, D4 = D3 + DK, ALLOC = 512;       // D1: two buffers of 64
+};
+template <int DK>
+struct Smem {
+    using Rec = GdRec<DK, true>;
+    static constexpr int VB = 4 * kPieceBytes, SB = DK / 16 * kPieceBytes;        // of 32 dv columns
+    static constexpr int X = 0, Y = 8192, V = 16384, S = V + 2 * VB, E = S + 2 * SB, STAGE = E + 2 * SB;
+    // a tile of zeros, A, B; K and Q, later dk and dq; b of two units
+    static constexpr int Z = kStages * STAGE, A = Z + 8192, K = A + 2 * 8192, Q = K + kGdC * DK * 2, SC = Q + kGdC * DK * 2;
+    static constexpr int SCB = 2 * kGdC * 4, BARS = SC + 2 * SCB, bytes = BARS + 256 + 1024;
+    static_assert(bytes <= 227 * 1024, "shared memory of an SM");
+};
+struct __align__(8) Bars {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t sc[2], sc_done[2];                      // b; workers -> copies
+    uint64_t kq, kq_done;                            // K and Q; workers -> copies: free, or holding dk and dq
+    uint64_t d123, d4, drain;                        // issuer -> workers, itself
+    uint64_t w, read;                                // workers -> issuer: A and B are there; D2 and D3 are read
+    uint32_t tmem;
+};
+struct Maps {
+    CUtensorMap dO, dv, q, dq, dk;
 };
 
-struct Src {
-    const __nv_bfloat16 *d, *y, *vp, *s, *e;
-    int64_t ld_do, ld_dv;
-    int dv, valid;
+// A (chunk, q/k head) of this CTA.
+struct Unit {
+    int64_t slot;
+    int hk, row, valid;     // row: the chunk's first token
+    bool between;           // <E, S'> is kept for the chunk behind this one, not for this one
 };
-
-// Stage i of pass 1 (dO, dv, V') or of pass 2 (those and both states).
-template <int DK>
-__device__ __forceinline__ void load_slice(__nv_bfloat16* st, const Src& x, int col, bool states, int tid)
+// Calls f for this CTA's units in turn, the same for all lanes, until it
+// returns false.  32 units at a time are looked up, a lane each.
+template <class F>
+__device__ __forceinline__ void for_units(const GdParams& p, int lane, F f)
 {
-    constexpr int KS = GradSmem<DK>::KS, tok = GradSmem<DK>::tok;
-    gd_load_rows(st, kVs, x.d + col, x.ld_do, kSl, x.valid, tid, kThreads);
-    gd_load_rows(st + tok, kVs, x.y + col, x.ld_dv, kSl, x.valid, tid, kThreads);
-    __nv_bfloat16* sv = st + 2 * tok;
-    for (int i = tid; i < GradSmem<DK>::vt / 8; i += kThreads)
-        cp_async16(sv + 8 * i, x.vp + static_cast<int64_t>(col) * kGdC + 8 * i, true);
-    if (states) {
-        constexpr int n = GradSmem<DK>::st / 8;
-        __nv_bfloat16* ss = st + GradSmem<DK>::stage1;
-        for (int i = tid; i < n; i += kThreads) {
-            cp_async16(ss + 8 * i, x.s + static_cast<int64_t>(col) * DK + 8 * i, true);
-            cp_async16(ss + 8 * (n + i), x.e + static_cast<int64_t>(col) * DK + 8 * i, true);
+    const int64_t total = p.slots * p.seqs.Hk, step = gridDim.x;
+    for (int64_t base = blockIdx.x; base < total; base += 32 * step) {
+        const int64_t i = base + lane * step;
+        int row = 0, valid = 0;
+        bool between = false;
+        if (i < total) {
+            const int64_t slot = i / p.seqs.Hk;
+            const int n = gd_seq_of_slot(p.seqs, slot);
+            int64_t row0;
+            int len;
+            p.seqs.span(n, row0, len);
+            const int64_t c = slot - p.seqs.slot0(n, row0);
+            if (len >= 0 && c >= 0 && c * kGdC < len) {      // else between two sequences
+                row = static_cast<int>(row0 + c * kGdC);
+                valid = min(kGdC, len - static_cast<int>(c) * kGdC);
+                between = (c & 1) == 0 && (c + 1) * kGdC < len;
+            }
+        }
+        for (uint32_t m = __ballot_sync(0xFFFFFFFFu, valid > 0); m; m &= m - 1) {
+            const int l = __ffs(m) - 1;
+            Unit u;
+            u.slot = (base + l * step) / p.seqs.Hk;
+            u.hk = static_cast<int>(base + l * step - u.slot * p.seqs.Hk);
+            u.row = __shfl_sync(0xFFFFFFFFu, row, l);
+            u.valid = __shfl_sync(0xFFFFFFFFu, valid, l);
+            u.between = __shfl_sync(0xFFFFFFFFu, static_cast<int>(between), l) != 0;
+            if (!f(u)) return;
         }
     }
 }
 
-// The rows_k and rows_at patterns on pieces.
-__device__ __forceinline__ int piece_k(int lane) { return (lane >> 4) * kGdPiece + ((lane & 7) + (((lane >> 3) & 1) << 3)) * 8; }
-__device__ __forceinline__ int piece_at(int lane) { return ((lane >> 3) & 1) * kGdPiece + ((lane & 7) + ((lane >> 4) << 3)) * 8; }
-
-// A left operand's rows g and g + 8 times f0 and f1.
-__device__ __forceinline__ void scale_a(uint32_t (&r)[4], float f0, float f1)
+// da and dbeta of a (chunk, value head): one warp, two tokens a lane.
+template <int DK>
+__device__ __forceinline__ void sums(const GdParams& p, const Unit& x, int h, int lane)
 {
+    const int H = p.seqs.H, wtot = p.dv >> 5;
+    const int64_t u = x.slot * H + h;
+    const float* beta = reinterpret_cast<const float*>(p.rec + u * GdRec<DK, true>::BYTES + GdRec<DK, true>::SC) + kScBeta * kGdC;
+    // <E, S'> is there after every second chunk and the last; before the
+    // others come the sums of the chunk in between
+    const float* part = p.part + u * 3 * wtot * kGdC + 2 * lane;
+    const float* pn = x.between ? part + static_cast<int64_t>(H) * 3 * wtot * kGdC : part;
+    const float* an = p.anch + (x.between ? u + H : u) * wtot * 2;
+    float2 od = make_float2(0.f, 0.f), s1 = od, s2 = od;
+    float tail = 0.f, next = 0.f;
+    // all loads at once: without branches, so that none waits for another
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float f = i & 1 ? f1 : f0;
-        r[i] = pack_bf16(f * bf16_lo(r[i]), f * bf16_hi(r[i]));
+    for (int t = 0; t < kMaxWarps; ++t) {
+        const bool on = t < wtot;
+        const int tt = on ? t : 0;
+        const float2 a = *reinterpret_cast<const float2*>(part + tt * kGdC);
+        const float2 b = *reinterpret_cast<const float2*>(part + (wtot + tt) * kGdC);
+        const float2 e = *reinterpret_cast<const float2*>(part + (2 * wtot + tt) * kGdC);
+        const float2 f = *reinterpret_cast<const float2*>(pn + tt * kGdC);
+        const float2 k = *reinterpret_cast<const float2*>(pn + (wtot + tt) * kGdC);
+        const float2 n = *reinterpret_cast<const float2*>(an + tt * 2);
+        od.x += on ? a.x : 0.f;
+        od.y += on ? a.y : 0.f;
+        s1.x += on ? b.x : 0.f;
+        s1.y += on ? b.y : 0.f;
+        s2.x += on ? e.x : 0.f;
+        s2.y += on ? e.y : 0.f;
+        tail += on ? n.x + n.y : 0.f;
+        next += on && x.between ? (f.x - k.x) + (f.y - k.y) : 0.f;
     }
-}
-
-template <int DK, bool ONE>
-__global__ void __launch_bounds__(kThreads, ONE ? 3 : 2) gd_grad_kernel(GdParams p)
-{
-    using M = GradSmem<DK>;
-    constexpr int KS = M::KS, NT = DK / 8;
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    constexpr int AS = kGdC + kGdPad;                      // row stride of A and B
-    __nv_bfloat16* sst = reinterpret_cast<__nv_bfloat16*>(smem_raw);
-    __nv_bfloat16* sk = sst + M::kq;
-    __nv_bfloat16* sq = sk + kGdC * KS;
-    float* sc = reinterpret_cast<float*>(sst + M::all);
-
-    const int64_t slot = blockIdx.x;
-    const int hk = blockIdx.y;
-    const int n = gd_seq_of_slot(p.seqs, slot);
-    int64_t row0;
-    int len;
-    p.seqs.span(n, row0, len);
-    if (len < 0) return;
-    const int64_t c = slot - p.seqs.slot0(n, row0);
-    if (c < 0 || c * kGdC >= len) return;
-    const int valid = min(kGdC, len - static_cast<int>(c) * kGdC);
-    const int64_t row = row0 + c * kGdC;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) next += __shfl_xor_sync(0xFFFFFFFFu, next, o);
+    tail += next;
+    const float d1 = od.y - s1.y;
+    float s = (od.x - s1.x) + d1;          // sums over this lane's tokens and all later ones
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float z = __shfl_down_sync(0xFFFFFFFFu, s, o);
+        if (lane + o < 32) s += z;
+    }
+    const float after = __shfl_down_sync(0xFFFFFFFFu, s, 1);
+    const float later = lane < 31 ? after : 0.f;
     [[maybe_unused]] const int64_t rows = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;   // of the checking build
-    const int H = p.seqs.H, group = H / p.seqs.Hk;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, c2 = (lane & 3) * 2;
-    const int nst = p.dv / kSl, wtot = p.dv >> 5;
-
-    float dq[NT][4], dk[NT][4];
-    if (!ONE) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dq[t][e] = dk[t][e] = 0.f;
+    const int64_t at = (static_cast<int64_t>(x.row) + 2 * lane) * H + h;
+    if (2 * lane < x.valid && GLA_DCHECK(at >= 0 && at < rows * H, p.status)) {
+        p.da[at] = s + tail;
+        p.dbeta[at] = s2.x / beta[2 * lane];
     }
-
-    for (int j = 0; j < (ONE ? 1 : group); ++j) {
-        const int h = hk * group + j;
-        const int64_t u = slot * H + h;
-        Src x{p.dO + row * p.ld_do + static_cast<int64_t>(h) * p.dv, p.dvv + row * H * p.dv + static_cast<int64_t>(h) * p.dv,
-              p.vp + u * kGdC * p.dv, p.sb + u * p.dv * DK, p.eb + u * p.dv * DK,
-              p.ld_do, static_cast<int64_t>(H) * p.dv, p.dv, valid};
-        __syncthreads();                   // the last head's scalars and stages are read
-        const float* src_sc = reinterpret_cast<const float*>(p.rec + u * GdRec<DK, true>::BYTES + GdRec<DK, true>::SC);
-        for (int i = tid; i < kGdSc * kGdC; i += kThreads) sc[i] = src_sc[i];
-        load_slice<DK>(sst, x, 0, false, tid);
-        gd_load_rows(sk, KS, p.k + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
-        gd_load_rows(sq, KS, p.q + row * p.ld_qk + hk * DK, p.ld_qk, DK, valid, tid, kThreads);
-        cp_async_commit();
-
-        // pass 1: products over dv of 16 rows with the tokens up to them, before the masks
-        float fa[8][4], fb[8][4];
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) fa[t][e] = fb[t][e] = 0.f;
-        for (int i = 0; i < nst; ++i) {
-            cp_async_wait<0>();
-            __syncthreads();
-            if (i + 1 < nst) load_slice<DK>(sst + ((i + 1) & 1) * M::stage1, x, (i + 1) * kSl, false, tid);
-            cp_async_commit();
-            const __nv_bfloat16* st = sst + (i & 1) * M::stage1;
-            const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
-            const uint32_t br = smem_u32(st + 2 * M::tok + piece_k(lane));
-            constexpr int tk = M::tok * 2;
-#pragma unroll
-            for (int s = 0; s < kSl / 16; ++s) {
-                uint32_t d[4], y[4];
-                ldsm4(d, ar + s * 32);
-                ldsm4(y, ar + tk + s * 32);
-#pragma unroll
-                for (int np = 0; np < 4; ++np) {
-                    if (np > w) continue;
-                    uint32_t b[4];
-                    ldsm4_t(b, br + s * 256 + np * 4 * kGdPiece);
-                    mma_bf16(fa[2 * np], d, b[0], b[1]);
-                    mma_bf16(fa[2 * np + 1], d, b[2], b[3]);
-                    mma_bf16(fb[2 * np], y, b[0], b[1]);
-                    mma_bf16(fb[2 * np + 1], y, b[2], b[3]);
-                }
-            }
-        }
-        __syncthreads();                   // both stages are read
-
-        // da and dbeta of this head: one warp, two tokens a lane
-        if (w == (j & 3)) {
-            // <E, S'> is there after every second chunk and the last; before the
-            // others come the sums of the chunk in between
-            const float* part = p.part + u * 3 * wtot * kGdC + 2 * lane;
-            const bool between = (c & 1) == 0 && (c + 1) * kGdC < len;
-            float2 od = make_float2(0.f, 0.f), s1 = od, s2 = od;
-            float tail = 0.f, next = 0.f;
-#pragma unroll
-            for (int t = 0; t < kMaxWarps; ++t) {          // all loads at once
-                if (t >= wtot) continue;
-                const float2 a = *reinterpret_cast<const float2*>(part + t * kGdC);
-                const float2 b = *reinterpret_cast<const float2*>(part + (wtot + t) * kGdC);
-                const float2 e = *reinterpret_cast<const float2*>(part + (2 * wtot + t) * kGdC);
-                od.x += a.x; od.y += a.y;
-                s1.x += b.x; s1.y += b.y;
-                s2.x += e.x; s2.y += e.y;
-                const int64_t un = between ? u + H : u;
-                const float2 an = *reinterpret_cast<const float2*>(p.anch + (un * wtot + t) * 2);
-                tail += an.x + an.y;
-                if (between) {
-                    const float* pn = part + static_cast<int64_t>(H) * 3 * wtot * kGdC;
-                    const float2 f = *reinterpret_cast<const float2*>(pn + t * kGdC);
-                    const float2 k = *reinterpret_cast<const float2*>(pn + (wtot + t) * kGdC);
-                    next += (f.x - k.x) + (f.y - k.y);
-                }
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) next += __shfl_xor_sync(0xFFFFFFFFu, next, o);
-            tail += next;
-            const float d1 = od.y - s1.y;
-            float s = (od.x - s1.x) + d1;          // sums over this lane's tokens and all later ones
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float z = __shfl_down_sync(0xFFFFFFFFu, s, o);
-                if (lane + o < 32) s += z;
-            }
-            const float after = __shfl_down_sync(0xFFFFFFFFu, s, 1);
-            const float later = lane < 31 ? after : 0.f;
-            const int64_t at = (row + 2 * lane) * H + h;
-            if (2 * lane < valid && GLA_DCHECK(at >= 0 && at < rows * H, p.status)) {
-                p.da[at] = s + tail;
-                p.dbeta[at] = s2.x / sc[kScBeta * kGdC + 2 * lane];
-            }
-            if (2 * lane + 1 < valid && GLA_DCHECK(at + H < rows * H, p.status)) {
-                p.da[at + H] = later + d1 + tail;
-                p.dbeta[at + H] = s2.y / sc[kScBeta * kGdC + 2 * lane + 1];
-            }
-        }
-
-        // masks and decays; A and B as left operands, and to shared memory
-        uint32_t pa[4][4], pb[4][4];
-        {
-            const float bh0 = sc[kScBh * kGdC + 16 * w + g], bl0 = sc[kScBl * kGdC + 16 * w + g];
-            const float bh1 = sc[kScBh * kGdC + 16 * w + g + 8], bl1 = sc[kScBl * kGdC + 16 * w + g + 8];
-            uint32_t* sa = reinterpret_cast<uint32_t*>(sst + (16 * w + g) * AS + c2);
-            uint32_t* sb = reinterpret_cast<uint32_t*>(sst + M::ab + (16 * w + g) * AS + c2);
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                if ((t >> 1) > w) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) pa[t >> 1][2 * (t & 1) + e] = pb[t >> 1][2 * (t & 1) + e] = 0u;
-                    continue;
-                }
-                const float2 qh = *reinterpret_cast<const float2*>(sc + kScBh * kGdC + 8 * t + c2);
-                const float2 ql = *reinterpret_cast<const float2*>(sc + kScBl * kGdC + 8 * t + c2);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = 16 * w + g + 8 * (e >> 1), q = 8 * t + c2 + (e & 1);
-                    const float diff = ((e >> 1 ? bh1 : bh0) - (e & 1 ? qh.y : qh.x)) + ((e >> 1 ? bl1 : bl0) - (e & 1 ? ql.y : ql.x));
-                    const float d = q <= r ? gd_exp2(diff) : 0.f;
-                    fa[t][e] *= d * p.scale;
-                    fb[t][e] = q < r ? -fb[t][e] * d : 0.f;
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t a = pack_bf16(fa[t][2 * e], fa[t][2 * e + 1]), b = pack_bf16(fb[t][2 * e], fb[t][2 * e + 1]);
-                    pa[t >> 1][2 * (t & 1) + e] = a;
-                    pb[t >> 1][2 * (t & 1) + e] = b;
-                    sa[(8 * e * AS + 8 * t) / 2] = a;
-                    sb[(8 * e * AS + 8 * t) / 2] = b;
-                }
-            }
-        }
-        __syncthreads();
-        // dq += A K; dk += A^T Q + B K + B^T K
-        {
-            if (ONE) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) dq[t][e] = dk[t][e] = 0.f;
-            }
-            const uint32_t kt = smem_u32(sk + rows_k(lane, KS)), qt = smem_u32(sq + rows_k(lane, KS));
-            const uint32_t ta = smem_u32(sst + 16 * w + rows_at(lane, AS)), tb = ta + M::ab * 2;
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                uint32_t at[4], bt[4];
-                if (s >= w) {
-                    ldsm4_t(at, ta + s * 16 * AS * 2);
-                    ldsm4_t(bt, tb + s * 16 * AS * 2);
-                }
-#pragma unroll
-                for (int np = 0; np < DK / 16; ++np) {
-                    uint32_t kf[4], qf[4];
-                    ldsm4_t(kf, kt + s * 16 * KS * 2 + np * 32);
-                    if (s <= w) {
-                        mma_bf16(dq[2 * np], pa[s], kf[0], kf[1]);
-                        mma_bf16(dq[2 * np + 1], pa[s], kf[2], kf[3]);
-                        mma_bf16(dk[2 * np], pb[s], kf[0], kf[1]);
-                        mma_bf16(dk[2 * np + 1], pb[s], kf[2], kf[3]);
-                    }
-                    if (s >= w) {
-                        ldsm4_t(qf, qt + s * 16 * KS * 2 + np * 32);
-                        mma_bf16(dk[2 * np], bt, kf[0], kf[1]);
-                        mma_bf16(dk[2 * np + 1], bt, kf[2], kf[3]);
-                        mma_bf16(dk[2 * np], at, qf[0], qf[1]);
-                        mma_bf16(dk[2 * np + 1], at, qf[2], qf[3]);
-                    }
-                }
-            }
-        }
-        __syncthreads();                   // K, Q, A and B are read
-        load_slice<DK>(sst, x, 0, true, tid);
-        cp_async_commit();
-
-        // pass 2: dq += G X S^T, dk += G Y S^T + R V' E^T
-        const float G0 = sc[kScG * kGdC + 16 * w + g], G1 = sc[kScG * kGdC + 16 * w + g + 8];
-        const float R0 = sc[kScR * kGdC + 16 * w + g], R1 = sc[kScR * kGdC + 16 * w + g + 8];
-        for (int i = 0; i < nst; ++i) {
-            cp_async_wait<0>();
-            __syncthreads();
-            if (i + 1 < nst) load_slice<DK>(sst + ((i + 1) & 1) * M::stage2, x, (i + 1) * kSl, true, tid);
-            cp_async_commit();
-            const __nv_bfloat16* st = sst + (i & 1) * M::stage2;
-            const uint32_t ar = smem_u32(st + 16 * w * kVs + rows_a(lane, kVs));
-            const uint32_t vr = smem_u32(st + 2 * M::tok + 2 * w * kGdPiece + piece_at(lane));
-            const uint32_t sr = smem_u32(st + M::stage1 + piece_k(lane));
-            constexpr int tk = M::tok * 2;
-#pragma unroll
-            for (int s = 0; s < kSl / 16; ++s) {
-                uint32_t d[4], y[4], v[4];
-                ldsm4(d, ar + s * 32);
-                ldsm4(y, ar + tk + s * 32);
-                ldsm4_t(v, vr + s * 256);
-                scale_a(d, p.scale * G0, p.scale * G1);
-                scale_a(y, -G0, -G1);
-                scale_a(v, R0, R1);
-#pragma unroll
-                for (int np = 0; np < DK / 16; ++np) {
-                    uint32_t sf[4], ef[4];
-                    ldsm4_t(sf, sr + s * 256 + np * 4 * kGdPiece);
-                    ldsm4_t(ef, sr + M::st * 2 + s * 256 + np * 4 * kGdPiece);
-                    mma_bf16(dq[2 * np], d, sf[0], sf[1]);
-                    mma_bf16(dq[2 * np + 1], d, sf[2], sf[3]);
-                    mma_bf16(dk[2 * np], y, sf[0], sf[1]);
-                    mma_bf16(dk[2 * np + 1], y, sf[2], sf[3]);
-                    mma_bf16(dk[2 * np], v, ef[0], ef[1]);
-                    mma_bf16(dk[2 * np + 1], v, ef[2], ef[3]);
-                }
-            }
-        }
-    }
-    // out through this warp's own rows of the K and Q tiles
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int at = (16 * w + g + 8 * hf) * KS + 8 * t + c2;
-            *reinterpret_cast<uint32_t*>(sq + at) = pack_bf16(dq[t][2 * hf], dq[t][2 * hf + 1]);
-            *reinterpret_cast<uint32_t*>(sk + at) = pack_bf16(dk[t][2 * hf], dk[t][2 * hf + 1]);
-        }
-    __syncwarp();
-    const int64_t ld = static_cast<int64_t>(p.seqs.Hk) * DK;
-    for (int i = lane; i < 16 * (DK / 8); i += 32) {
-        const int r = 16 * w + i / (DK / 8), cc = (i % (DK / 8)) * 8;
-        if (r < valid && GLA_DCHECK(row + r < rows, p.status)) {
-            const int64_t at = (row + r) * ld + hk * DK + cc;
-            *reinterpret_cast<uint4*>(p.dq + at) = *reinterpret_cast<const uint4*>(sq + r * KS + cc);
-            *reinterpret_cast<uint4*>(p.dkk + at) = *reinterpret_cast<const uint4*>(sk + r * KS + cc);
-        }
+    if (2 * lane + 1 < x.valid && GLA_DCHECK(at + H < rows * H, p.status)) {
+        p.da[at + H] = later + d1 + tail;
+        p.dbeta[at + H] = s2.y / beta[2 * lane + 1];
     }
 }
 
-template <int DK, bool ONE>
-gla_status launch(const GdParams& p, cudaStream_t st)
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 1) gd_grad_kernel(GdParams p, const __grid_constant__ Maps maps, WaitCtl ctl)
 {
-    constexpr int smem = GradSmem<DK>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(gd_grad_kernel<DK, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    using C = Cols<DK>;
+    using M = Smem<DK>;
+    using Rec = GdRec<DK, true>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Bars& B = *reinterpret_cast<Bars*>(smem + M::BARS);
+    static_assert(sizeof(Bars) <= 256, "");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int H = p.seqs.H, group = H / p.seqs.Hk, ns = (p.dv + kCols - 1) / kCols;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&B.full[i], 1);
+            mbar_init(&B.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.sc[i], 1);
+            mbar_init(&B.sc_done[i], kGdWorkers);
+        }
+        uint64_t* one[4] = {&B.kq, &B.d123, &B.d4, &B.drain};
+        for (uint64_t* b : one) mbar_init(b, 1);
+        uint64_t* from_workers[3] = {&B.kq_done, &B.w, &B.read};
+        for (uint64_t* b : from_workers) mbar_init(b, kGdWorkers);
+        mbar_init_fence();
+    }
+    for (int i = tid; i < 8192 / 16; i += kThreads) reinterpret_cast<uint4*>(smem + M::Z)[i] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+    if (warp == kGdWorkers + 1) {
+        tmem_alloc(&B.tmem, C::ALLOC);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = B.tmem;
+
+    if (warp == kGdWorkers) {
+        // ---- b; slices of dO, dv, V' and the states
+        int step = 0, n = 0;
+        for_units(p, lane, [&](const Unit& x) {
+            bool ok = true;
+            for (int j = 0; j < group && ok; ++j) {
+                if (lane == 0) {
+                    const int h = x.hk * group + j;
+                    const int64_t u = x.slot * H + h;
+                    const int b = step & 1;
+                    ok = step < 2 || mbar_wait(&B.sc_done[b], ((step >> 1) - 1) & 1, ctl);
+                    if (ok) {
+                        mbar_arrive_expect_tx(&B.sc[b], M::SCB);
+                        bulk_load(smem + M::SC + b * M::SCB, p.rec + u * Rec::BYTES + Rec::SC + kScBh * kGdC * 4, M::SCB, &B.sc[b]);
+                        ++step;
+                    }
+                    for (int s = 0; s < ns && ok; ++s, ++n) {
+                        const int st = n % kStages, col = s * kCols, left = min(kCols, p.dv - col);
+                        ok = n < kStages || mbar_wait(&B.empty[st], (n / kStages - 1) & 1, ctl);
+                        if (!ok) break;
+                        unsigned char* at = smem + st * M::STAGE;
+                        const uint32_t vb = left / 32 * M::VB, sb = left / 32 * M::SB;
+                        const int64_t block = (u * p.dv + col) / 32;
+                        mbar_arrive_expect_tx(&B.full[st], 16384 + vb + 2 * sb);
+                        tma_load_2d(at + M::X, &maps.dO, &B.full[st], h * p.dv + col, x.row);
+                        tma_load_2d(at + M::Y, &maps.dv, &B.full[st], h * p.dv + col, x.row);
+                        bulk_load(at + M::V, p.vp + block * (M::VB / 2), vb, &B.full[st]);
+                        bulk_load(at + M::S, p.sb + block * (M::SB / 2), sb, &B.full[st]);
+                        bulk_load(at + M::E, p.eb + block * (M::SB / 2), sb, &B.full[st]);
+                    }
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(ok), 0) != 0;
+            }
+            return ok;
+        });
+        // no copy may be in flight when the block ends
+        if (lane == 0) {
+            for (int i = max(0, n - kStages); i < n; ++i) mbar_wait(&B.full[i % kStages], (i / kStages) & 1, ctl);
+            for (int i = max(0, step - 2); i < step; ++i) mbar_wait(&B.sc[i & 1], (i >> 1) & 1, ctl);
+        }
+        __syncwarp();
+    } else if (warp == kGdWorkers + 3) {
+        // ---- K and Q, and in their place dk and dq on the way out
+        int step = 0, last_row = 0, last_hk = -1;             // heads so far; what waits to leave
+        auto leave = [&]() {                                  // dq and dk of the step before, where whole
+            if (step == 0) return true;
+            if (!mbar_wait(&B.kq_done, (step - 1) & 1, ctl)) return false;
+            if (last_hk >= 0) {
+                for (int b = 0; b < DK / 32; ++b) {
+                    tma_store_2d(&maps.dq, smem + M::Q + b * 4096, last_hk * DK + 32 * b, last_row);
+                    tma_store_2d(&maps.dk, smem + M::K + b * 4096, last_hk * DK + 32 * b, last_row);
+                }
+                tma_store_commit();
+                tma_store_wait_read();
+            }
+            return true;
+        };
+        for_units(p, lane, [&](const Unit& x) {
+            bool ok = true;
+            for (int j = 0; j < group && ok; ++j) {
+                if (lane == 0) {
+                    const unsigned char* rec = p.rec + (x.slot * H + x.hk * group + j) * Rec::BYTES;
+                    bulk_prefetch_l2(rec, kGdC * DK * 2);
+                    ok = leave();
+                    if (ok) {
+                        mbar_arrive_expect_tx(&B.kq, 2 * kGdC * DK * 2);
+                        bulk_load(smem + M::K, rec, kGdC * DK * 2, &B.kq);
+                        for (int b = 0; b < DK / 32; ++b)
+                            tma_load_2d(smem + M::Q + b * 4096, &maps.q, &B.kq, x.hk * DK + 32 * b, x.row);
+                        last_row = x.row;
+                        last_hk = j + 1 == group && x.valid == kGdC ? x.hk : -1;
+                        ++step;
+                    }
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(ok), 0) != 0;
+            }
+            return ok;
+        });
+        if (lane == 0) {
+            leave();
+            tma_store_wait_read();
+            if (step > 0) mbar_wait(&B.kq, (step - 1) & 1, ctl);
+        }
+        __syncwarp();
+    } else if (warp == kGdWorkers + 1) {
+        // ---- products
+        int step = 0, n = 0;
+        constexpr uint32_t id1 = idesc_bf16_f32(128, 64, 0, 1), id2 = idesc_bf16_f32(128, DK, 0, 1);
+        constexpr uint32_t id3 = idesc_bf16_f32(128, DK, 1, 1);
+        // A, B and the state's part of step t into dq and dk
+        auto last_product = [&](int t) {
+            if (!mbar_wait(&B.kq, t & 1, ctl) || !mbar_wait(&B.w, t & 1, ctl)) return false;
+            tc_fence_after();
+            const uint64_t k_n = smem_desc(smem_u32(smem + M::K), 4096, 512, kLayoutSW64);
+            const uint64_t q_n = smem_desc(smem_u32(smem + M::Q), 4096, 512, kLayoutSW64);
+            const uint64_t ab = smem_desc(smem_u32(smem + M::A), 16, 1024, kLayoutSW128);
+            const uint64_t at = smem_desc(smem_u32(smem + M::Z), 8192, 1024, kLayoutSW128);         // zeros, then A
+            const uint64_t bt = smem_desc(smem_u32(smem + M::Z), 16384, 1024, kLayoutSW128);        // zeros, then B
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                umma_bf16(tm + C::D4, desc_add(ab, 32 * k), desc_add(k_n, 1024 * k), id2, k > 0);
+                umma_bf16(tm + C::D4, desc_add(bt, 2048 * k), desc_add(k_n, 1024 * k), id3, 1);
+                umma_bf16(tm + C::D4, desc_add(at, 2048 * k), desc_add(q_n, 1024 * k), id3, 1);
+            }
+            umma_commit(&B.d4);
+            return true;
+        };
+        for_units(p, lane, [&](const Unit&) {
+            bool ok = true;
+            for (int j = 0; j < group && ok; ++j, ++step) {
+                if (lane == 0) {
+                    ok = step == 0 || mbar_wait(&B.read, (step - 1) & 1, ctl);
+                    const uint32_t d1 = tm + C::D1 + 64 * (step & 1);
+                    for (int s = 0; s < ns && ok; ++s, ++n) {
+                        const int st = n % kStages, left = p.dv - s * kCols;
+                        ok = mbar_wait(&B.full[st], (n / kStages) & 1, ctl);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t at = smem_u32(smem + st * M::STAGE);
+                        const uint64_t xy = smem_desc(at + M::X, 16, 1024, kLayoutSW128);
+                        const uint64_t v = smem_desc(at + M::V, kPieceBytes, 256, kLayoutSW32);
+                        const uint64_t vl = smem_desc(at + M::V - M::VB, kPieceBytes, 256, kLayoutSW32);
+                        const uint64_t sd = smem_desc(at + M::S, kPieceBytes, 256, kLayoutSW32);
+                        const uint64_t ed = smem_desc(at + M::E, kPieceBytes, 256, kLayoutSW32);
+                        const uint32_t on = s > 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k >= 2 && left == 32) break;
+                            const uint32_t vo = (k >> 1) * M::VB + (k & 1) * 512, so = (k >> 1) * M::SB + (k & 1) * 512;
+                            const uint32_t acc = k > 0 ? 1 : on;
+                            const uint64_t a = desc_add(xy, 32 * k);
+                            umma_bf16(d1, a, desc_add(v, vo), id1, acc);
+                            umma_bf16(tm + C::D2, a, desc_add(sd, so), id2, acc);
+                            umma_bf16(tm + C::D3, desc_add(vl, vo), desc_add(ed, so), id3, acc);
+                        }
+                        umma_commit(&B.empty[st]);
+                        // while the workers get to this unit: the last product of the one before
+                        if (s == 0 && step > 0) ok = last_product(step - 1);
+                    }
+                    if (ok) umma_commit(&B.d123);
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(ok), 0) != 0;
+            }
+            return ok;
+        });
+        if (lane == 0) {
+            if (step > 0) last_product(step - 1);
+            umma_commit(&B.drain);
+            mbar_wait(&B.drain, 0, ctl);
+        }
+        __syncwarp();
+    } else if (warp == kGdWorkers + 2) {
+        // ---- da and dbeta
+        for_units(p, lane, [&](const Unit& x) {
+            for (int j = 0; j < group; ++j) sums<DK>(p, x, x.hk * group + j, lane);
+            return true;
+        });
+    } else {
+        // ---- workers: lane = token of dq or of dk, half of the columns
+        const int half = warp >> 2, i = (warp & 1) * 32 + lane;
+        const bool is_k = (warp & 2) != 0;
+        const uint32_t t0 = tm + (static_cast<uint32_t>(warp & 3) << 21);
+        constexpr int HS = DK / 2;
+        [[maybe_unused]] const int64_t rows = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;
+        int step = 0;
+        for_units(p, lane, [&](const Unit& x) {
+            float acc[HS];
+#pragma unroll
+            for (int e = 0; e < HS; ++e) acc[e] = 0.f;
+            for (int j = 0; j < group; ++j, ++step) {
+                const float* own = reinterpret_cast<const float*>(p.rec + (x.slot * H + x.hk * group + j) * Rec::BYTES + Rec::SC) + i;
+                const float g = own[kScG * kGdC], f2 = is_k ? -g : p.scale * g, f3 = own[kScR * kGdC];
+                if (!warp_wait(&B.d123, step & 1, ctl)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < HS / 16; ++k) {
+                    uint32_t d[16], e[16];
+                    tmem_ld16(t0 + C::D2 + half * HS + 16 * k, d);
+                    if (is_k) tmem_ld16(t0 + C::D3 + half * HS + 16 * k, e);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) {
+                        acc[16 * k + t] = fmaf(f2, __uint_as_float(d[t]), acc[16 * k + t]);
+                        if (is_k) acc[16 * k + t] = fmaf(f3, __uint_as_float(e[t]), acc[16 * k + t]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.read);
+                if (!warp_wait(&B.sc[step & 1], (step >> 1) & 1, ctl)) return false;
+                // A or B, 16 columns at a time: up to the diagonal, in the sequence
+                // (a loop: a first pass waits for every line of its code)
+                {
+                    const float* sc = reinterpret_cast<const float*>(smem + M::SC + (step & 1) * M::SCB);     // b, high and low
+                    const float bh = sc[i], bl = sc[kGdC + i], f = is_k ? -1.f : p.scale;
+                    const int end = i >= x.valid ? 0 : i + !is_k;                 // columns of this row
+                    unsigned char* tile = smem + M::A + (is_k ? 8192 : 0);
+#pragma unroll 1
+                    for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                        uint32_t w[8];
+                        if (16 * c > (warp & 1) * 32 + 31) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = 0u;
+                        } else {
+                            uint32_t d[16];
+                            tmem_ld16(t0 + C::D1 + 64 * (step & 1) + 16 * c, d);
+                            float m[16];
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                const float4 jh = *reinterpret_cast<const float4*>(sc + 16 * c + e);
+                                const float4 jl = *reinterpret_cast<const float4*>(sc + kGdC + 16 * c + e);
+                                m[e] = f * gd_exp2((bh - jh.x) + (bl - jl.x));
+                                m[e + 1] = f * gd_exp2((bh - jh.y) + (bl - jl.y));
+                                m[e + 2] = f * gd_exp2((bh - jh.z) + (bl - jl.z));
+                                m[e + 3] = f * gd_exp2((bh - jh.w) + (bl - jl.w));
+                            }
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                m[e] *= __uint_as_float(d[e]);
+                                if (16 * c + e >= end) m[e] = 0.f;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = pack_bf16(m[2 * e], m[2 * e + 1]);
+                        }
+                        *reinterpret_cast<uint4*>(tile + swz_off(i, 2 * c, 128)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(tile + swz_off(i, 2 * c + 1, 128)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+                if (x.valid < kGdC && (warp & 3) == 0) {
+                    // rows of Q behind the sequence's end are another's: zeros times them need not be zeros
+                    if (!warp_wait(&B.kq, step & 1, ctl)) return false;
+                    for (int r = x.valid + half; r < kGdC; r += 2)
+                        for (int b = lane; b < DK / 8; b += 32)
+                            *reinterpret_cast<uint4*>(smem + M::Q + (b >> 2) * 4096 + r * 64 + (b & 3) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&B.w);
+                    mbar_arrive(&B.sc_done[step & 1]);
+                }
+                if (!warp_wait(&B.d4, step & 1, ctl)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < HS / 16; ++k) {
+                    uint32_t d[16];
+                    tmem_ld16(t0 + C::D4 + half * HS + 16 * k, d);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) acc[16 * k + t] += __uint_as_float(d[t]);
+                }
+                if (j + 1 == group) {
+                    // out: through K's and Q's place where the chunk is whole
+                    unsigned char* tile = smem + (is_k ? M::K : M::Q);
+                    __nv_bfloat16* out = is_k ? p.dkk : p.dq;
+                    const int64_t at = (static_cast<int64_t>(x.row) + i) * p.seqs.Hk * DK + x.hk * DK + half * HS;
+#pragma unroll
+                    for (int e = 0; e < HS; e += 8) {
+                        uint4 w;
+                        w.x = pack_bf16(acc[e], acc[e + 1]);
+                        w.y = pack_bf16(acc[e + 2], acc[e + 3]);
+                        w.z = pack_bf16(acc[e + 4], acc[e + 5]);
+                        w.w = pack_bf16(acc[e + 6], acc[e + 7]);
+                        const int k = (half * HS + e) >> 3;
+                        if (x.valid == kGdC) *reinterpret_cast<uint4*>(tile + (k >> 2) * 4096 + swz_off(i, k & 3, 64)) = w;
+                        else if (i < x.valid && GLA_DCHECK(x.row + i < rows, p.status)) *reinterpret_cast<uint4*>(out + at + e) = w;
+                    }
+                    fence_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.kq_done);
+            }
+            return true;
+        });
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kGdWorkers + 1) tmem_dealloc(tm, C::ALLOC);
+}
+
+template <int DK>
+gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
+{
+    const uint64_t tokens = p.seqs.cu ? p.seqs.T : static_cast<uint64_t>(p.seqs.N) * p.seqs.T;
+    const int64_t wv = static_cast<int64_t>(p.seqs.H) * p.dv, wk = static_cast<int64_t>(p.seqs.Hk) * DK;
+    auto map = [&](CUtensorMap* m, const void* base, int64_t width, int64_t ld, uint32_t box, int swizzle) {
+        const uint64_t dims[2] = {static_cast<uint64_t>(width), tokens}, strides[2] = {2, static_cast<uint64_t>(ld) * 2};
+        const uint32_t boxes[2] = {box, kGdC};
+        return make_tmap(m, base, 2, dims, strides, boxes, 2, swizzle);
+    };
+    Maps maps;
+    gla_status s;
+    if ((s = map(&maps.dO, p.dO, wv, p.ld_do, kCols, 128)) != GLA_OK || (s = map(&maps.dv, p.dvv, wv, wv, kCols, 128)) != GLA_OK ||
+        (s = map(&maps.q, p.q, wk, p.ld_qk, 32, 64)) != GLA_OK || (s = map(&maps.dq, p.dq, wk, wk, 32, 64)) != GLA_OK ||
+        (s = map(&maps.dk, p.dkk, wk, wk, 32, 64)) != GLA_OK)
+        return s;
+    constexpr int smem = Smem<DK>::bytes;
+    cudaError_t e = cudaFuncSetAttribute(gd_grad_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return status_of(e);
+    const int64_t units = p.slots * p.seqs.Hk;
     trace_begin(st);
-    gd_grad_kernel<DK, ONE><<<dim3(static_cast<unsigned>(p.slots), static_cast<unsigned>(p.seqs.Hk)), kThreads, smem, st>>>(p);
+    gd_grad_kernel<DK><<<static_cast<unsigned>(units < kSms ? units : kSms), kThreads, smem, st>>>(p, maps, ctl);
     trace_end(st, "gd_grad_kernel");
     count_launch();
     return check_launch("gd_grad_kernel");
 }
 
-template <int DK>
-gla_status pick(const GdParams& p, cudaStream_t st)
-{
-    return p.seqs.H == p.seqs.Hk ? launch<DK, true>(p, st) : launch<DK, false>(p, st);
-}
-
 }  // namespace
 
-gla_status gd_launch_grad(const GdParams& p, cudaStream_t st)
+gla_status gd_launch_grad(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
 {
     if (p.slots == 0) return GLA_OK;
     switch (p.dk) {
-    case 64: return pick<64>(p, st);
-    case 96: return pick<96>(p, st);
-    default: return pick<128>(p, st);
+    case 64: return launch<64>(p, ctl, st);
+    case 96: return launch<96>(p, ctl, st);
+    default: return launch<128>(p, ctl, st);
     }
 }
 

@@ -254,7 +254,7 @@ gla_status gated_delta_chunk_bwd(const void* q, const void* k, const void* v, co
     if ((s = gd_launch_chunks(p, true, stream)) != GLA_OK) return s;
     if (p.nseg > 1 && (s = gd_launch_segment_states(p, ctl, stream)) != GLA_OK) return s;
     if ((s = gd_launch_sweeps_bwd(p, ctl, stream)) != GLA_OK) return s;
-    return gd_launch_grad(p, stream);
+    return gd_launch_grad(p, ctl, stream);
 }
 
 gla_status gated_delta_decode_step(float* state, const int32_t* slot_idx, int n_slots, const void* q, const void* k,
