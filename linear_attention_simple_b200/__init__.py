@@ -720,8 +720,16 @@ def _gated_delta_args(fn, q, k, v, a, beta, lead, cu_seqlens, types):
     dev = q.device
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    _fit(a, "a", torch.float32, lead + (H,), dev)
-    _fit(beta, "beta", torch.float32, lead + (H,), dev)
+    # a step on few sequences lasts as long as its checks: one test when all is right
+    per_head, dt = lead + (H,), q.dtype
+    if a.dtype is beta.dtype is torch.float32 and k.dtype is v.dtype is dt and \
+            a.shape == beta.shape == per_head and q.shape == k.shape and v.shape[:-2] == lead and \
+            q.shape[:-2] == lead and a.device == beta.device == k.device == v.device == dev and \
+            a.is_contiguous() and beta.is_contiguous() and q.is_contiguous() and k.is_contiguous() and \
+            v.is_contiguous():
+        return Hk, H, dk, dv, 0
+    _fit(a, "a", torch.float32, per_head, dev)
+    _fit(beta, "beta", torch.float32, per_head, dev)
     ld, packed = [], True
     for x, name, h, d in ((q, "q", Hk, dk), (k, "k", Hk, dk), (v, "v", H, dv)):
         if x.is_contiguous():
@@ -753,11 +761,11 @@ def _sequences(fn, q, v, cu_seqlens):
     return lead, cu_seqlens.numel() - 1, lead[0]
 
 
-def _new(t, name, shape, dtype, device):
-    """`t` checked against shape and type, or a new tensor."""
+def _new(t, name, shape, dtype, like):
+    """`t` checked against shape and type, or a new tensor on `like`'s device."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _fit(t, name, dtype, shape, device)
+        return like.new_empty(shape, dtype=dtype)
+    _fit(t, name, dtype, shape, like.device)
     return t
 
 
@@ -779,9 +787,9 @@ def gated_delta_chunk_fwd(q, k, v, a, beta, s0=None, cu_seqlens=None, o=None, s_
                                           (torch.bfloat16,))
     dev = q.device
     _fit(s0, "s0", torch.float32, (N, H, dk, dv), dev)
-    o = _new(o, "o", lead + (H, dv), torch.bfloat16, dev)
+    o = _new(o, "o", lead + (H, dv), torch.bfloat16, q)
     if s_final is not None or want_final_state:
-        s_final = _new(s_final, "s_final", (N, H, dk, dv), torch.float32, dev)
+        s_final = _new(s_final, "s_final", (N, H, dk, dv), torch.float32, q)
     ws = _workspace(ws, gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None), dev)
     _call_on(dev, "gated_delta_chunk_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), beta.data_ptr(),
              _data(cu_seqlens), _data(s0), o.data_ptr(), _data(s_final), ws.data_ptr(), ws.numel(), N, T, Hk, H, dk, dv,
@@ -803,13 +811,13 @@ def gated_delta_chunk_bwd(q, k, v, a, beta, dO, s0=None, ds_final=None, cu_seqle
     _fit(ds_final, "ds_final", f32, (N, H, dk, dv), dev)
     _fit(dO, "dO", bf16, lead + (H, dv), dev)
     gq, gk, gv, ga, gb, gs = grads if grads is not None else (None,) * 6
-    gq = _new(gq, "grad_q", lead + (Hk, dk), bf16, dev)
-    gk = _new(gk, "grad_k", lead + (Hk, dk), bf16, dev)
-    gv = _new(gv, "grad_v", lead + (H, dv), bf16, dev)
-    ga = _new(ga, "grad_a", lead + (H,), f32, dev)
-    gb = _new(gb, "grad_beta", lead + (H,), f32, dev)
+    gq = _new(gq, "grad_q", lead + (Hk, dk), bf16, q)
+    gk = _new(gk, "grad_k", lead + (Hk, dk), bf16, q)
+    gv = _new(gv, "grad_v", lead + (H, dv), bf16, q)
+    ga = _new(ga, "grad_a", lead + (H,), f32, q)
+    gb = _new(gb, "grad_beta", lead + (H,), f32, q)
     if gs is not None or (want_grad_s0 and grads is None):
-        gs = _new(gs, "grad_s0", (N, H, dk, dv), f32, dev)
+        gs = _new(gs, "grad_s0", (N, H, dk, dv), f32, q)
     ws = _workspace(ws, gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None, True), dev)
     _call_on(dev, "gated_delta_chunk_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), beta.data_ptr(),
              _data(cu_seqlens), _data(s0), dO.data_ptr(), _data(ds_final), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
@@ -836,7 +844,7 @@ def gated_delta_decode_step(state, q, k, v, a, beta, o=None, slot_idx=None, scal
     _fit(slot_idx, "slot_idx", torch.int32, (N,), dev)
     if slot_idx is None and state.shape[0] != N:
         raise ValueError("without slot_idx the state must have N slots")
-    o = _new(o, "o", lead + (H, dv), torch.float32, dev)
+    o = _new(o, "o", lead + (H, dv), torch.float32, q)
     _call_on(dev, "gated_delta_decode_step", state.data_ptr(), _data(slot_idx), state.shape[0], q.data_ptr(),
              k.data_ptr(), v.data_ptr(), a.data_ptr(), beta.data_ptr(), o.data_ptr(), N, T, Hk, H, dk, dv, ld,
              dk ** -0.5 if scale is None else scale, _dt(q), stream=stream)
@@ -881,7 +889,7 @@ def group_norm_silu(x, weight=None, bias=None, gate=None, center=True, act=True,
     n * silu(gate), or silu(n) without a gate (act=False: the identity in
     silu's place), bf16 in x's shape."""
     M, G, d, ldx, ldg, shared = _norm_args(x, weight, bias, gate)
-    y = _new(y, "y", x.shape, torch.bfloat16, x.device)
+    y = _new(y, "y", x.shape, torch.bfloat16, x)
     _call_on(x.device, "group_norm_silu", x.data_ptr(), _data(gate), _data(weight), _data(bias), y.data_ptr(), M, G, d,
              ldx, ldg, shared, int(center), int(act), eps, _dt(x), stream=stream)
     return y
@@ -900,10 +908,10 @@ def group_norm_silu_bwd(x, dy, weight=None, bias=None, gate=None, center=True, a
     dev, f32 = x.device, torch.float32
     _fit(dy, "dy", torch.bfloat16, x.shape, dev)
     gx, gg, gw, gb = grads if grads is not None else (None,) * 4
-    gx = _new(gx, "grad_x", x.shape, x.dtype, dev)
-    gg = _new(gg, "grad_gate", x.shape, torch.bfloat16, dev) if gate is not None else None
-    gw = _new(gw, "grad_weight", weight.shape, f32, dev) if weight is not None else None
-    gb = _new(gb, "grad_bias", bias.shape, f32, dev) if bias is not None else None
+    gx = _new(gx, "grad_x", x.shape, x.dtype, x)
+    gg = _new(gg, "grad_gate", x.shape, torch.bfloat16, x) if gate is not None else None
+    gw = _new(gw, "grad_weight", weight.shape, f32, x) if weight is not None else None
+    gb = _new(gb, "grad_bias", bias.shape, f32, x) if bias is not None else None
     if ws is not None or gw is not None or gb is not None:
         ws = _workspace(ws, group_norm_silu_bwd_workspace_bytes(M, G, d), dev)
     _call_on(dev, "group_norm_silu_bwd", x.data_ptr(), _data(gate), _data(weight), _data(bias), dy.data_ptr(),
