@@ -9,8 +9,8 @@
 // at one token that stream is all there is (0.9 flop a byte): HBM bandwidth
 // bounds it.  One CTA per (sequence, head, slice of columns); a thread holds
 // a float4 of columns in every RG-th row, all loads in flight before the
-// first use.  Columns of S do not meet, so with few (sequence, head) pairs
-// the columns are spread over more CTAs.  Everything is fp32.
+// first use.  Columns of S do not meet, so they may be spread over more CTAs.
+// Everything is fp32.
 #include <cuda_bf16.h>
 
 #include "gated_delta.cuh"
@@ -39,14 +39,15 @@ struct StepParams {
     int* status;
 };
 
-// Sixteen rows a thread: 64 registers of state, and room for the rest below 96,
-// so that two CTAs share an SM at 192 columns.
+// Sixteen rows a thread: 64 registers of state, and room for the rest below
+// kRegs, so that two CTAs share an SM at 192 columns.
 template <int DK>
 constexpr int row_groups() { return DK / 16; }
+constexpr int kRegs = 96;
 constexpr int kMaxQuads = 64;              // float4 column groups of a CTA (dv <= 256)
 
 template <int DK, class Tin>
-__global__ void __maxnreg__(96) gd_step_kernel(StepParams p)
+__global__ void __maxnreg__(kRegs) gd_step_kernel(StepParams p)
 {
     constexpr int RG = row_groups<DK>(), R = DK / RG;
     __shared__ float2 s_kq[2][DK];
@@ -150,6 +151,22 @@ gla_status launch(const StepParams& p, int N, bool f32, cudaStream_t st)
     return check_launch("gd_step_kernel");
 }
 
+// Columns of a CTA.  64 keep the most threads on an SM, and the tokens' barriers
+// in few warps; 16 heads, whole rows against 64 columns: 300 sequences of 128 x
+// 256 252 and 212 us, of 96 x 192 with four tokens 194 and 162, one sequence 9.7
+// and 8.6.  But where whole rows leave the threads on the SM and there is one
+// token, their longer runs in memory pay: 1,280 sequences of 96 x 192 464 against
+// 488 us.  Widths that are no multiple of 64 take whole rows (300 sequences of
+// 64 x 160 68 us, 109 with 32 columns), or 32 columns while there are too few
+// CTAs (3 sequences of 96 x 96 10.0 and 9.2).
+int slice_width(int64_t units, int T, int dk, int dv)
+{
+    const int threads = dk / 16 * (dv >> 2), fit = 65536 / kRegs / threads * threads;
+    const bool many = units >= 296;
+    if (dv % 64 == 0) return many && T == 1 && fit >= 576 ? dv : 64;
+    return many ? dv : 32;
+}
+
 }  // namespace
 
 gla_status gd_launch_step(float* state, const int32_t* slot_idx, int n_slots, const void* q, const void* k,
@@ -157,9 +174,8 @@ gla_status gd_launch_step(float* state, const int32_t* slot_idx, int n_slots, co
                           int dk, int dv, int64_t ld_qk, int64_t ld_v, float scale, bool f32, int* status,
                           cudaStream_t st)
 {
-    // whole rows of columns a CTA once there are CTAs enough for every SM, else 32 columns
-    const int64_t units = static_cast<int64_t>(N) * H;
-    StepParams p{state, slot_idx, q, k, v, a, beta, o, n_slots, T, H, Hk, dv, units >= 296 ? dv : 32, ld_qk, ld_v, scale, status};
+    const StepParams p{state, slot_idx, q, k, v, a, beta, o, n_slots, T, H, Hk, dv,
+                       slice_width(static_cast<int64_t>(N) * H, T, dk, dv), ld_qk, ld_v, scale, status};
     switch (dk) {
     case 64: return launch<64>(p, N, f32, st);
     case 96: return launch<96>(p, N, f32, st);
