@@ -107,6 +107,25 @@ def test_chunk_bwd(N, T, Hk, H, dk, dv, with_states):
     check_bwd(d, s0, dO, ds)
 
 
+def test_more_chunks_than_fit_at_once():
+    """The gradients' kernel walks over the chunks: several rounds of it, dense and
+    packed with sequences that are empty."""
+    N, T, H, dk, dv = 300, 65, 8, 64, 32
+    d, dO = make((N, T), H, H, dk, dv, 71), make((N, T), H, H, dk, dv, 72)["v"]
+    check_bwd(d, states(N, H, dk, dv, 73), dO, states(N, H, dk, dv, 74))
+    lens = [3, 0, 70, 0, 0, 1] * 60
+    d, dO = make((sum(lens),), 4, 8, dk, dv, 75), make((sum(lens),), 4, 8, dk, dv, 76)["v"]
+    got = gla.gated_delta_chunk_bwd(*args(d), dO, cu_seqlens=cu_of(lens))
+    # the pattern of lengths repeats: a dense call on each of its sequences
+    x = {n: t.view(60, 74, *t.shape[1:]) for n, t in dict(d, dO=dO).items()}
+    out = [t.view(60, 74, *t.shape[1:]) for t in got[:5]]
+    for b, e in ((0, 3), (3, 73), (73, 74)):
+        part = {n: t[:, b:e].contiguous() for n, t in x.items()}
+        want = gla.gated_delta_chunk_bwd(*args(part), part["dO"])
+        for u, v in zip(out, want):
+            assert torch.equal(u[:, b:e], v)
+
+
 # few heads and long sequences: both directions cut them into segments
 LONG = [(1, 1600, 1, 1, 96, 192, None), (2, 2100, 1, 2, 128, 128, None), (1, 1537, 2, 2, 64, 256, None),
         (1, 1793, 1, 1, 96, 160, None), (1, 0, 1, 2, 96, 192, [700, 0, 1200, 65]), (1, 0, 1, 1, 128, 32, [1, 1700])]
