@@ -31,7 +31,7 @@
 // (chunk, head): a ring of three stages of 64 dv columns keeps the loads going,
 // and the products of the next unit start as soon as D2 and D3 are read (D1 has
 // two buffers).  Every byte is read once, and HBM bounds it: 8 x 2,048 tokens,
-// 16 heads of 96 x 192, 855 MB in 146 us, 5.9 TB/s.  (With mma.sync, two passes
+// 16 heads of 96 x 192, 819 MB in 146 us, 5.6 TB/s.  (With mma.sync, two passes
 // over dv and 12 warps an SM, latency did: 272 us.)
 #include "gated_delta_tc.cuh"
 
