@@ -156,8 +156,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ int rows_n(int lane, int ld) { return ((lane & 7) + ((lane >> 4) << 3)) * ld + (((lane >> 3) & 1) << 3); }
 __device__ __forceinline__ int rows_a(int lane, int ld) { return (lane & 15) * ld + ((lane >> 4) << 3); }
 
-// 2^x for the decay factors: x <= 0 here (0 -> 1, very negative -> 0).
-__device__ __forceinline__ float gd_exp2(float x) { return exp2f(x); }
+// 2^x for the decay factors, x <= 0 where the result is used (0 -> 1, below
+// -126 -> 0: such a factor is lost in any sum with others).
+__device__ __forceinline__ float gd_exp2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // ---- parameters
 struct GdParams {

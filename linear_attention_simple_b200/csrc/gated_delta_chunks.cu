@@ -9,7 +9,7 @@
 // forward substitution, a warp each and a column per lane; then the blocks
 // below them, -T22 L21 T11, at 16 and at 32 rows.  (Substitution over all 64
 // rows, a column per thread, left two of the four warps waiting: 125 us
-// against 91 at 8 x 16 heads x 2,048 tokens, 81 with the blocks on tensor
+// against 91 at 8 x 16 heads x 2,048 tokens, 80 with the blocks on tensor
 // cores.)  The running sum of the log-decays is taken in 64 bits, so that the differences
 // behind a strong decay (a reset between documents) keep their precision; a
 // is taken no lower than -10^4, where e^a is 0 in any case.
