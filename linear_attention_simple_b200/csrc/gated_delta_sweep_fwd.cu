@@ -32,8 +32,9 @@
 // zeros) and A (the same sweep with V = 0 from the identity: dk more rows), a
 // small fp32 kernel hands the states on from segment to segment, and the sweep
 // proper starts every segment from its own.  The pass needs neither Q, P nor o:
-// two of its CTAs share an SM at dk = 128 too (169 us with one each, 143 so).  One prompt of 16,384 tokens at 16
-// heads of 128 x 128: 783 us in one piece, 273 us so (143 + 30 + 100).
+// two of its CTAs share an SM at dk = 128 too (169 us with one each, 143 so).
+// One prompt of 16,384 tokens at 16 heads of 128 x 128: 783 us in one piece, 273
+// us so (143 + 30 + 100).
 #include "gated_delta_tc.cuh"
 
 namespace gla {
