@@ -55,23 +55,32 @@ gla_status gd_check(int N, int T, int Hk, int H, int dk, int dv, int64_t ld_qkv,
 }
 
 // Segments of long sequences: as many as fill the SMs once (two CTAs each in
-// the forward up to dk = 96, else one), of at least 8 chunks.  The passes over
-// the segments and their hand-over cost about what the sweeps themselves do, so
-// two would gain nothing (three did: both sides' times are with the sweeps).
-// The backward's have an even number of chunks: it keeps the state after every
-// second one.
+// the forward up to dk = 96, else one), where one CTA an SM leaves room for three
+// (a pass over them costs about what the sweep does, so two would gain nothing).
+// And no more than 2 sqrt(chunks) backward, sqrt(2 chunks) forward: the hand-over
+// takes some 2 us a segment, passes and sweeps 15 and 6.5 a chunk (4 heads of 96 x
+// 192, forward: 16,384 tokens in 37 segments 219 us, in 22 200; 4,096 tokens of 8
+// heads in 14 132 us, in 11 122).  One piece against segments: 768 tokens of 8 heads
+// of 96 x 192 backward 167 and 142 us, 1,024 tokens of 8 heads of 64 x 64 184 and
+// 124, forward 83 and 67; but 555 tokens of two sequences of 8 heads of 128 x 128
+// 168 and 181, and 4,096 tokens of two sequences of 16 heads of 96 x 192 forward 257
+// and 270.  The backward's have an even number of chunks: it keeps the state after
+// every second one.
 void gd_segments(GdParams& p, bool bwd)
 {
+    constexpr int64_t kSms = 148;
     const int64_t chunks = (static_cast<int64_t>(p.seqs.T) + kGdC - 1) / kGdC;
     const int64_t ctas = static_cast<int64_t>(p.seqs.N) * p.seqs.H * ((p.dv + 127) / 128);
-    int64_t n = ctas > 0 ? 148 * (p.dk <= 96 && !bwd ? 2 : 1) / ctas : 1;
-    if (n > chunks / 8) n = chunks / 8;
-    if (n < 3) n = 1;
-    p.seg_chunks = static_cast<int>((chunks + n - 1) / n);
-    if (bwd) p.seg_chunks += p.seg_chunks & 1;
-    if (p.seg_chunks < 1) p.seg_chunks = 1;
-    p.nseg = static_cast<int>((chunks + p.seg_chunks - 1) / p.seg_chunks);
-    if (p.nseg < 1) p.nseg = 1;
+    int64_t n = 1;
+    if (ctas > 0 && 3 * ctas <= kSms && chunks >= 12) {
+        n = kSms * (p.dk <= 96 && !bwd ? 2 : 1) / ctas;
+        while (n * n > (bwd ? 4 : 2) * chunks) --n;
+    }
+    int64_t c = (chunks + n - 1) / n;
+    if (bwd && n > 1) c += c & 1;
+    if (c < 1) c = 1;
+    p.seg_chunks = static_cast<int>(c);
+    p.nseg = static_cast<int>(chunks > c ? (chunks + c - 1) / c : 1);
 }
 
 // The workspace: parts one behind the other, 256-byte aligned.  With base

@@ -32,9 +32,9 @@
 // once, as in the forward: the states that enter them come from the same pass
 // (on this direction's records); the gradients of the states that leave them
 // from a reverse pass from zeros and a hand-over with A^T.  Whole backward of
-// 16,384 tokens, in one piece and so: 4 heads of 96 x 192 2,283 us, 504 us; 16
-// heads 2,561, 1,445; 48 heads of 128 x 128 (three segments) 4,030, 2,907; of
-// 2,048 tokens and 8 heads of 64 x 64 (four segments of 8 chunks) 317, 195.
+// 16,384 tokens, in one piece and so: 4 heads of 96 x 192 2,283 us, 460 us; 16
+// heads 2,561, 1,312; 48 heads of 128 x 128 (three segments) 4,030, 2,610; of
+// 1,024 tokens and 8 heads of 64 x 64 184, 124.
 #include "gated_delta_tc.cuh"
 
 namespace gla {

@@ -128,7 +128,8 @@ def test_more_chunks_than_fit_at_once():
 
 # few heads and long sequences: both directions cut them into segments
 LONG = [(1, 1600, 1, 1, 96, 192, None), (2, 2100, 1, 2, 128, 128, None), (1, 1537, 2, 2, 64, 256, None),
-        (1, 1793, 1, 1, 96, 160, None), (1, 0, 1, 2, 96, 192, [700, 0, 1200, 65]), (1, 0, 1, 1, 128, 32, [1, 1700])]
+        (1, 1793, 1, 1, 96, 160, None), (1, 0, 1, 2, 96, 192, [700, 0, 1200, 65]), (1, 0, 1, 1, 128, 32, [1, 1700]),
+        (1, 769, 2, 2, 96, 192, None), (1, 0, 1, 1, 64, 64, [770, 3, 129])]
 
 
 @pytest.mark.parametrize("N,T,Hk,H,dk,dv,lens", LONG)
