@@ -366,6 +366,34 @@ def test_other_stream_and_graph_replay():
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (96, 192)])
+def test_calls_that_overlap(dk, dv):
+    """Forward and backward on two streams at once, each with buffers of its own."""
+    d = make((2, 900), 4, 4, dk, dv, 77)
+    dO, s0, ds = make((2, 900), 4, 4, dk, dv, 78)["v"], states(2, 4, dk, dv, 79), states(2, 4, dk, dv, 80)
+
+    def fwd():
+        return gla.gated_delta_chunk_fwd(*args(d), s0=s0)
+
+    def bwd():
+        return gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds)
+
+    want = fwd() + tuple(bwd())
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(8):
+        with torch.cuda.stream(a):
+            x = fwd()
+        with torch.cuda.stream(b):
+            y = bwd()
+        got.append(x + tuple(y))
+    torch.cuda.synchronize()
+    for g in got:
+        for x, y in zip(g, want):
+            assert torch.equal(x, y)
+
+
 def test_gradients_against_differences():
     """Central differences of the loss along random directions, by the GPU's own
     forward: the loss in fp32 from S_T and the step's fp32 outputs (bf16 o would
