@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(NV)) group_norm_silu_bwd
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = c0 + j * cstep;
-            if (c >= p.d) continue;
+            // a row that is not there adds nothing (its x^ is NaN at eps = 0)
+            if (!on || c >= p.d) continue;
             f2 w[4], n[4], z[4], slope[4];
             Raw<float> t;
             t.a = *reinterpret_cast<const float4*>(params + c);
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(NV)) group_norm_silu_bwd
                 s1 = f2_add(s1, dn[j][e]);
                 s2 = f2_fma(dn[j][e], f[j][e], s2);
             }
-            if (GATE && on) store8(p.dgate + at + c, z);
+            if (GATE) store8(p.dgate + at + c, z);
         }
         const float2 t1 = f2_get(s1), t2 = f2_get(s2);
         const float m1 = p.center ? lanes_sum(t1.x + t1.y, lanes) * inv : 0.f;

@@ -125,3 +125,23 @@ def test_gradients_against_differences():
             side.append(float((norm(e[0], e[1], e[2], e[3], True, True, 1e-5) * dy.double()).sum()))
         diff, want = (side[0] - side[1]) / (2 * h), float((grad.double() * v).sum())
         assert abs(diff - want) <= 2 * U * float((grad.double() * v).norm()), (i, diff, want)
+
+
+@pytest.mark.parametrize("M,G,d", [(37, 16, 192), (1000, 16, 192), (7, 3, 40), (601, 1, 1024)])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("center", [False, True])
+def test_eps_of_zero(M, G, d, gate, center):
+    """Numbers of rows that the CTAs do not divide: the seats behind the last row
+    hold zeros, whose norm is undefined at eps = 0, and add nothing.  Tolerances as
+    above (every group's variance is some 0.09, far from zero)."""
+    x, w, b, z, dy = make(M, G, d, torch.bfloat16, gate, False, True, True, 11)
+    y = gla.group_norm_silu(x, w, b, z, center=center, eps=0.0)
+    got = gla.group_norm_silu_bwd(x, dy, w, b, z, center=center, eps=0.0)
+    leaves = [t.double().requires_grad_(True) if t is not None else None for t in (x, z, w, b)]
+    ref = norm(leaves[0], leaves[2], leaves[3], leaves[1], center, True, 0.0)
+    assert rel(y, ref) <= U
+    want = iter(torch.autograd.grad(ref, [t for t in leaves if t is not None], dy.double()))
+    for n, t, g in zip(("dx", "dgate", "dweight", "dbias"), leaves, got):
+        if t is not None:
+            r = next(want)
+            assert rel(g, r) <= (1e-5 if g.dtype == torch.float32 else U), (n, rel(g, r))
