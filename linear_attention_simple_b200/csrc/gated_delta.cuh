@@ -28,8 +28,15 @@ constexpr int kGdC = 64;                 // tokens per chunk
 constexpr int kGdPad = 8;                // bf16 elements behind each shared-memory row: rows an odd
                                          // multiple of 16 bytes apart, so ldmatrix has no bank conflicts
 constexpr int kGdPiece = 32 * 16;        // a piece: 16 values of each of 32 dv rows (32-byte swizzle)
-constexpr int kGdSc = 6;                 // per-token scalars of a chunk: G, R, beta, P_ii, b (high, low)
-enum { kScG = 0, kScR = 1, kScBeta = 2, kScPd = 3, kScBh = 4, kScBl = 5 };
+// Per-token scalars of a chunk: G, R, beta, P_ii, b (high, low).  The backward's
+// two more: beta~, which is beta but no nearer to zero than 2^-40, and beta / beta~.
+// dbeta is <dv, z> / beta, and dv = beta dV' would lose its bits (at beta = 0 all
+// of them): so T and the reverse sweep have beta~, which changes their sums by
+// 2^-40 of a term; V' has beta, and dv leaves with the factor.  (1e-30 in beta~'s
+// place left dbeta 14 bits at a dO of 2^-30 and none at 2^-60.)
+constexpr int gd_scalars(bool bwd) { return bwd ? 8 : 6; }
+enum { kScG = 0, kScR = 1, kScBeta = 2, kScPd = 3, kScBh = 4, kScBl = 5, kScBt = 6, kScF = 7 };
+constexpr float kGdBetaMin = 0x1p-40f;
 
 // Sequences of one call: dense [N][T] (cu null) or packed rows cu[n] .. cu[n+1]-1.
 struct GdSeqs {
@@ -68,7 +75,7 @@ template <int DK, bool BWD>
 struct GdRec {
     static constexpr int K = 0;
     static constexpr int SC = DK * 128;
-    static constexpr int KSC = SC + kGdSc * kGdC * 4;              // K and the scalars: one copy
+    static constexpr int KSC = SC + gd_scalars(BWD) * kGdC * 4;    // K and the scalars: one copy
     static constexpr int Q = (KSC + 1023) / 1024 * 1024;           // tiles start on their swizzle's period
     static constexpr int QL = Q + DK * 128;                        // BWD only
     static constexpr int T = BWD ? QL + DK * 128 : QL;

@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
     __nv_bfloat16* sq = sk + kGdC * KS;
     float* sl = reinterpret_cast<float*>(sq + kGdC * KS);          // L
     float* tt = reinterpret_cast<float*>(smem);                    // T, over K and Q once both are read
-    __shared__ float sc[kGdSc][kGdC];
+    constexpr int kSc = gd_scalars(BWD), kB = BWD ? kScBt : kScBeta;       // beta as T has it
+    __shared__ float sc[kSc][kGdC];
 
     const int64_t slot = blockIdx.x;
     const int h = blockIdx.y;
@@ -142,10 +143,12 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
                 av = av < -1e4f ? -1e4f : av;          // (a NaN stays one)
                 be = p.beta[at];
             }
-            // beta = 0 would leave dbeta = <dv, z> / beta undefined: a value too
-            // small to matter takes its place.
-            if (fabsf(be) < 1e-30f) be = 1e-30f;
             sc[kScBeta][i] = be;
+            if (BWD) {
+                const bool small = fabsf(be) < kGdBetaMin;
+                sc[kB][i] = small ? kGdBetaMin : be;
+                sc[kSc - 1][i] = small ? be * (1.f / kGdBetaMin) : 1.f;
+            }
             x[e] = static_cast<double>(av) * 1.4426950408889634074;
         }
         double s = x[0] + x[1];
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
                 const float bh = sc[kScBh][i], bl = sc[kScBl][i];
                 const float2 jh = *reinterpret_cast<const float2*>(&sc[kScBh][j0]);
                 const float2 jl = *reinterpret_cast<const float2*>(&sc[kScBl][j0]);
-                const float2 be = *reinterpret_cast<const float2*>(&sc[kScBeta][j0]);
+                const float2 be = *reinterpret_cast<const float2*>(&sc[kB][j0]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int j = j0 + e;
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
     }
     for (int i = tid; i < (BWD ? 1024 : 512); i += kThreads)
         reinterpret_cast<uint4*>(rec + Rec::P)[i] = reinterpret_cast<const uint4*>(sl)[i];
-    for (int i = tid; i < kGdSc * kGdC / 4; i += kThreads)
+    for (int i = tid; i < kSc * kGdC / 4; i += kThreads)
         reinterpret_cast<float4*>(rec + Rec::SC)[i] = reinterpret_cast<const float4*>(&sc[0][0])[i];
 }
 

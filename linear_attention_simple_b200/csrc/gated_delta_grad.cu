@@ -120,7 +120,7 @@ __device__ __forceinline__ void sums(const GdParams& p, const Unit& x, int h, in
 {
     const int H = p.seqs.H, wtot = p.dv >> 5;
     const int64_t u = x.slot * H + h;
-    const float* beta = reinterpret_cast<const float*>(p.rec + u * GdRec<DK, true>::BYTES + GdRec<DK, true>::SC) + kScBeta * kGdC;
+    const float* beta = reinterpret_cast<const float*>(p.rec + u * GdRec<DK, true>::BYTES + GdRec<DK, true>::SC) + kScBt * kGdC;
     // <E, S'> is there after every second chunk and the last; before the
     // others come the sums of the chunk in between
     const float* part = p.part + u * 3 * wtot * kGdC + 2 * lane;

@@ -10,7 +10,8 @@
 //   S  = G_63 S + (e^{b_63 - b} V') K
 // kept: S (bf16, and fp32 for the sums), y, V', and sum_dv o'.dO per token.
 //
-// Reverse, with E the gradient of the state that leaves the chunk:
+// Reverse, with E the gradient of the state that leaves the chunk (beta here and in
+// T: no nearer to zero than 2^-40; dv leaves with the factor that is missing):
 //   dVs' = R (E K^T) + dO P,   dV' = dVs' + P_ii dO
 //   dvs  = beta dVs' + (beta dV') T,   dv = dvs + beta P_ii dO
 //   E    = G_63 E + dO (scale G Q) - (G dv) K
@@ -649,7 +650,7 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             Cols16 d[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const Cols16 f = load16(sc + kScBeta * kGdC + 16 * b) * load16(sc + kScPd * kGdC + 16 * b);
+                const Cols16 f = load16(sc + kScBt * kGdC + 16 * b) * load16(sc + kScPd * kGdC + 16 * b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d[b].p[j] = f2_mul(f.p[j], f2_from_bf16x2(dw[b][j]));       // beta P_ii dO
             }
@@ -660,7 +661,7 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             for (int b = 0; b < 2; ++b) {
                 Cols16 f, q;
                 get16x2(f, q, t0 + C::Y + 16 * (s + b), t0 + C::PO + 16 * (s + b));
-                f = load16(sc + kScBeta * kGdC + 16 * b) * fma16(load16(sc + kScR * kGdC + 16 * b), f, q);
+                f = load16(sc + kScBt * kGdC + 16 * b) * fma16(load16(sc + kScR * kGdC + 16 * b), f, q);
                 put16(t0 + C::PO + 16 * (s + b), f);
                 put_terms<2>(t0 + C::Y + 16 * (s + b), f + d[b]);
             }
@@ -697,6 +698,13 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             }
             warp_done(&B.w, lane);
             const float gl = sc[kScG * kGdC + kGdC - 1 - 16 * s];
+            // what beta has that beta~ has not, on the rounded rows: nearly always 1, and as a
+            // factor of dv before its rounding it cost 2% of the backward
+            if (!PRE && __any_sync(0xFFFFFFFFu, sc[kScF * kGdC + lane] != 1.f)) {
+#pragma unroll 1
+                for (int t = 0; t < 32; ++t)
+                    vs[t * x.rows] = __float2bfloat16_rn(__bfloat162float(vs[t * x.rows]) * sc[kScF * kGdC + t]);
+            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {

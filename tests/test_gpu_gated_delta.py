@@ -483,3 +483,42 @@ def test_prefill_decode_and_norm_together():
         assert rel(y[b:e], ref[:e - b]) <= TOL_O + 2 * U
         assert rel(torch.stack([x[i] for x in ys]), ref[e - b:]) <= 2 * U
         assert rel(pool[idx[i].long()], rs[0]) <= TOL_S
+
+
+@pytest.mark.parametrize("size", [2.0 ** -30, 2.0 ** -60])
+@pytest.mark.parametrize("lens", [None, [130, 0, 1700]])
+def test_small_gradients_at_write_strengths_of_zero(size, lens):
+    """beta of zero and next to it, gradients as small as a mean over many tokens
+    makes them: dbeta is <dV' ..., z>, which does not get smaller with beta, and dv
+    is beta times that.  The tolerances are relative and do not change."""
+    cu = cu_of(lens) if lens else None
+    lead, N = ((sum(lens),), len(lens)) if lens else ((2, 140), 2)
+    d = make(lead, 1, 2, 96, 192, 81)
+    flat = d["beta"].view(-1, 2)
+    flat[3::5] = 0.0
+    flat[4::25] = 1e-35
+    flat[9::25] = 1e-20
+    flat[14::25] = 1e-11
+    flat[19::25] = -1e-20
+    dO, ds = make(lead, 1, 2, 96, 192, 82)["v"] * size, states(N, 2, 96, 192, 83) * size
+    got = check_bwd(d, states(N, 2, 96, 192, 84), dO, ds, cu)
+    ref = backward(d, states(N, 2, 96, 192, 84), dO, ds, 96 ** -0.5, cu)
+    (gv, gb), (rv, rb) = ((x[2].flatten(0, -3), x[4].flatten(0, -2)) for x in (got, ref))
+    assert bool((gv[3::5] == 0).all())
+    assert rel(gb[3::5], rb[3::5]) <= TOL_S
+    for first in (4, 9, 14, 19):
+        assert rel(gb[first::25], rb[first::25]) <= TOL_S
+        if float(rv[first::25].abs().mean()) > 2.0 ** -100:      # else its values are not normal numbers
+            assert rel(gv[first::25], rv[first::25]) <= TOL_V
+
+
+def test_write_strengths_of_zero_leave_a_state_of_zeros():
+    d = make((2, 100), 1, 2, 96, 192, 85)
+    d["beta"].zero_()
+    o, s = gla.gated_delta_chunk_fwd(*args(d))
+    assert bool((o == 0).all()) and bool((s == 0).all())
+    got = gla.gated_delta_chunk_bwd(*args(d), make((2, 100), 1, 2, 96, 192, 86)["v"])
+    for n, x in zip(("dq", "dk", "dv"), got):
+        assert bool((x == 0).all()), n
+    # beta stands at 2^-40 in da's sums of up to 128 x 192 terms of size 1, of either sign
+    assert float(got[3].abs().max()) <= 2.0 ** -40 * (128 * 192) ** 0.5 * 8
