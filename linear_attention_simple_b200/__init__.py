@@ -3,7 +3,10 @@
 Thin Python binding over the C ABI in ``include/gla.h``: the functions below
 have the same names as the exported C entry points and only marshal
 arguments (check dtypes/devices/strides, allocate outputs with PyTorch when
-the caller passes none, pass raw pointers and the current CUDA stream).
+the caller passes none, pass raw pointers and the current CUDA stream, or the
+one given as ``stream``: what is allocated for such a call belongs to that
+stream; tensors passed in are the caller's to order and to keep until it is
+done with them).
 Every step of the computation runs in the kernels of ``libgla.so``; there is
 no CPU or PyTorch fallback.  Importing this package does not load the
 library; the first call does, and raises ``GlaLibraryMissing`` when
@@ -667,9 +670,22 @@ def _fit(x, name, dtype, shape, device):
     raise ValueError("%s is on %s, expected %s" % (name, x.device, device))
 
 
-def _workspace(ws, need, device):
+def _empty(shape, dtype, device, stream, output=True):
+    """A new tensor for kernels on `stream` (None: the current one).  The caching
+    allocator reuses a block in the order of its own stream's work, so it has to be
+    that stream's; an output is the current stream's to read as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _workspace(ws, need, device, stream):
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return _empty(need, torch.uint8, device, stream, output=False)
     _fit(ws, "ws", torch.uint8, (ws.numel(),), device)
     return ws
 
@@ -761,10 +777,10 @@ def _sequences(fn, q, v, cu_seqlens):
     return lead, cu_seqlens.numel() - 1, lead[0]
 
 
-def _new(t, name, shape, dtype, like):
+def _new(t, name, shape, dtype, like, stream):
     """`t` checked against shape and type, or a new tensor on `like`'s device."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape, dtype=dtype) if stream is None else _empty(shape, dtype, like.device, stream)
     _fit(t, name, dtype, shape, like.device)
     return t
 
@@ -787,10 +803,10 @@ def gated_delta_chunk_fwd(q, k, v, a, beta, s0=None, cu_seqlens=None, o=None, s_
                                           (torch.bfloat16,))
     dev = q.device
     _fit(s0, "s0", torch.float32, (N, H, dk, dv), dev)
-    o = _new(o, "o", lead + (H, dv), torch.bfloat16, q)
+    o = _new(o, "o", lead + (H, dv), torch.bfloat16, q, stream)
     if s_final is not None or want_final_state:
-        s_final = _new(s_final, "s_final", (N, H, dk, dv), torch.float32, q)
-    ws = _workspace(ws, gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None), dev)
+        s_final = _new(s_final, "s_final", (N, H, dk, dv), torch.float32, q, stream)
+    ws = _workspace(ws, gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None), dev, stream)
     _call_on(dev, "gated_delta_chunk_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), beta.data_ptr(),
              _data(cu_seqlens), _data(s0), o.data_ptr(), _data(s_final), ws.data_ptr(), ws.numel(), N, T, Hk, H, dk, dv,
              ld, dk ** -0.5 if scale is None else scale, GLA_BF16, stream=stream)
@@ -811,14 +827,14 @@ def gated_delta_chunk_bwd(q, k, v, a, beta, dO, s0=None, ds_final=None, cu_seqle
     _fit(ds_final, "ds_final", f32, (N, H, dk, dv), dev)
     _fit(dO, "dO", bf16, lead + (H, dv), dev)
     gq, gk, gv, ga, gb, gs = grads if grads is not None else (None,) * 6
-    gq = _new(gq, "grad_q", lead + (Hk, dk), bf16, q)
-    gk = _new(gk, "grad_k", lead + (Hk, dk), bf16, q)
-    gv = _new(gv, "grad_v", lead + (H, dv), bf16, q)
-    ga = _new(ga, "grad_a", lead + (H,), f32, q)
-    gb = _new(gb, "grad_beta", lead + (H,), f32, q)
+    gq = _new(gq, "grad_q", lead + (Hk, dk), bf16, q, stream)
+    gk = _new(gk, "grad_k", lead + (Hk, dk), bf16, q, stream)
+    gv = _new(gv, "grad_v", lead + (H, dv), bf16, q, stream)
+    ga = _new(ga, "grad_a", lead + (H,), f32, q, stream)
+    gb = _new(gb, "grad_beta", lead + (H,), f32, q, stream)
     if gs is not None or (want_grad_s0 and grads is None):
-        gs = _new(gs, "grad_s0", (N, H, dk, dv), f32, q)
-    ws = _workspace(ws, gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None, True), dev)
+        gs = _new(gs, "grad_s0", (N, H, dk, dv), f32, q, stream)
+    ws = _workspace(ws, gated_delta_chunk_workspace_bytes(N, T, H, dk, dv, cu_seqlens is not None, True), dev, stream)
     _call_on(dev, "gated_delta_chunk_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), beta.data_ptr(),
              _data(cu_seqlens), _data(s0), dO.data_ptr(), _data(ds_final), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
              ga.data_ptr(), gb.data_ptr(), _data(gs), ws.data_ptr(), ws.numel(), N, T, Hk, H, dk, dv, ld,
@@ -844,7 +860,7 @@ def gated_delta_decode_step(state, q, k, v, a, beta, o=None, slot_idx=None, scal
     _fit(slot_idx, "slot_idx", torch.int32, (N,), dev)
     if slot_idx is None and state.shape[0] != N:
         raise ValueError("without slot_idx the state must have N slots")
-    o = _new(o, "o", lead + (H, dv), torch.float32, q)
+    o = _new(o, "o", lead + (H, dv), torch.float32, q, stream)
     _call_on(dev, "gated_delta_decode_step", state.data_ptr(), _data(slot_idx), state.shape[0], q.data_ptr(),
              k.data_ptr(), v.data_ptr(), a.data_ptr(), beta.data_ptr(), o.data_ptr(), N, T, Hk, H, dk, dv, ld,
              dk ** -0.5 if scale is None else scale, _dt(q), stream=stream)
@@ -889,7 +905,7 @@ def group_norm_silu(x, weight=None, bias=None, gate=None, center=True, act=True,
     n * silu(gate), or silu(n) without a gate (act=False: the identity in
     silu's place), bf16 in x's shape."""
     M, G, d, ldx, ldg, shared = _norm_args(x, weight, bias, gate)
-    y = _new(y, "y", x.shape, torch.bfloat16, x)
+    y = _new(y, "y", x.shape, torch.bfloat16, x, stream)
     _call_on(x.device, "group_norm_silu", x.data_ptr(), _data(gate), _data(weight), _data(bias), y.data_ptr(), M, G, d,
              ldx, ldg, shared, int(center), int(act), eps, _dt(x), stream=stream)
     return y
@@ -908,12 +924,12 @@ def group_norm_silu_bwd(x, dy, weight=None, bias=None, gate=None, center=True, a
     dev, f32 = x.device, torch.float32
     _fit(dy, "dy", torch.bfloat16, x.shape, dev)
     gx, gg, gw, gb = grads if grads is not None else (None,) * 4
-    gx = _new(gx, "grad_x", x.shape, x.dtype, x)
-    gg = _new(gg, "grad_gate", x.shape, torch.bfloat16, x) if gate is not None else None
-    gw = _new(gw, "grad_weight", weight.shape, f32, x) if weight is not None else None
-    gb = _new(gb, "grad_bias", bias.shape, f32, x) if bias is not None else None
+    gx = _new(gx, "grad_x", x.shape, x.dtype, x, stream)
+    gg = _new(gg, "grad_gate", x.shape, torch.bfloat16, x, stream) if gate is not None else None
+    gw = _new(gw, "grad_weight", weight.shape, f32, x, stream) if weight is not None else None
+    gb = _new(gb, "grad_bias", bias.shape, f32, x, stream) if bias is not None else None
     if ws is not None or gw is not None or gb is not None:
-        ws = _workspace(ws, group_norm_silu_bwd_workspace_bytes(M, G, d), dev)
+        ws = _workspace(ws, group_norm_silu_bwd_workspace_bytes(M, G, d), dev, stream)
     _call_on(dev, "group_norm_silu_bwd", x.data_ptr(), _data(gate), _data(weight), _data(bias), dy.data_ptr(),
              gx.data_ptr(), _data(gg), _data(gw), _data(gb), _data(ws), 0 if ws is None else ws.numel(), M, G, d, ldx, ldg,
              shared, int(center), int(act), eps, _dt(x), stream=stream)
