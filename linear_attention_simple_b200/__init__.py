@@ -230,6 +230,19 @@ def _need(x, name, dtype, shape=None, contiguous=True):
         raise ValueError("%s must be contiguous" % name)
 
 
+def _empty(shape, dtype, device, stream, output=True):
+    """A new tensor for kernels on `stream` (None: the current one).  The caching
+    allocator reuses a block in the order of its own stream's work, so it has to be
+    that stream's; an output is the current stream's to read as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def gla_status_string(status):
     return lib().gla_status_string(int(status)).decode()
 
@@ -284,14 +297,14 @@ def gla_chunk_fwd(q, k, v, a, s0=None, o=None, s_final=None, ws=None, scale=None
     _need(a, "a", torch.float32, (B, T, H))
     _need(s0, "s0", torch.float32, (B, H, dk, dv))
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((B, T, H, dv), q.dtype, q.device, stream)
     _need(o, "o", q.dtype, (B, T, H, dv))
     if s_final is None and want_final_state:
-        s_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        s_final = _empty((B, H, dk, dv), torch.float32, q.device, stream)
     _need(s_final, "s_final", torch.float32, (B, H, dk, dv))
     need = gla_chunk_workspace_bytes(B, T, H, dk, dv, False) if dt == GLA_BF16 else 0
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _empty(need, torch.uint8, q.device, stream, output=False)
     if scale is None:
         scale = dk ** -0.5
     st = lib().gla_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(s0), _ptr(o),
@@ -314,11 +327,11 @@ def gla_chunk_bwd(q, k, v, a, dO, s0=None, ds_final=None, grads=None, ws=None, s
     _need(ds_final, "ds_final", torch.float32, (B, H, dk, dv))
     dev = q.device
     if grads is None:
-        grads = (torch.empty((B, T, H, dk), dtype=q.dtype, device=dev),
-                 torch.empty((B, T, H, dk), dtype=q.dtype, device=dev),
-                 torch.empty((B, T, H, dv), dtype=q.dtype, device=dev),
-                 torch.empty((B, T, H), dtype=torch.float32, device=dev),
-                 torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        grads = (_empty((B, T, H, dk), q.dtype, dev, stream),
+                 _empty((B, T, H, dk), q.dtype, dev, stream),
+                 _empty((B, T, H, dv), q.dtype, dev, stream),
+                 _empty((B, T, H), torch.float32, dev, stream),
+                 _empty((B, H, dk, dv), torch.float32, dev, stream)
                  if want_grad_s0 else None)
     gq, gk, gv, ga, gs0 = grads
     _need(gq, "grad_q", q.dtype, (B, T, H, dk))
@@ -328,7 +341,7 @@ def gla_chunk_bwd(q, k, v, a, dO, s0=None, ds_final=None, grads=None, ws=None, s
     _need(gs0, "grad_s0", torch.float32, (B, H, dk, dv))
     need = gla_chunk_workspace_bytes(B, T, H, dk, dv, True)
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = _empty(need, torch.uint8, dev, stream, output=False)
     if scale is None:
         scale = dk ** -0.5
     st = lib().gla_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(s0), _ptr(dO),
@@ -352,18 +365,18 @@ def gla_chunk_fwd_train(q, k, v, a, s0=None, o=None, s_final=None, saved=None, w
     _need(a, "a", torch.float32, (B, T, H))
     _need(s0, "s0", torch.float32, (B, H, dk, dv))
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((B, T, H, dv), q.dtype, q.device, stream)
     _need(o, "o", q.dtype, (B, T, H, dv))
     if s_final is None:
-        s_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        s_final = _empty((B, H, dk, dv), torch.float32, q.device, stream)
     _need(s_final, "s_final", torch.float32, (B, H, dk, dv))
     nsv = gla_chunk_saved_state_bytes(B, T, H, dk, dv)
     if saved is None:
-        saved = torch.empty(max(nsv, 16), dtype=torch.uint8, device=q.device)
+        saved = _empty(max(nsv, 16), torch.uint8, q.device, stream)
     _need(saved, "saved", torch.uint8)
     need = gla_chunk_workspace_bytes(B, T, H, dk, dv)
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _empty(need, torch.uint8, q.device, stream, output=False)
     sc = dk ** -0.5 if scale is None else scale
     st = lib().gla_chunk_fwd_train(_ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(s0), _ptr(o), _ptr(s_final),
                                    _ptr(saved), saved.numel(), _ptr(ws), 0 if ws is None else ws.numel(),
@@ -388,11 +401,11 @@ def gla_chunk_bwd_saved(q, k, v, a, saved, dO, s_final=None, ds_final=None, grad
     _need(ds_final, "ds_final", torch.float32, (B, H, dk, dv))
     dev = q.device
     if grads is None:
-        grads = (torch.empty((B, T, H, dk), dtype=q.dtype, device=dev),
-                 torch.empty((B, T, H, dk), dtype=q.dtype, device=dev),
-                 torch.empty((B, T, H, dv), dtype=q.dtype, device=dev),
-                 torch.empty((B, T, H), dtype=torch.float32, device=dev),
-                 torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if want_grad_s0 else None)
+        grads = (_empty((B, T, H, dk), q.dtype, dev, stream),
+                 _empty((B, T, H, dk), q.dtype, dev, stream),
+                 _empty((B, T, H, dv), q.dtype, dev, stream),
+                 _empty((B, T, H), torch.float32, dev, stream),
+                 _empty((B, H, dk, dv), torch.float32, dev, stream) if want_grad_s0 else None)
     gq, gk, gv, ga, gs0 = grads
     _need(gq, "grad_q", q.dtype, (B, T, H, dk))
     _need(gk, "grad_k", q.dtype, (B, T, H, dk))
@@ -401,7 +414,7 @@ def gla_chunk_bwd_saved(q, k, v, a, saved, dO, s_final=None, ds_final=None, grad
     _need(gs0, "grad_s0", torch.float32, (B, H, dk, dv))
     need = gla_chunk_workspace_bytes(B, T, H, dk, dv, for_bwd=True, from_saved=True)
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = _empty(need, torch.uint8, dev, stream, output=False)
     sc = dk ** -0.5 if scale is None else scale
     st = lib().gla_chunk_bwd_saved(_ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(saved), saved.numel(), _ptr(s_final),
                                    _ptr(dO), _ptr(ds_final), _ptr(gq), _ptr(gk), _ptr(gv), _ptr(ga), _ptr(gs0),
@@ -428,7 +441,7 @@ def gla_decode_step(state, q, k, v, a, o=None, slot_idx=None, scale=None, stream
     if slot_idx is None and state.shape[0] != N:
         raise ValueError("without slot_idx the state must have N slots")
     if o is None:
-        o = torch.empty((N, H, dv), dtype=torch.float32, device=q.device)
+        o = _empty((N, H, dv), torch.float32, q.device, stream)
     _need(o, "o", torch.float32, (N, H, dv))
     if scale is None:
         scale = dk ** -0.5
@@ -453,7 +466,7 @@ def conv1d_silu_causal(x, w, apply_ln=True, ln_gamma=None, ln_beta=None, ln_eps=
     _need(conv_state_in, "conv_state_in", torch.float32, (B, W - 1, D))
     _need(conv_state_out, "conv_state_out", torch.float32, (B, W - 1, D))
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     _need(y, "y", torch.bfloat16, (B, T, D))
     st = lib().conv1d_silu_causal(_ptr(x), 1 if apply_ln else 0, _ptr(ln_gamma), _ptr(ln_beta),
                                   float(ln_eps), _ptr(w), _ptr(bias), _ptr(conv_state_in),
@@ -485,16 +498,16 @@ def gla_chunk_fwd_varlen(q, k, v, a, cu_seqlens, s0=None, o=None, s_final=None, 
     _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,))
     _need(s0, "s0", torch.float32, (N, H, dk, dv))
     if o is None:
-        o = torch.empty((total, H, dv), dtype=torch.bfloat16, device=q.device)
+        o = _empty((total, H, dv), torch.bfloat16, q.device, stream)
     _need(o, "o", torch.bfloat16, (total, H, dv))
     if s_final is None and want_final_state:
-        s_final = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+        s_final = _empty((N, H, dk, dv), torch.float32, q.device, stream)
     _need(s_final, "s_final", torch.float32, (N, H, dk, dv))
     sc = dk ** -0.5 if scale is None else scale
     if ws is None and segmented:
         need = gla_chunk_varlen_workspace_bytes(N, total, H, dk, dv)
         if need > 0:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = _empty(need, torch.uint8, q.device, stream, output=False)
     st = lib().gla_chunk_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(cu_seqlens), N, _ptr(s0), _ptr(o),
                                     _ptr(s_final), _ptr(ws), 0 if ws is None else ws.numel(), total, H, dk, dv,
                                     0, float(sc), GLA_BF16, _stream(stream))
@@ -506,20 +519,20 @@ def gla_segment_workspace_bytes(B, T, H, dk=96, dv=192):
     return int(lib().gla_segment_workspace_bytes(B, T, H, dk, dv))
 
 
-def _segment_outputs(B, H, dk, dv, dev, s_seg, g_seg, want_g):
+def _segment_outputs(B, H, dk, dv, dev, s_seg, g_seg, want_g, stream):
     if s_seg is None:
-        s_seg = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        s_seg = _empty((B, H, dk, dv), torch.float32, dev, stream)
     _need(s_seg, "s_seg", torch.float32, (B, H, dk, dv))
     if g_seg is None and want_g:
-        g_seg = torch.empty((B, H), dtype=torch.float32, device=dev)
+        g_seg = _empty((B, H), torch.float32, dev, stream)
     _need(g_seg, "g_seg", torch.float32, (B, H))
     return s_seg, g_seg
 
 
-def _segment_ws(ws, B, T, H, dk, dv, dev):
+def _segment_ws(ws, B, T, H, dk, dv, dev, stream):
     need = gla_segment_workspace_bytes(B, T, H, dk, dv)
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = _empty(need, torch.uint8, dev, stream, output=False)
     return ws
 
 
@@ -540,8 +553,8 @@ def gla_segment_state_fwd(k, v, a, s_seg=None, g_seg=None, ws=None, want_decay=T
     else:
         raise ValueError("k and v must share one token stride when not packed (got %d, %d)" % (lk, lv))
     _need(a, "a", torch.float32, (B, T, H))
-    s_seg, g_seg = _segment_outputs(B, H, dk, dv, k.device, s_seg, g_seg, want_decay)
-    ws = _segment_ws(ws, B, T, H, dk, dv, k.device)
+    s_seg, g_seg = _segment_outputs(B, H, dk, dv, k.device, s_seg, g_seg, want_decay, stream)
+    ws = _segment_ws(ws, B, T, H, dk, dv, k.device, stream)
     st = lib().gla_segment_state_fwd(_ptr(k), _ptr(v), _ptr(a), _ptr(s_seg), _ptr(g_seg), _ptr(ws),
                                      0 if ws is None else ws.numel(), B, T, H, dk, dv, ld, GLA_BF16,
                                      _stream(stream))
@@ -564,8 +577,8 @@ def gla_segment_state_bwd(q, dO, a, ds_seg=None, g_seg=None, ws=None, scale=None
         raise ValueError("an unpacked q needs a token stride >= H*dv (got %d)" % lq)
     _need(dO, "dO", torch.bfloat16, (B, T, H, dv))
     _need(a, "a", torch.float32, (B, T, H))
-    ds_seg, g_seg = _segment_outputs(B, H, dk, dv, q.device, ds_seg, g_seg, want_decay)
-    ws = _segment_ws(ws, B, T, H, dk, dv, q.device)
+    ds_seg, g_seg = _segment_outputs(B, H, dk, dv, q.device, ds_seg, g_seg, want_decay, stream)
+    ws = _segment_ws(ws, B, T, H, dk, dv, q.device, stream)
     sc = dk ** -0.5 if scale is None else scale
     st = lib().gla_segment_state_bwd(_ptr(q), _ptr(dO), _ptr(a), _ptr(ds_seg), _ptr(g_seg), _ptr(ws),
                                      0 if ws is None else ws.numel(), B, T, H, dk, dv,
@@ -588,7 +601,7 @@ def gla_state_fold(s, g, reverse=False, s_in=None, out=None, stream=None):
     _need(g, "g", torch.float32, (n,) + unit_shape)
     _need(s_in, "s_in", torch.float32, unit_shape + (dk, dv))
     if out is None:
-        out = torch.empty(unit_shape + (dk, dv), dtype=torch.float32, device=s.device)
+        out = _empty(unit_shape + (dk, dv), torch.float32, s.device, stream)
     _need(out, "out", torch.float32, unit_shape + (dk, dv))
     st = lib().gla_state_fold(_ptr(s), _ptr(g), n, 1 if reverse else 0, _ptr(s_in), _ptr(out), units, dk, dv,
                               _stream(stream))
@@ -616,13 +629,13 @@ def conv1d_silu_causal_bwd(x, w, dy, apply_ln=True, ln_gamma=None, ln_beta=None,
     _need(bias, "bias", torch.float32, (D,))
     _need(conv_state_in, "conv_state_in", torch.float32, (B, W - 1, D))
     dev = x.device
-    out = {"dx": torch.empty_like(x), "dw": torch.empty((D, W), dtype=torch.float32, device=dev)}
+    out = {"dx": _empty(x.shape, x.dtype, x.device, stream), "dw": _empty((D, W), torch.float32, dev, stream)}
     for name, shape in (("dbias", (D,)), ("dln_gamma", (D,)), ("dln_beta", (D,)),
                         ("dconv_state_in", (B, W - 1, D))):
-        out[name] = torch.empty(shape, dtype=torch.float32, device=dev) if name in want else None
+        out[name] = _empty(shape, torch.float32, dev, stream) if name in want else None
     need = conv1d_silu_causal_bwd_workspace_bytes(B, T, D, W)
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        ws = _empty(max(need, 16), torch.uint8, dev, stream, output=False)
     st = lib().conv1d_silu_causal_bwd(_ptr(x), 1 if apply_ln else 0, _ptr(ln_gamma), _ptr(ln_beta), float(ln_eps),
                                       _ptr(w), _ptr(bias), _ptr(conv_state_in), _ptr(dy), _ptr(out["dx"]),
                                       _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dln_gamma"]),
@@ -651,7 +664,7 @@ def conv1d_silu_decode_step(x, w, conv_state, slot_idx=None, apply_ln=True, ln_g
     elif n_slots != N:
         raise ValueError("conv_state has %d slots for %d sequences and no slot_idx" % (n_slots, N))
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     _need(y, "y", torch.bfloat16, (N, D))
     st = lib().conv1d_silu_decode_step(_ptr(x), _ptr(slot_idx), n_slots, 1 if apply_ln else 0, _ptr(ln_gamma),
                                        _ptr(ln_beta), float(ln_eps), _ptr(w), _ptr(bias), _ptr(conv_state),
@@ -668,19 +681,6 @@ def _fit(x, name, dtype, shape, device):
         return
     _need(x, name, dtype, shape)
     raise ValueError("%s is on %s, expected %s" % (name, x.device, device))
-
-
-def _empty(shape, dtype, device, stream, output=True):
-    """A new tensor for kernels on `stream` (None: the current one).  The caching
-    allocator reuses a block in the order of its own stream's work, so it has to be
-    that stream's; an output is the current stream's to read as well."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if output:
-        t.record_stream(torch.cuda.current_stream(t.device))
-    return t
 
 
 def _workspace(ws, need, device, stream):
@@ -980,10 +980,10 @@ def gla_chunk_fwd_noalloc(q, k, v, a, s0=None, o=None, s_final=None, scale=None,
     _need(a, "a", torch.float32, (B, T, H))
     _need(s0, "s0", torch.float32, (B, H, dk, dv))
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((B, T, H, dv), q.dtype, q.device, stream)
     _need(o, "o", q.dtype, (B, T, H, dv))
     if s_final is None and want_final_state:
-        s_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        s_final = _empty((B, H, dk, dv), torch.float32, q.device, stream)
     _need(s_final, "s_final", torch.float32, (B, H, dk, dv))
     if scale is None:
         scale = dk ** -0.5

@@ -115,3 +115,54 @@ def test_an_output_dropped_here_is_not_reused_there(name):
         over = [torch.full(s, 3, dtype=t, device="cuda") for s, t in shapes]
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(copies, want)) and len(over) == len(want)
+
+
+# ---------------------------------------------------------------- the other entry points
+def mixer_calls():
+    B, T, H, D = 8, 1024, 16, 1024
+    d = dict(q=rnd(B, T, H, 96, seed=21), k=rnd(B, T, H, 96, seed=22), v=rnd(B, T, H, 192, seed=23),
+             a=torch.nn.functional.logsigmoid(rnd(B, T, H, seed=24, dtype=torch.float32) + 3))
+    dO, s0 = rnd(B, T, H, 192, seed=25), rnd(B, H, 96, 192, seed=26, dtype=torch.float32, std=0.1)
+    saved = gla.gla_chunk_fwd_train(**d)[2]
+    flat = {n: t.flatten(0, 1) for n, t in d.items()}
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * T
+    one, pools = {n: t[:, 0].contiguous() for n, t in d.items()}, [s0.clone() for _ in range(8)]
+    g = -rnd(B, H, seed=27, dtype=torch.float32).abs()
+    x, dy, w = rnd(4, 2048, D, seed=28), rnd(4, 2048, D, seed=29), rnd(D, 4, seed=30, dtype=torch.float32, std=0.5)
+    histories, x1 = [rnd(64, 3, D, seed=31, dtype=torch.float32) for _ in range(8)], rnd(64, D, seed=32)
+    return {
+        "gla_chunk_fwd": lambda **kw: gla.gla_chunk_fwd(**d, s0=s0, **kw),
+        "gla_chunk_fwd_noalloc": lambda **kw: gla.gla_chunk_fwd_noalloc(**{n: t[:1, :128] for n, t in d.items()}, **kw),
+        "gla_chunk_fwd_varlen": lambda **kw: gla.gla_chunk_fwd_varlen(**flat, cu_seqlens=cu, **kw),
+        "gla_chunk_fwd_train": lambda **kw: gla.gla_chunk_fwd_train(**d, s0=s0, **kw)[:2],
+        "gla_chunk_bwd": lambda **kw: gla.gla_chunk_bwd(**d, dO=dO, s0=s0, **kw),
+        "gla_chunk_bwd_saved": lambda **kw: gla.gla_chunk_bwd_saved(**d, saved=saved, dO=dO, **kw),
+        "gla_decode_step": lambda **kw: (gla.gla_decode_step(pools.pop(), **one, **kw),),
+        "gla_segment_state_fwd": lambda **kw: gla.gla_segment_state_fwd(d["k"], d["v"], d["a"], **kw),
+        "gla_segment_state_bwd": lambda **kw: gla.gla_segment_state_bwd(d["q"], dO, d["a"], want_decay=True, **kw),
+        "gla_state_fold": lambda **kw: (gla.gla_state_fold(s0, g, **kw),),
+        "conv1d_silu_causal": lambda **kw: (gla.conv1d_silu_causal(x, w, **kw),),
+        "conv1d_silu_causal_bwd": lambda **kw: tuple(gla.conv1d_silu_causal_bwd(x, w, dy, **kw).values()),
+        "conv1d_silu_decode_step": lambda **kw: (gla.conv1d_silu_decode_step(x1, w, histories.pop(), **kw),),
+    }
+
+
+MIXER = ["gla_chunk_fwd", "gla_chunk_fwd_noalloc", "gla_chunk_fwd_varlen", "gla_chunk_fwd_train", "gla_chunk_bwd",
+         "gla_chunk_bwd_saved", "gla_decode_step", "gla_segment_state_fwd", "gla_segment_state_bwd", "gla_state_fold",
+         "conv1d_silu_causal", "conv1d_silu_causal_bwd", "conv1d_silu_decode_step"]
+
+
+@pytest.mark.parametrize("name", MIXER)
+def test_outputs_of_the_mixer_and_its_front_end(name):
+    check_outputs(mixer_calls()[name])
+
+
+@pytest.mark.parametrize("name", ["gla_chunk_bwd", "gla_chunk_bwd_saved", "gla_segment_state_fwd",
+                                  "gla_segment_state_bwd", "conv1d_silu_causal_bwd"])
+def test_workspaces_of_the_mixer_and_its_front_end(name):
+    need = {"gla_chunk_bwd": lambda: gla.gla_chunk_workspace_bytes(8, 1024, 16, for_bwd=True),
+            "gla_chunk_bwd_saved": lambda: gla.gla_chunk_workspace_bytes(8, 1024, 16, for_bwd=True, from_saved=True),
+            "conv1d_silu_causal_bwd": lambda: gla.conv1d_silu_causal_bwd_workspace_bytes(4, 2048, 1024),
+            }.get(name, lambda: gla.gla_segment_workspace_bytes(8, 1024, 16))()
+    assert need > 0
+    check_workspace(mixer_calls()[name], need)
