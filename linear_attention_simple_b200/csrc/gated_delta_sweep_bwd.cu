@@ -655,7 +655,10 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 for (int j = 0; j < 8; ++j) d[b].p[j] = f2_mul(f.p[j], f2_from_bf16x2(dw[b][j]));       // beta P_ii dO
             }
             ok = warp_wait(&B.y, ph, ctl);
-            if (!ok) break;
+            if (!ok) {                       // no copy may be in flight when the block ends
+                if (!PRE) warp_wait(&B.yin[warp], i & 1, ctl);
+                break;
+            }
             tc_fence_after();
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -668,7 +671,10 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             warp_done(&B.r, lane);
             if (i + 1 < x.nc) {
                 ok = warp_wait(&B.full[ph ^ 1], ((i + 1) >> 1) & 1, ctl);
-                if (!ok) break;
+                if (!ok) {
+                    if (!PRE) warp_wait(&B.yin[warp], i & 1, ctl);
+                    break;
+                }
                 put_dO(i + 1);
             }
             ok = (PRE || warp_wait(&B.yin[warp], i & 1, ctl)) && warp_wait(&B.z, ph, ctl);

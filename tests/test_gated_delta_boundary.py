@@ -146,3 +146,22 @@ def test_row_strides_of_views():
                 b[..., :24].unflatten(-1, (8, 3)).transpose(-1, -2), b[:1, :1].expand(2, 5, 40).unflatten(-1, (5, 8))):
         with pytest.raises(ValueError):
             f(bad)
+
+
+@pytest.mark.parametrize("name", ["gated_delta_sweep_fwd.cu", "gated_delta_sweep_bwd.cu", "gated_delta_grad.cu"])
+def test_every_load_is_waited_for_before_its_block_ends(name):
+    """A wait that runs out ends a kernel's work early.  What no input brings about is
+    read from the source: each barrier that asynchronous loads complete on has a wait
+    in the lines behind a note that no copy may be in flight when the block ends."""
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(gla.__file__), "csrc", name)) as f:
+        text = f.read()
+    loads = set(re.findall(r"(?:bulk_load|tma_load_2d)\([^;]*?&B\.(\w+)", text)) | set(re.findall(r"= tile\(\w+, &B\.(\w+)", text))
+    drained = set()
+    for part in text.split("no copy may be in flight when the block ends")[1:]:
+        drained |= set(re.findall(r"(?:mbar|warp)_wait\(&B\.(\w+)", "\n".join(part.split("\n")[:8])))
+    if "kq" in loads:                                  # behind what is on its way out of the same place
+        assert re.search(r"tma_store_wait_read\(\);\s*if \(step > 0\) mbar_wait\(&B\.kq,", text)
+        drained.add("kq")
+    assert len(loads) >= 3 and loads <= drained, loads - drained
