@@ -72,7 +72,11 @@ unsigned long long gla_launch_count(void);
  * with -DGLA_DEBUG_BOUNDS).  It has the same ABI and results as the normal
  * build and additionally, without ever trapping:
  *   - scans the inputs of every chunk, segment and decode call before its
- *     kernels run: a_t <= 0 and finite, q/k/v/dO and fp32 states finite;
+ *     kernels run: a_t <= 0 and finite, q/k/v/dO and fp32 states finite (and
+ *     beta; of packed tokens the sequences' own, of a pool the states that the
+ *     call addresses).  Not scanned: gla_chunk_fwd with GLA_F32, s0 of
+ *     gla_chunk_fwd_varlen, the pool of gla_decode_step, the convolution and
+ *     the group norm;
  *   - checks the index of each direct global store in its kernels against
  *     the tensor it writes, and skips a store that would fall outside (the
  *     gated delta rule: its gradients' kernel only, the others write whole

@@ -135,23 +135,35 @@ GdParams gd_params(const void* q, const void* k, const void* v, const float* a, 
     return p;
 }
 
-// The checking build's scan of the inputs (nothing in the normal build).
-gla_status gd_scan(const GdParams& p, cudaStream_t st)
+// The checking build's scan of the inputs (nothing in the normal build).  f32: the
+// type of q, k and v; pool: the step's states.
+gla_status gd_scan(const GdParams& p, cudaStream_t st, bool f32 = false, const float* pool = nullptr,
+                   const int32_t* slot_idx = nullptr, int n_slots = 0)
 {
     DebugScan d;
     const int64_t rows = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;
     const int64_t wq = static_cast<int64_t>(p.seqs.Hk) * p.dk, wv = static_cast<int64_t>(p.seqs.H) * p.dv;
+    d.cu = p.seqs.cu;
+    d.n_seq = p.seqs.N;
+    d.heads = p.seqs.H;
     d.a = p.a;
     d.na = rows * p.seqs.H;
-    d.bf16[0] = {p.q, rows, p.ld_qk, wq};
-    d.bf16[1] = {p.k, rows, p.ld_qk, wq};
-    d.bf16[2] = {p.v, rows, p.ld_v, wv};
+    DebugScan::Rows* qkv = f32 ? d.tokens_f32 + 1 : d.bf16;
+    qkv[0] = {p.q, rows, p.ld_qk, wq};
+    qkv[1] = {p.k, rows, p.ld_qk, wq};
+    qkv[2] = {p.v, rows, p.ld_v, wv};
     d.bf16[3] = {p.dO, rows, p.ld_do, wv};
-    const int64_t ns = static_cast<int64_t>(p.seqs.N) * p.seqs.H * p.dk * p.dv;
+    d.tokens_f32[0] = {p.beta, rows, p.seqs.H, p.seqs.H};
+    const int64_t per = static_cast<int64_t>(p.seqs.H) * p.dk * p.dv, ns = p.seqs.N * per;
     d.f32[0] = p.s0;
     d.nf32[0] = p.s0 ? ns : 0;
-    d.f32[1] = p.beta;
-    d.nf32[1] = rows * p.seqs.H;
+    d.f32[1] = p.ds_final;
+    d.nf32[1] = p.ds_final ? ns : 0;
+    d.pool = pool;
+    d.slot_idx = slot_idx;
+    d.n = p.seqs.N;
+    d.n_slots = n_slots;
+    d.per_slot = per;
     return debug_scan(d, p.status, st);
 }
 
@@ -283,11 +295,9 @@ gla_status gated_delta_decode_step(float* state, const int32_t* slot_idx, int n_
         return GLA_ERR_MISALIGNED;
     const WaitCtl ctl = wait_ctl_for_current_device(&s);
     if (s != GLA_OK) return s;
-    if (!f32) {
-        GdParams p = gd_params(q, k, v, a, beta, nullptr, nullptr, N, T, Hk, H, dk, dv, ld_qk, ld_v, scale);
-        p.status = ctl.status;
-        if ((s = gd_scan(p, stream)) != GLA_OK) return s;
-    }
+    GdParams p = gd_params(q, k, v, a, beta, nullptr, nullptr, N, T, Hk, H, dk, dv, ld_qk, ld_v, scale);
+    p.status = ctl.status;
+    if ((s = gd_scan(p, stream, f32, state, slot_idx, n_slots)) != GLA_OK) return s;
     return gd_launch_step(state, slot_idx, n_slots, q, k, v, a, beta, o, N, T, Hk, H, dk, dv, ld_qk, ld_v, scale, f32,
                           ctl.status, stream);
 }

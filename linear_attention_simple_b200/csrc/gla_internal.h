@@ -100,17 +100,27 @@ gla_status run_chunk_bwd(const ChunkProblem& p, const float* s0, const void* dO,
 gla_status launch_wait_selftest(const WaitCtl& ctl, cudaStream_t st);
 
 // Inputs of one call for the checking build's precondition scan
-// (debug_checks.cu): the decay a (<= 0 and finite), bf16 token tensors and
-// fp32 states (finite).  debug_scan launches nothing in the normal build.
+// (debug_checks.cu): the decay a (<= 0 and finite), token tensors and fp32
+// states (finite).  debug_scan launches nothing in the normal build.
 struct DebugScan {
-    static constexpr int kMaxBf16 = 4, kMaxF32 = 2;
+    static constexpr int kMaxBf16 = 4, kMaxF32 = 2, kMaxTokensF32 = 4;
     struct Rows {
-        const void* base;          // bf16; rows of `width` values, `ld` elements apart
+        const void* base;          // rows of `width` values, `ld` elements apart
         int64_t rows, ld, width;
     };
+    // Packed sequences: of the token tensors (a among them, `heads` values a row)
+    // only rows cu[0] .. cu[n_seq]-1 are scanned, the others are not read by the call.
+    const int32_t* cu = nullptr;
+    int n_seq = 0, heads = 1;
     const float* a = nullptr;
     int64_t na = 0;
     Rows bf16[kMaxBf16] = {};
+    Rows tokens_f32[kMaxTokensF32] = {};
+    // A pool of states: the slots slot_idx[0 .. n) (NULL: 0 .. n) inside 0 .. n_slots.
+    const float* pool = nullptr;
+    const int32_t* slot_idx = nullptr;
+    int n = 0, n_slots = 0;
+    int64_t per_slot = 0;
     const float* f32[kMaxF32] = {};
     int64_t nf32[kMaxF32] = {};
 };
