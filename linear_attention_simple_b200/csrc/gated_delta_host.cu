@@ -328,7 +328,7 @@ gla_status group_norm_silu_bwd(const void* x, const void* gate, const float* wei
 {
     gla_status s = norm_check(x, dt, gate, weight, bias, M, G, d, &ld_x, &ld_gate, eps);
     if (s != GLA_OK) return s;
-    if (G == 0) return GLA_OK;
+    if (G == 0) M = 0;                          // no group: the gradients of shared parameters are zeros
     if (M > 0 && (!dy || !grad_x || (gate && !grad_gate))) return GLA_ERR_INVALID_ARG;
     if (!a16(dy) || !a16(grad_x) || !a16(grad_gate) || !a16(grad_weight) || !a16(grad_bias) || !a16(ws))
         return GLA_ERR_MISALIGNED;

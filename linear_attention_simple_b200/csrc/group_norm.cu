@@ -530,9 +530,9 @@ gla_status launch_group_norm_bwd(const void* x, bool f32, const void* gate, cons
         const gla_status s = run_any<true>(p, f32, st);
         if (s != GLA_OK || !p.part) return s;
     }
-    if (!dweight && !dbias) return GLA_OK;
     int blocks;
     const int C = shared_w ? d : G * d;
+    if ((!dweight && !dbias) || C == 0) return GLA_OK;
     trace_begin(st);
     group_norm_reduce_kernel<<<(C + 31) / 32, 256, 0, st>>>(ws, dweight, dbias, M > 0 ? ctas_of_block(M, G, d, &blocks) : 0, G, d, shared_w);
     trace_end(st, "group_norm_reduce_kernel");

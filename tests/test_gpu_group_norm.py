@@ -145,3 +145,18 @@ def test_eps_of_zero(M, G, d, gate, center):
         if t is not None:
             r = next(want)
             assert rel(g, r) <= (1e-5 if g.dtype == torch.float32 else U), (n, rel(g, r))
+
+
+@pytest.mark.parametrize("shape", [(3, 0, 64), (0, 4, 64)])
+def test_shared_parameters_of_no_groups_and_of_no_rows_have_gradients_of_zero(shape):
+    x = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    w, b = torch.ones(64, device="cuda"), torch.ones(64, device="cuda")
+    assert gla.group_norm_silu(x, w, b).shape == x.shape
+    grads = (torch.empty_like(x), None, torch.full_like(w, 7), torch.full_like(b, 7))
+    _, _, gw, gb = gla.group_norm_silu_bwd(x, x, w, b, grads=grads)
+    assert bool((gw == 0).all()) and bool((gb == 0).all())
+
+
+def test_parameters_per_group_of_no_groups():
+    x, w = torch.zeros(3, 0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(0, 64, device="cuda")
+    assert gla.group_norm_silu_bwd(x, x, w)[2].shape == (0, 64)
