@@ -882,17 +882,19 @@ def _norm_args(x, weight, bias, gate):
     """Check group_norm_silu's tensors; returns (M, G, d, ld_x, ld_gate, shared)."""
     if x.dim() < 2:
         raise ValueError("x must be [..., G, d]")
+    shape, dev = x.shape, x.device
+    G, d = shape[-2:]
+    M = x.numel() // (G * d) if G * d else 0
+    if M > 0x7FFFFFFF:
+        raise ValueError("x has %d rows, more than 2^31 - 1" % M)
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
     _dt(x)
-    shape, dev = x.shape, x.device
-    G, d = shape[-2:]
     first = weight if weight is not None else bias
     shared = first is not None and first.dim() == 1
     params = (d,) if shared else (G, d)
     _fit(weight, "weight", torch.float32, params, dev)
     _fit(bias, "bias", torch.float32, params, dev)
-    M = x.numel() // (G * d) if G * d else 0
     return (M, G, d, _norm_rows(x, "x", x.dtype, shape, dev), _norm_rows(gate, "gate", torch.bfloat16, shape, dev),
             int(shared))
 

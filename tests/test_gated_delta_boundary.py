@@ -165,3 +165,11 @@ def test_every_load_is_waited_for_before_its_block_ends(name):
         assert re.search(r"tma_store_wait_read\(\);\s*if \(step > 0\) mbar_wait\(&B\.kq,", text)
         drained.add("kq")
     assert len(loads) >= 3 and loads <= drained, loads - drained
+
+
+@pytest.mark.parametrize("shape", [(1 << 31, 1, 8), (1 << 16, (1 << 16) + 5, 1, 8)])
+def test_binding_refuses_more_rows_than_the_abi_counts(shape):
+    x = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    for call in (lambda: gla.group_norm_silu(x), lambda: gla.group_norm_silu_bwd(x, x)):
+        with pytest.raises(ValueError, match="rows, more than"):
+            call()
