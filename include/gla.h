@@ -510,7 +510,8 @@ gla_status group_norm_silu_bwd(const void* x, const void* gate, const float* wei
  * device status word of the current device (0 or a gla_status recorded by a
  * kernel, e.g. GLA_ERR_TIMEOUT) into *device_status and clears it.
  * gla_set_wait_limit_ns sets the bound on every device-side wait of later
- * launches (default 2e9 ns; 0 restores the default).
+ * launches (default 2e9 ns; 0 restores the default; less than 1e6 counts as
+ * 1e6, within which the copies of a kernel that gives up have landed).
  * gla_selftest_wait_timeout launches one kernel whose only wait is on a
  * barrier that nothing completes, so the bound runs out by design and the
  * kernel returns having recorded GLA_ERR_TIMEOUT; it lets callers check the

@@ -22,6 +22,7 @@ thread_local int t_last_cuda_error = 0;
 std::atomic<unsigned long long> g_launches{0};
 std::atomic<unsigned long long> g_wait_limit_ns{0};
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;  // 2 s
+constexpr unsigned long long kLeastWaitNs = 1000000ull;       // 1 ms: a block that gives up has to see its own copies land
 constexpr int kMaxDevices = 64;
 int* g_status_addr[kMaxDevices] = {};
 const void* g_status_ctx[kMaxDevices] = {};
@@ -154,7 +155,7 @@ WaitCtl wait_ctl_for_current_device(gla_status* err)
     WaitCtl c;
     c.status = status_addr_current(err);
     const unsigned long long lim = g_wait_limit_ns.load();
-    c.limit_ns = lim ? lim : kDefaultWaitNs;
+    c.limit_ns = !lim ? kDefaultWaitNs : lim < kLeastWaitNs ? kLeastWaitNs : lim;
     return c;
 }
 

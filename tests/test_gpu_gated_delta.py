@@ -522,3 +522,25 @@ def test_write_strengths_of_zero_leave_a_state_of_zeros():
         assert bool((x == 0).all()), n
     # beta stands at 2^-40 in da's sums of up to 128 x 192 terms of size 1, of either sign
     assert float(got[3].abs().max()) <= 2.0 ** -40 * (128 * 192) ** 0.5 * 8
+
+
+def test_a_short_wait_limit_still_lets_copies_land():
+    """A block that gives up waits for its own copies in flight, within the same
+    limit: so limits of less than a millisecond count as one."""
+    d, dO = make((2, 200), 2, 2, 96, 192, 87), make((2, 200), 2, 2, 96, 192, 88)["v"]
+    want = gla.gated_delta_chunk_fwd(*args(d)) + gla.gated_delta_chunk_bwd(*args(d), dO)
+    gla.gla_get_device_status()
+    gla.gla_set_wait_limit_ns(1)
+    try:
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        gla.gla_selftest_wait_timeout()
+        end.record()
+        assert gla.gla_get_device_status() == 5
+        assert 0.9 <= start.elapsed_time(end) <= 500
+        got = gla.gated_delta_chunk_fwd(*args(d)) + gla.gated_delta_chunk_bwd(*args(d), dO)
+        assert gla.gla_get_device_status() == 0
+    finally:
+        gla.gla_set_wait_limit_ns(0)
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
