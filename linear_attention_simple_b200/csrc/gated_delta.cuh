@@ -67,22 +67,22 @@ struct GdSeqs {
 
 // What the all-chunks kernel leaves of a (chunk, value head) for the sweeps:
 // one record, copied to shared memory as it is, its tiles in the layouts that
-// the tensor core reads: K and scale G Q as blocks of [64 tokens][32] (64-byte
-// swizzle), T and P as [64][64] (128-byte swizzle); then the scalars.  The
-// backward's record has Q, T and P in two bf16 terms, T without its unit
-// diagonal and P without its diagonal.
+// the tensor core reads: K as blocks of [64 tokens][32] (64-byte swizzle), T and
+// P in two bf16 terms as [64][64] (128-byte swizzle); and the scalars, in the
+// forward's record scale G in the place of P_ii.  The backward's has scale G Q
+// too, in two terms, T without its unit diagonal and P without its diagonal.
 template <int DK, bool BWD>
 struct GdRec {
     static constexpr int K = 0;
     static constexpr int SC = DK * 128;
     static constexpr int KSC = SC + gd_scalars(BWD) * kGdC * 4;    // K and the scalars: one copy
     static constexpr int Q = (KSC + 1023) / 1024 * 1024;           // tiles start on their swizzle's period
-    static constexpr int QL = Q + DK * 128;                        // BWD only
-    static constexpr int T = BWD ? QL + DK * 128 : QL;
+    static constexpr int QL = Q + DK * 128;                        // Q: BWD only
+    static constexpr int T = BWD ? QL + DK * 128 : Q;
     static constexpr int TL = T + 8192;
     static constexpr int P = TL + 8192;
-    static constexpr int PL = P + 8192;                            // BWD only
-    static constexpr int BYTES = BWD ? PL + 8192 : PL;
+    static constexpr int PL = P + 8192;
+    static constexpr int BYTES = PL + 8192;
 };
 inline size_t gd_rec_bytes(int dk, bool bwd)
 {

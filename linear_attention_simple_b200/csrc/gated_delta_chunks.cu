@@ -1,5 +1,5 @@
 // gated_delta_chunks.cu -- what the sweeps of the gated delta rule need of a
-// chunk's own tokens: decay factors, K and scale G Q, the triangular inverse
+// chunk's own tokens: decay factors, K (backward: and scale G Q), the triangular inverse
 // T = (I + tril(K K^T . D beta_j, -1))^-1 and P = tril(scale Q K^T . D), as one
 // record per (chunk, value head).  Every chunk at once, a CTA of 4 warps each.
 //
@@ -30,18 +30,17 @@ __device__ __forceinline__ void mul8(float (&f)[8], const uint4& w, float s)
         f[2 * i + 1] = s * bf16_hi(a[i]);
     }
 }
-// Eight values as one or two bf16 terms of 16 bytes.
-template <bool TWO>
+// Eight values as two bf16 terms of 16 bytes.
 __device__ __forceinline__ void put8(unsigned char* hi, unsigned char* lo, const float (&f)[8])
 {
     uint32_t a[4], b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         a[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-        if (TWO) b[i] = pack_bf16(f[2 * i] - bf16_lo(a[i]), f[2 * i + 1] - bf16_hi(a[i]));
+        b[i] = pack_bf16(f[2 * i] - bf16_lo(a[i]), f[2 * i + 1] - bf16_hi(a[i]));
     }
     *reinterpret_cast<uint4*>(hi) = make_uint4(a[0], a[1], a[2], a[3]);
-    if (TWO) *reinterpret_cast<uint4*>(lo) = make_uint4(b[0], b[1], b[2], b[3]);
+    *reinterpret_cast<uint4*>(lo) = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 // Three bf16 terms of a pair.
@@ -163,6 +162,7 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
             const int i = 2 * lane + e;
             const double b = e ? s : s - x[1];
             sc[kScG][i] = gd_exp2(static_cast<float>(b));
+            if (!BWD) sc[kScPd][i] = p.scale * sc[kScG][i];
             sc[kScR][i] = gd_exp2(static_cast<float>(last - b));
             const float bh = static_cast<float>(b);
             sc[kScBh][i] = bh;
@@ -197,14 +197,15 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
             mma_bf16(qk[2 * np + 1], fq, b[2], b[3]);
         }
     }
-    // K and scale G Q into the record
+    // K and, for the backward, scale G Q into the record
     for (int i = tid; i < kGdC * (DK / 8); i += kThreads) {
         const int r = i / (DK / 8), j = i - r * (DK / 8);
         const uint32_t at = (j >> 2) * 4096 + swz_off(r, j & 3, 64);
         *reinterpret_cast<uint4*>(rec + Rec::K + at) = *reinterpret_cast<const uint4*>(sk + r * KS + 8 * j);
+        if (!BWD) continue;
         float f[8];
         mul8(f, *reinterpret_cast<const uint4*>(sq + r * KS + 8 * j), p.scale * sc[kScG][r]);
-        put8<BWD>(rec + Rec::Q + at, rec + Rec::QL + at, f);
+        put8(rec + Rec::Q + at, rec + Rec::QL + at, f);
     }
     const int g = lane >> 2, c2 = (lane & 3) * 2;
     uint32_t ph[8][2], pl[8][2];                       // P as it leaves, once L's tile is free to carry it
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
                 *reinterpret_cast<float2*>(sl + i * kLs + j0) = make_float2(l[0], l[1]);
             }
             ph[t][hf] = pack_bf16(pv[0], pv[1]);
-            if (BWD) pl[t][hf] = pack_bf16(pv[0] - bf16_lo(ph[t][hf]), pv[1] - bf16_hi(ph[t][hf]));
+            pl[t][hf] = pack_bf16(pv[0] - bf16_lo(ph[t][hf]), pv[1] - bf16_hi(ph[t][hf]));
         }
     }
     __syncthreads();
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
             for (int hf = 0; hf < 2; ++hf) {
                 const uint32_t at = swz_off(16 * w + g + 8 * hf, t, 128) + (lane & 3) * 4;
                 *reinterpret_cast<uint32_t*>(sp + at) = ph[t][hf];
-                if (BWD) *reinterpret_cast<uint32_t*>(sp + 8192 + at) = pl[t][hf];
+                *reinterpret_cast<uint32_t*>(sp + 8192 + at) = pl[t][hf];
             }
         block_mul<32>(tt + (32 + r0) * kLs + c0, tt + (32 + r0) * kLs + 32, tt + 32 + c0, -1.f, lane);
     }
@@ -298,9 +299,9 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
         for (int e = 0; e < 8; ++e)
             if (j0 + e > r || (BWD && j0 + e == r)) f[e] = 0.f;
         const uint32_t at = swz_off(r, i & 7, 128);
-        put8<true>(rec + Rec::T + at, rec + Rec::TL + at, f);
+        put8(rec + Rec::T + at, rec + Rec::TL + at, f);
     }
-    for (int i = tid; i < (BWD ? 1024 : 512); i += kThreads)
+    for (int i = tid; i < 1024; i += kThreads)
         reinterpret_cast<uint4*>(rec + Rec::P)[i] = reinterpret_cast<const uint4*>(sl)[i];
     for (int i = tid; i < kSc * kGdC / 4; i += kThreads)
         reinterpret_cast<float4*>(rec + Rec::SC)[i] = reinterpret_cast<const float4*>(&sc[0][0])[i];

@@ -495,12 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1) gd_grad_kernel(GdParams p, const 
 template <int DK>
 gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
 {
-    const uint64_t tokens = p.seqs.cu ? p.seqs.T : static_cast<uint64_t>(p.seqs.N) * p.seqs.T;
+    const int64_t tokens = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;
     const int64_t wv = static_cast<int64_t>(p.seqs.H) * p.dv, wk = static_cast<int64_t>(p.seqs.Hk) * DK;
-    auto map = [&](CUtensorMap* m, const void* base, int64_t width, int64_t ld, uint32_t box, int swizzle) {
-        const uint64_t dims[2] = {static_cast<uint64_t>(width), tokens}, strides[2] = {2, static_cast<uint64_t>(ld) * 2};
-        const uint32_t boxes[2] = {box, kGdC};
-        return make_tmap(m, base, 2, dims, strides, boxes, 2, swizzle);
+    auto map = [&](CUtensorMap* m, const void* base, int64_t width, int64_t ld, int box, int swizzle) {
+        return gd_block_map(m, base, width, ld, tokens, box, swizzle);
     };
     Maps maps;
     gla_status s;

@@ -8,15 +8,18 @@
 // chunk, M = 128 lanes of dv rows, N tokens or dk columns:
 //
 //   Y  = S K^T            workers:  R  = V - G Y
-//   O  = S (scale G Q)^T
+//   O  = S Q^T                               scale G O
 //   Z  = R T^T                      V' = beta Z,  W = (e^{b_63 - b} V')
 //   dS = W K                        S  = G_63 S + dS   (fp32, in registers)
 //   O += V' P^T                     o
 //
 // with T = (I + tril(K K^T . D beta_j, -1))^-1.  Worker threads hold one lane
-// (dv row) and half of the columns.  S, R and W enter as two bf16 terms
-// against operands exact in bf16 (K) or of two terms (T): 16 bits of each
-// value, for the fp32 state; o leaves in bf16 and takes one term of each.
+// (dv row) and half of the columns.  S, R, W and V' enter as two bf16 terms
+// against operands exact in bf16 (K, Q) or of two terms (T, P): 16 bits of each
+// value, for the fp32 state; o's error is its own rounding.  (One term each of S,
+// scale G Q, V' and P, as o leaves in bf16, put o 3.0e-3 from 64 bits where its
+// rounding alone is 1.7e-3, and took 217 us for 8 x 2,048 tokens of 16 heads of
+// 96 x 192 with the chunks' kernel, 228 so.)
 //
 // V is read from a shared [token][row] slice and o leaves through the same
 // one, two stages, each a single tensor copy (a bulk copy per token row was
@@ -45,9 +48,13 @@ template <int DK>
 struct Cols {
     static constexpr int S = 0;                      // state terms -> Z -> dS
     static constexpr int Y = DK;                     // Y -> R terms -> W terms
-    static constexpr int V = DK + 64;                // V', one term
-    static constexpr int O = DK + 96;
-    static constexpr int alloc(bool pre) { return pre || DK + 160 <= 256 ? 256 : 512; }
+    static constexpr int V = DK + 64;                // V'
+    // V' second term: where two CTAs share an SM at dk = 96 all columns are taken,
+    // but the last 32 of the state's are free between Z and dS
+    static constexpr bool TIGHT = DK == 96;
+    static constexpr int VL = TIGHT ? 64 : DK + 96;
+    static constexpr int O = TIGHT ? DK + 96 : DK + 128;
+    static constexpr int alloc(bool pre) { return pre || O + 64 <= 256 ? 256 : 512; }
 };
 
 struct __align__(8) Bars {
@@ -55,7 +62,7 @@ struct __align__(8) Bars {
     uint64_t fq, ft, fp, eq, et, ep;                 // Q, T, P
     uint64_t s, r, w, o;                             // workers -> issuer
     uint64_t staged[2];                              // workers -> copies: o is in the V slice
-    uint64_t y, z, ds, out, drain;                   // issuer -> workers
+    uint64_t y, q, z, ds, out, drain;                // issuer -> workers
     uint32_t tmem;
 };
 
@@ -64,7 +71,7 @@ template <int DK, bool PRE>
 struct Smem {
     using Rec = GdRec<DK, false>;
     static constexpr int KSC = (Rec::KSC + 1023) / 1024 * 1024;    // a stage of K and scalars
-    static constexpr int T = 2 * KSC, Q = T + 16384, P = Q + DK * 128, V = PRE ? Q : P + 8192;
+    static constexpr int T = 2 * KSC, Q = T + 16384, P = Q + DK * 128, V = PRE ? Q : P + 16384;
     static constexpr int bytes(int sw) { return V + 2 * kGdC * sw * 2 + 1024; }
 };
 
@@ -74,8 +81,8 @@ struct Smem {
 enum { kSweep = 0, kSegments = 1, kSegmentsBwd = 2 };
 template <int DK, int MODE>
 __global__ void __launch_bounds__(kGdThreads, DK <= 96 || MODE != kSweep ? 2 : 1)
-gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __grid_constant__ GdMap map_o, int sw, int nslices,
-                    WaitCtl ctl)
+gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __grid_constant__ GdMap map_o,
+                    const __grid_constant__ CUtensorMap map_q, int sw, int nslices, WaitCtl ctl)
 {
     using C = Cols<DK>;
     constexpr bool PRE = MODE != kSweep;
@@ -122,7 +129,7 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
         for (uint64_t* b : tiles) mbar_init(b, 1);
         uint64_t* from_workers[4] = {&B.s, &B.r, &B.w, &B.o};
         for (uint64_t* b : from_workers) mbar_init(b, active);
-        uint64_t* from_issuer[5] = {&B.y, &B.z, &B.ds, &B.out, &B.drain};
+        uint64_t* from_issuer[6] = {&B.y, &B.q, &B.z, &B.ds, &B.out, &B.drain};
         for (uint64_t* b : from_issuer) mbar_init(b, 1);
         mbar_init_fence();
     }
@@ -142,7 +149,7 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             const CUtensorMap* mv = whole ? &map_v.all : &map_v.last;
             const CUtensorMap* mo = whole ? &map_o.all : &map_o.last;
             const uint32_t vbytes = kGdC * rows * 2;
-            const int col = h * p.dv + w0;
+            const int col = h * p.dv + w0, hk = h / (p.seqs.H / p.seqs.Hk);
             bool ok = true;
             // K, scalars and V of chunk c (rows behind the sequence's end are not used)
             auto first = [&](int c) {
@@ -163,15 +170,19 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             if (nc > 0) first(a++);
             for (int c = 0; c < nc; ++c) {
                 if (!PRE) {
-                    ok = tile(c, &B.fq, &B.eq, M::Q, Rec::Q, DK * 128);
+                    ok = c == 0 || mbar_wait(&B.eq, (c - 1) & 1, ctl);
                     if (!ok) break;
+                    mbar_arrive_expect_tx(&B.fq, DK * 128);          // (what lies behind the sequence's end gives columns of o that do not leave)
+#pragma unroll
+                    for (int i = 0; i < DK / 32; ++i)
+                        tma_load_2d(smem + M::Q + i * 4096, &map_q, &B.fq, hk * DK + 32 * i, static_cast<int>(row0) + c * kGdC);
                     ++q;
                 }
                 ok = tile(c, &B.ft, &B.et, M::T, Rec::T, 16384);
                 if (!ok) break;
                 ++t;
                 if (!PRE) {
-                    ok = tile(c, &B.fp, &B.ep, M::P, Rec::P, 8192);
+                    ok = tile(c, &B.fp, &B.ep, M::P, Rec::P, 16384);
                     if (!ok) break;
                     ++pp;
                 }
@@ -240,9 +251,12 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                     if (!mbar_wait(&B.fq, c & 1, ctl)) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        umma_bf16_ts(tm + C::O, tm + C::S + 16 * k, desc_add(q_k, (k >> 1) * 4096 + (k & 1) * 32), id64,
-                                     k > 0);
+                    for (int k = 0; k < DK / 16; ++k) {
+                        const uint64_t b = desc_add(q_k, (k >> 1) * 4096 + (k & 1) * 32);
+                        umma_bf16_ts(tm + C::O, tm + C::S + 16 * k, b, id64, k > 0);
+                        umma_bf16_ts(tm + C::O, tm + C::S + 16 * k + 8, b, id64, 1);
+                    }
+                    umma_commit(&B.q);
                     umma_commit(&B.eq);
                 }
                 if (!mbar_wait(&B.ft, c & 1, ctl)) break;
@@ -261,7 +275,15 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 umma_commit(&B.z);
                 umma_commit(&B.et);
                 if (!mbar_wait(&B.w, c & 1, ctl)) break;
+                if (!PRE && C::TIGHT && !mbar_wait(&B.fp, c & 1, ctl)) break;
                 tc_fence_after();
+                auto add_low = [&]() {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        umma_bf16_ts(tm + C::O + 16 * s, tm + C::VL + 8 * s, desc_add(p_k, 2048 * s + 32 * s),
+                                     idesc_bf16_f32(128, 64 - 16 * s, 0, 0), 1);
+                };
+                if (!PRE && C::TIGHT) add_low();             // dS takes its place
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     umma_bf16_ts(tm + C::S, tm + C::Y + 16 * s, desc_add(k_n, 1024 * s), idDk, s > 0);
@@ -269,11 +291,17 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 }
                 umma_commit(&B.ds);
                 if (!PRE) {
-                    if (!mbar_wait(&B.fp, c & 1, ctl)) break;
+                    if (!C::TIGHT) {
+                        if (!mbar_wait(&B.fp, c & 1, ctl)) break;
+                        add_low();
+                    }
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        umma_bf16_ts(tm + C::O + 16 * s, tm + C::V + 8 * s, desc_add(p_k, 2048 * s + 32 * s),
-                                     idesc_bf16_f32(128, 64 - 16 * s, 0, 0), 1);
+                    for (int s = 0; s < 4; ++s) {
+                        const uint32_t id = idesc_bf16_f32(128, 64 - 16 * s, 0, 0);
+                        const uint64_t hi = desc_add(p_k, 2048 * s + 32 * s);
+                        umma_bf16_ts(tm + C::O + 16 * s, tm + C::V + 8 * s, hi, id, 1);
+                        umma_bf16_ts(tm + C::O + 16 * s, tm + C::V + 8 * s, desc_add(hi, 8192), id, 1);
+                    }
                     umma_commit(&B.out);
                     umma_commit(&B.ep);
                 }
@@ -328,6 +356,15 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 if (MODE == kSegmentsBwd) put16(t0 + C::S + 16 * (s + b), r);         // this record's T lacks its diagonal
             }
             warp_done(&B.r, lane);
+            if (!PRE) {
+                // Q is exact in bf16, so its factor scale G comes here, while Z is on its way
+                ok = warp_wait(&B.q, ph, ctl);
+                if (!ok) break;
+                tc_fence_after();
+                get16x2(x[0], x[1], t0 + C::O + 16 * s, t0 + C::O + 16 * s + 16);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) put16(t0 + C::O + 16 * (s + b), load16(sc + kScPd * kGdC + 16 * b) * x[b]);
+            }
             ok = warp_wait(&B.z, ph, ctl);
             if (!ok) break;
             tc_fence_after();
@@ -335,7 +372,7 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 x[b] = x[b] * load16(sc + kScBeta * kGdC + 16 * b);
-                if (!PRE) put_terms<1>(t0 + C::V + 8 * (s + b), x[b]);
+                if (!PRE) put_two(t0 + C::V + 8 * (s + b), t0 + C::VL + 8 * (s + b), x[b]);
                 put_terms<2>(t0 + C::Y + 16 * (s + b), x[b] * load16(sc + kScR * kGdC + 16 * b));
             }
             warp_done(&B.w, lane);
@@ -522,7 +559,7 @@ gla_status segments(const GdParams& p, const GdMap& v, const GdMap& o, const GdS
     if (e != cudaSuccess) return status_of(e);
     trace_begin(st);
     gd_sweep_fwd_kernel<DK, MODE><<<static_cast<unsigned>(p.seqs.N) * p.seqs.H * p.nseg * (sl.n + 1), kGdThreads, smem, st>>>(
-        p, v, o, sl.width, sl.n + 1, ctl);
+        p, v, o, CUtensorMap{}, sl.width, sl.n + 1, ctl);
     trace_end(st, "gd_sweep_segments_kernel");
     count_launch();
     const gla_status s = check_launch("gd_sweep_segments_kernel");
@@ -536,9 +573,11 @@ gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
     const int64_t width = static_cast<int64_t>(p.seqs.H) * p.dv;
     const int64_t tokens = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;
     GdMap v{}, o{};
+    CUtensorMap q{};
     gla_status s = GLA_OK;
     if (tokens > 0 && ((s = gd_slice_map(&v, p.v, width, p.ld_v, tokens, sl.width, sl.last)) != GLA_OK ||
-                       (s = gd_slice_map(&o, p.o, width, width, tokens, sl.width, sl.last)) != GLA_OK))
+                       (s = gd_slice_map(&o, p.o, width, width, tokens, sl.width, sl.last)) != GLA_OK ||
+                       (s = gd_block_map(&q, p.q, static_cast<int64_t>(p.seqs.Hk) * DK, p.ld_qk, tokens, 32, 64)) != GLA_OK))
         return s;
     const int smem = Smem<DK, false>::bytes(sl.width);
     const unsigned pairs = static_cast<unsigned>(p.seqs.N) * p.seqs.H;
@@ -546,7 +585,7 @@ gla_status launch(const GdParams& p, const WaitCtl& ctl, cudaStream_t st)
     if (e != cudaSuccess) return status_of(e);
     if (p.nseg > 1 && (s = segments<DK, kSegments>(p, v, o, sl, ctl, st)) != GLA_OK) return s;
     trace_begin(st);
-    gd_sweep_fwd_kernel<DK, kSweep><<<pairs * p.nseg * sl.n, kGdThreads, smem, st>>>(p, v, o, sl.width, sl.n, ctl);
+    gd_sweep_fwd_kernel<DK, kSweep><<<pairs * p.nseg * sl.n, kGdThreads, smem, st>>>(p, v, o, q, sl.width, sl.n, ctl);
     trace_end(st, "gd_sweep_fwd_kernel");
     count_launch();
     return check_launch("gd_sweep_fwd_kernel");

@@ -36,6 +36,15 @@ inline gla_status gd_slice_map(GdMap* m, const void* base, int64_t width, int64_
     return s != GLA_OK ? s : make_tmap(&m->last, base, 2, dims, strides, tail, 2, 0);
 }
 
+// The same rows in boxes of `box` columns, swizzled.
+inline gla_status gd_block_map(CUtensorMap* m, const void* base, int64_t width, int64_t ld, int64_t tokens, int box, int swizzle)
+{
+    const uint64_t dims[2] = {static_cast<uint64_t>(width), static_cast<uint64_t>(tokens)};
+    const uint64_t strides[2] = {2, static_cast<uint64_t>(ld) * 2};
+    const uint32_t boxes[2] = {static_cast<uint32_t>(box), kGdC};
+    return make_tmap(m, base, 2, dims, strides, boxes, 2, swizzle);
+}
+
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -186,7 +195,7 @@ __device__ __forceinline__ void put16(uint32_t taddr, const Cols16& x)
 // terms hold 16 bits of a value (off by at most 2^-17 of it), three 24, where
 // one rounding (2^-9) would be all of the fp32 outputs' error.
 template <int NT>
-__device__ __forceinline__ void put_terms(uint32_t taddr, const Cols16& v, uint32_t taddr2 = 0)
+__device__ __forceinline__ void put_terms(uint32_t (&at)[NT], const Cols16& v)
 {
     Cols16 x = v;
 #pragma unroll
@@ -197,8 +206,21 @@ __device__ __forceinline__ void put_terms(uint32_t taddr, const Cols16& v, uint3
             w[i] = f2_to_bf16x2(x.p[i]);
             if (n + 1 < NT) x.p[i] = f2_sub(x.p[i], f2_from_bf16x2(w[i]));
         }
-        tmem_st8(n < 2 ? taddr + 8 * n : taddr2, w);
+        tmem_st8(at[n], w);
     }
+}
+template <int NT>
+__device__ __forceinline__ void put_terms(uint32_t taddr, const Cols16& v, uint32_t taddr2 = 0)
+{
+    uint32_t at[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) at[n] = n < 2 ? taddr + 8 * n : taddr2;
+    put_terms<NT>(at, v);
+}
+__device__ __forceinline__ void put_two(uint32_t high, uint32_t low, const Cols16& v)
+{
+    uint32_t at[2] = {high, low};
+    put_terms<2>(at, v);
 }
 // S = f S + HS columns of what the products added.
 template <int HS>

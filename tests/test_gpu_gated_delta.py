@@ -544,3 +544,28 @@ def test_a_short_wait_limit_still_lets_copies_land():
         gla.gla_set_wait_limit_ns(0)
     for x, y in zip(want, got):
         assert torch.equal(x, y)
+
+
+def beyond_rounding(x, ref):
+    """By how much the elements of a bf16 x are off beyond a rounding of ref, at
+    most, against the root mean square of ref's rows."""
+    ref = ref.double()
+    over = (x.double() - ref).abs() - U * ref.abs()
+    rms = ref.square().mean(-1, keepdim=True).sqrt().clamp_min(1e-300)
+    return float((over / rms).max())
+
+
+# What o's own rounding does not account for, per element: pairs of bf16 terms leave 8 P
+# of the terms' root mean square (TOL_S), whose largest of some 10^6 is five times that;
+# the two parts of o (state, chunk) are up to 1.5 times their sum.  One term in a pair's
+# place leaves 2^-10 of the root mean square and more.
+TOL_ROUNDED = 8 * P * 5 * 1.5
+
+
+@pytest.mark.parametrize("decay", ["usual", "slow", "strong"])
+@pytest.mark.parametrize("N,T,Hk,H,dk,dv", [(2, 1, 1, 2, 96, 192), (2, 300, 2, 4, 96, 192), (2, 130, 1, 2, 128, 128),
+                                            (2, 130, 1, 2, 64, 64), (1, 900, 1, 1, 96, 160), (1, 100, 1, 1, 64, 256)])
+def test_o_is_off_by_its_own_rounding(N, T, Hk, H, dk, dv, decay):
+    d, s0 = make((N, T), Hk, H, dk, dv, 90, decay), states(N, H, dk, dv, 91)
+    o, _ = gla.gated_delta_chunk_fwd(*args(d), s0=s0)
+    assert beyond_rounding(o, forward(d, s0, dk ** -0.5)[0]) <= TOL_ROUNDED
