@@ -28,14 +28,15 @@ constexpr int kGdC = 64;                 // tokens per chunk
 constexpr int kGdPad = 8;                // bf16 elements behind each shared-memory row: rows an odd
                                          // multiple of 16 bytes apart, so ldmatrix has no bank conflicts
 constexpr int kGdPiece = 32 * 16;        // a piece: 16 values of each of 32 dv rows (32-byte swizzle)
-// Per-token scalars of a chunk: G, R, beta, P_ii, b (high, low).  The backward's
-// two more: beta~, which is beta but no nearer to zero than 2^-40, and beta / beta~.
-// dbeta is <dv, z> / beta, and dv = beta dV' would lose its bits (at beta = 0 all
-// of them): so T and the reverse sweep have beta~, which changes their sums by
-// 2^-40 of a term; V' has beta, and dv leaves with the factor.  (1e-30 in beta~'s
-// place left dbeta 14 bits at a dO of 2^-30 and none at 2^-60.)
+// Per-token scalars of a chunk: G, R, beta~, P_ii, b (high, low).  beta~ is beta in
+// the forward; in the backward it is beta but no nearer to zero than 2^-40, and two
+// scalars more are beta and beta / beta~.  dbeta is <dv, z> / beta, and dv = beta dV'
+// would lose its bits (at beta = 0 all of them): so T and the reverse sweep have
+// beta~, which changes their sums by 2^-40 of a term; V' has beta, and dv leaves with
+// the factor.  (1e-30 in beta~'s place left dbeta 14 bits at a dO of 2^-30 and none
+// at 2^-60.)
 constexpr int gd_scalars(bool bwd) { return bwd ? 8 : 6; }
-enum { kScG = 0, kScR = 1, kScBeta = 2, kScPd = 3, kScBh = 4, kScBl = 5, kScBt = 6, kScF = 7 };
+enum { kScG = 0, kScR = 1, kScBt = 2, kScPd = 3, kScBh = 4, kScBl = 5, kScBeta = 6, kScF = 7 };
 constexpr float kGdBetaMin = 0x1p-40f;
 
 // Sequences of one call: dense [N][T] (cu null) or packed rows cu[n] .. cu[n+1]-1.

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
     __nv_bfloat16* sq = sk + kGdC * KS;
     float* sl = reinterpret_cast<float*>(sq + kGdC * KS);          // L
     float* tt = reinterpret_cast<float*>(smem);                    // T, over K and Q once both are read
-    constexpr int kSc = gd_scalars(BWD), kB = BWD ? kScBt : kScBeta;       // beta as T has it
+    constexpr int kSc = gd_scalars(false);             // (the backward's last two: five CTAs share an SM without them)
     __shared__ float sc[kSc][kGdC];
 
     const int64_t slot = blockIdx.x;
@@ -132,23 +132,28 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
     cp_async_commit();
     if (w == 0) {
         double x[2];
+        float be[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = 2 * lane + e;
             const int64_t at = (row + i) * p.seqs.H + h;
-            float av = 0.f, be = 0.f;
+            float av = 0.f;
+            be[e] = 0.f;
             if (i < valid) {
                 av = p.a[at];
                 av = av < -1e4f ? -1e4f : av;          // (a NaN stays one)
-                be = p.beta[at];
+                be[e] = p.beta[at];
             }
-            sc[kScBeta][i] = be;
-            if (BWD) {
-                const bool small = fabsf(be) < kGdBetaMin;
-                sc[kB][i] = small ? kGdBetaMin : be;
-                sc[kSc - 1][i] = small ? be * (1.f / kGdBetaMin) : 1.f;
-            }
+            sc[kScBt][i] = BWD && fabsf(be[e]) < kGdBetaMin ? kGdBetaMin : be[e];
             x[e] = static_cast<double>(av) * 1.4426950408889634074;
+        }
+        if (BWD) {
+            int64_t u = slot;                          // (the address is formed anew later: held so long it costs an SM its fifth CTA)
+            asm volatile("" : "+l"(u));
+            float2* more = reinterpret_cast<float2*>(p.rec + (u * p.seqs.H + h) * Rec::BYTES + Rec::SC) + lane;
+            auto missing = [](float v) { return fabsf(v) < kGdBetaMin ? v * (1.f / kGdBetaMin) : 1.f; };
+            more[kScBeta * kGdC / 2] = make_float2(be[0], be[1]);
+            more[kScF * kGdC / 2] = make_float2(missing(be[0]), missing(be[1]));
         }
         double s = x[0] + x[1];
 #pragma unroll
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) gd_chunks_kernel(GdParams p)
                 const float bh = sc[kScBh][i], bl = sc[kScBl][i];
                 const float2 jh = *reinterpret_cast<const float2*>(&sc[kScBh][j0]);
                 const float2 jl = *reinterpret_cast<const float2*>(&sc[kScBl][j0]);
-                const float2 be = *reinterpret_cast<const float2*>(&sc[kB][j0]);
+                const float2 be = *reinterpret_cast<const float2*>(&sc[kScBt][j0]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int j = j0 + e;

@@ -371,7 +371,7 @@ gd_sweep_fwd_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             get16x2(x[0], x[1], t0 + C::S + 16 * s, t0 + C::S + 16 * s + 16);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                x[b] = x[b] * load16(sc + kScBeta * kGdC + 16 * b);
+                x[b] = x[b] * load16(sc + (MODE == kSegmentsBwd ? kScBeta : kScBt) * kGdC + 16 * b);
                 if (!PRE) put_two(t0 + C::V + 8 * (s + b), t0 + C::VL + 8 * (s + b), x[b]);
                 put_terms<2>(t0 + C::Y + 16 * (s + b), x[b] * load16(sc + kScR * kGdC + 16 * b));
             }
