@@ -190,7 +190,7 @@ struct GdParams {
     float* sn;              // [u][dv / 32][2][dk / 8][32 lanes][4]: the state entering in fp32, half rows
     float* sn_last;         // [N H][..]: the final state in the same form
     float* yn;              // [u][dv / 32][2][8][32 lanes][4]: y, half rows
-    __nv_bfloat16* vp;      // [u][dv / 32][4][piece]: V', 16 tokens a piece
+    __nv_bfloat16* vp;      // [u][dv / 32][2][4][piece]: V', two terms, 16 tokens a piece
     float* part;            // [u][3][dv / 32][64]: sums over 32 dv rows, per token
     float* anch;            // [u][dv / 32][2]: <gradient of the state leaving, state leaving>
     // segments of seg_chunks chunks, at most nseg of a sequence; per (sequence,

@@ -16,23 +16,27 @@
 //
 // ([.; V']: its upper rows are whatever lies before V' in shared memory; what
 // they give is not read).  Workers take scale G D2 and -G D2 + R D3 into their
-// registers, turn D1, masked and decayed, into A over B (bf16, in shared memory),
-// and the tensor core reads those as they stand and transposed:
+// registers, turn D1, masked and decayed, into A over B (in shared memory), and
+// the tensor core reads those as they stand and transposed:
 //
 //   D4 = [A; B] K + [0; B^T] K + [0; A^T] Q
 //
-// The value heads that share a q/k head are added up in the registers.  dq and
-// dk leave in bf16, so every operand is one bf16 rounding of its value; the sums
-// behind da and dbeta come in fp32 from the sweeps, and a warp of its own adds
-// them up.
+// The value heads that share a q/k head are added up in the registers.  V', A and
+// B are two bf16 terms, dO, K and Q are exact; S, E and dv are one term each: the
+// parts that they give are the smaller ones unless decays are slow, and their
+// second terms would double this kernel's bytes.  With the usual decays dq is off
+// by 1.74e-3 and dk by 1.8e-3, of which 1.66e-3 is their own rounding (one term of
+// V', A and B too: 2.9e-3; 147 us here and 304 in the reverse sweep where it is
+// 171 and 332 so); with slow ones by 2.3e-3 and 2.5e-3.  The sums behind da and
+// dbeta come in fp32 from the sweeps, and a warp of its own adds them up.
 //
 // The states and V' are read as the sweeps left them, in pieces of 16 values of
 // 32 dv rows with the tensor core's 32-byte swizzle.  One CTA an SM walks over
-// (chunk, head): a ring of three stages of 64 dv columns keeps the loads going,
+// (chunk, head): a ring of stages of 64 dv columns keeps the loads going,
 // and the products of the next unit start as soon as D2 and D3 are read (D1 has
 // two buffers).  Every byte is read once, and HBM bounds it: 8 x 2,048 tokens,
-// 16 heads of 96 x 192, 819 MB in 146 us, 5.6 TB/s.  (With mma.sync, two passes
-// over dv and 12 warps an SM, latency did: 272 us.)
+// 16 heads of 96 x 192, 920 MB in 171 us, 5.4 TB/s.  (With one term each, mma.sync,
+// two passes over dv and 12 warps an SM, latency did: 272 us against 146.)
 #include "gated_delta_tc.cuh"
 
 namespace gla {
@@ -41,7 +45,6 @@ namespace {
 constexpr int kSms = 148;
 constexpr int kThreads = (kGdWorkers + 4) * 32;      // + a slice, an issue, a sums and a tile warp
 constexpr int kCols = 64;                            // dv columns of a stage
-constexpr int kStages = 3;
 constexpr int kPieceBytes = kGdPiece * 2;
 constexpr int kMaxWarps = 8;                         // of 32 dv rows (dv <= 256)
 
@@ -53,15 +56,17 @@ struct Cols {
 template <int DK>
 struct Smem {
     using Rec = GdRec<DK, true>;
-    static constexpr int VB = 4 * kPieceBytes, SB = DK / 16 * kPieceBytes;        // of 32 dv columns
+    static constexpr int VB = 8 * kPieceBytes, SB = DK / 16 * kPieceBytes;        // of 32 dv columns
     static constexpr int X = 0, Y = 8192, V = 16384, S = V + 2 * VB, E = S + 2 * SB, STAGE = E + 2 * SB;
-    // a tile of zeros, A, B; K and Q, later dk and dq; b of two units
-    static constexpr int Z = kStages * STAGE, A = Z + 8192, K = A + 2 * 8192, Q = K + kGdC * DK * 2, SC = Q + kGdC * DK * 2;
+    // a tile of zeros, A, B, their second terms; K and Q, later dk and dq; b of two units
+    static constexpr int STAGES = DK == 64 ? 3 : 2, AB = 2 * 8192;
+    static constexpr int Z = STAGES * STAGE, A = Z + 8192, K = A + 2 * AB, Q = K + kGdC * DK * 2, SC = Q + kGdC * DK * 2;
     static constexpr int SCB = 2 * kGdC * 4, BARS = SC + 2 * SCB, bytes = BARS + 256 + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory of an SM");
 };
+template <int STAGES>
 struct __align__(8) Bars {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[STAGES], empty[STAGES];
     uint64_t sc[2], sc_done[2];                      // b; workers -> copies
     uint64_t kq, kq_done;                            // K and Q; workers -> copies: free, or holding dk and dq
     uint64_t d123, d4, drain;                        // issuer -> workers, itself
@@ -180,8 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1) gd_grad_kernel(GdParams p, const 
     using Rec = GdRec<DK, true>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    Bars& B = *reinterpret_cast<Bars*>(smem + M::BARS);
-    static_assert(sizeof(Bars) <= 256, "");
+    constexpr int kStages = M::STAGES;
+    Bars<kStages>& B = *reinterpret_cast<Bars<kStages>*>(smem + M::BARS);
+    static_assert(sizeof(B) <= 256, "");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int H = p.seqs.H, group = H / p.seqs.Hk, ns = (p.dv + kCols - 1) / kCols;
     if (tid == 0) {
@@ -308,11 +314,17 @@ __global__ void __launch_bounds__(kThreads, 1) gd_grad_kernel(GdParams p, const 
             const uint64_t ab = smem_desc(smem_u32(smem + M::A), 16, 1024, kLayoutSW128);
             const uint64_t at = smem_desc(smem_u32(smem + M::Z), 8192, 1024, kLayoutSW128);         // zeros, then A
             const uint64_t bt = smem_desc(smem_u32(smem + M::Z), 16384, 1024, kLayoutSW128);        // zeros, then B
+            const uint64_t atl = smem_desc(smem_u32(smem + M::Z), 8192 + M::AB, 1024, kLayoutSW128);
+            const uint64_t btl = smem_desc(smem_u32(smem + M::Z), 16384 + M::AB, 1024, kLayoutSW128);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                umma_bf16(tm + C::D4, desc_add(ab, 32 * k), desc_add(k_n, 1024 * k), id2, k > 0);
-                umma_bf16(tm + C::D4, desc_add(bt, 2048 * k), desc_add(k_n, 1024 * k), id3, 1);
-                umma_bf16(tm + C::D4, desc_add(at, 2048 * k), desc_add(q_n, 1024 * k), id3, 1);
+                const uint64_t kb = desc_add(k_n, 1024 * k), qb = desc_add(q_n, 1024 * k);
+                umma_bf16(tm + C::D4, desc_add(ab, 32 * k), kb, id2, k > 0);
+                umma_bf16(tm + C::D4, desc_add(ab, 32 * k + M::AB), kb, id2, 1);
+                umma_bf16(tm + C::D4, desc_add(bt, 2048 * k), kb, id3, 1);
+                umma_bf16(tm + C::D4, desc_add(btl, 2048 * k), kb, id3, 1);
+                umma_bf16(tm + C::D4, desc_add(at, 2048 * k), qb, id3, 1);
+                umma_bf16(tm + C::D4, desc_add(atl, 2048 * k), qb, id3, 1);
             }
             umma_commit(&B.d4);
             return true;
@@ -331,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) gd_grad_kernel(GdParams p, const 
                         const uint32_t at = smem_u32(smem + st * M::STAGE);
                         const uint64_t xy = smem_desc(at + M::X, 16, 1024, kLayoutSW128);
                         const uint64_t v = smem_desc(at + M::V, kPieceBytes, 256, kLayoutSW32);
-                        const uint64_t vl = smem_desc(at + M::V - M::VB, kPieceBytes, 256, kLayoutSW32);
+                        const uint64_t vm = smem_desc(at + M::V - M::VB / 2, kPieceBytes, 256, kLayoutSW32);
                         const uint64_t sd = smem_desc(at + M::S, kPieceBytes, 256, kLayoutSW32);
                         const uint64_t ed = smem_desc(at + M::E, kPieceBytes, 256, kLayoutSW32);
                         const uint32_t on = s > 0;
@@ -342,8 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1) gd_grad_kernel(GdParams p, const 
                             const uint32_t acc = k > 0 ? 1 : on;
                             const uint64_t a = desc_add(xy, 32 * k);
                             umma_bf16(d1, a, desc_add(v, vo), id1, acc);
+                            umma_bf16(d1, a, desc_add(v, vo + M::VB / 2), id1, 1);
                             umma_bf16(tm + C::D2, a, desc_add(sd, so), id2, acc);
-                            umma_bf16(tm + C::D3, desc_add(vl, vo), desc_add(ed, so), id3, acc);
+                            umma_bf16(tm + C::D3, desc_add(vm, vo), desc_add(ed, so), id3, acc);
+                            umma_bf16(tm + C::D3, desc_add(vm, vo + M::VB / 2), desc_add(ed, so), id3, 1);
                         }
                         umma_commit(&B.empty[st]);
                         // while the workers get to this unit: the last product of the one before
@@ -409,10 +423,10 @@ __global__ void __launch_bounds__(kThreads, 1) gd_grad_kernel(GdParams p, const 
                     unsigned char* tile = smem + M::A + (is_k ? 8192 : 0);
 #pragma unroll 1
                     for (int c = 2 * half; c < 2 * half + 2; ++c) {
-                        uint32_t w[8];
+                        uint32_t w[8], l[8];
                         if (16 * c > (warp & 1) * 32 + 31) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = 0u;
+                            for (int e = 0; e < 8; ++e) w[e] = l[e] = 0u;
                         } else {
                             uint32_t d[16];
                             tmem_ld16(t0 + C::D1 + 64 * (step & 1) + 16 * c, d);
@@ -433,10 +447,15 @@ __global__ void __launch_bounds__(kThreads, 1) gd_grad_kernel(GdParams p, const 
                                 if (16 * c + e >= end) m[e] = 0.f;
                             }
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = pack_bf16(m[2 * e], m[2 * e + 1]);
+                            for (int e = 0; e < 8; ++e) {
+                                w[e] = pack_bf16(m[2 * e], m[2 * e + 1]);
+                                l[e] = pack_bf16(m[2 * e] - bf16_lo(w[e]), m[2 * e + 1] - bf16_hi(w[e]));
+                            }
                         }
                         *reinterpret_cast<uint4*>(tile + swz_off(i, 2 * c, 128)) = make_uint4(w[0], w[1], w[2], w[3]);
                         *reinterpret_cast<uint4*>(tile + swz_off(i, 2 * c + 1, 128)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        *reinterpret_cast<uint4*>(tile + M::AB + swz_off(i, 2 * c, 128)) = make_uint4(l[0], l[1], l[2], l[3]);
+                        *reinterpret_cast<uint4*>(tile + M::AB + swz_off(i, 2 * c + 1, 128)) = make_uint4(l[4], l[5], l[6], l[7]);
                     }
                 }
                 if (x.valid < kGdC && (warp & 3) == 0) {

@@ -106,7 +106,7 @@ size_t gd_layout(GdParams& p, bool bwd, unsigned char* base)
         p.sn = reinterpret_cast<float*>(take(u * dk * dv * 4));
         p.sn_last = reinterpret_cast<float*>(take(static_cast<size_t>(p.seqs.N) * p.seqs.H * dk * dv * 4));
         p.yn = reinterpret_cast<float*>(take(u * kGdC * dv * 4));
-        p.vp = reinterpret_cast<__nv_bfloat16*>(take(u * kGdC * dv * 2));
+        p.vp = reinterpret_cast<__nv_bfloat16*>(take(u * 2 * kGdC * dv * 2));
         p.part = reinterpret_cast<float*>(take(u * 3 * (dv / 32) * kGdC * 4));
         p.anch = reinterpret_cast<float*>(take(u * (dv / 32) * 2 * 4));
     }

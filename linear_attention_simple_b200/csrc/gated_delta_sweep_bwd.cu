@@ -8,7 +8,7 @@
 //   y  = G S K^T - R T^T,  R = V - y's first term      z = V - y,  V' = beta z
 //   o' = S (scale G Q)^T + V' P^T                      o without the token's own part
 //   S  = G_63 S + (e^{b_63 - b} V') K
-// kept: S (bf16, and fp32 for the sums), y, V', and sum_dv o'.dO per token.
+// kept: S (bf16, and fp32 for the sums), y, V' (bf16), and sum_dv o'.dO per token.
 //
 // Reverse, with E the gradient of the state that leaves the chunk (beta here and in
 // T: no nearer to zero than 2^-40; dv leaves with the factor that is missing):
@@ -437,7 +437,7 @@ gd_sweep_keep_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.empty[ph]);        // scalars, V and dO are read
             float* yn = p.yn + ((u * nwr + wr) * 2 + half) * (32 * 32) + lane * 4;
-            __nv_bfloat16* vp = p.vp + ((u * nwr + wr) * 4 + s) * kGdPiece;
+            __nv_bfloat16* vp = p.vp + ((u * nwr + wr) * 8 + s) * kGdPiece;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 store_piece(vp + b * kGdPiece, v[b], lane);
@@ -700,7 +700,10 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 }
                 // dv.y + dvs.z = dvs.v + (dv - dvs).y
                 split_pairs(s1, b, fma16(f, v, d[b] * y));
-                split_pairs(s2, b, full * (v - y));
+                const Cols16 z = v - y;
+                split_pairs(s2, b, full * z);
+                // V' second term, from what this sweep has in hand: bytes cost the forward one more
+                store_piece(p.vp + ((u * nwr + wr) * 8 + 4 + s + b) * kGdPiece, low16(load16(sc + kScBeta * kGdC + 16 * b) * z), lane);
             }
             warp_done(&B.w, lane);
             const float gl = sc[kScG * kGdC + kGdC - 1 - 16 * s];

@@ -112,6 +112,14 @@ __device__ __forceinline__ Cols16 fma16(const Cols16& a, const Cols16& b, const 
     for (int i = 0; i < 8; ++i) r.p[i] = f2_fma(a.p[i], b.p[i], c.p[i]);
     return r;
 }
+// What one bf16 term leaves of a value.
+__device__ __forceinline__ Cols16 low16(const Cols16& a)
+{
+    Cols16 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.p[i] = f2_sub(a.p[i], f2_from_bf16x2(f2_to_bf16x2(a.p[i])));
+    return r;
+}
 __device__ __forceinline__ Cols16 zero16()
 {
     Cols16 r;

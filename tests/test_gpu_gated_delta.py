@@ -569,3 +569,24 @@ def test_o_is_off_by_its_own_rounding(N, T, Hk, H, dk, dv, decay):
     d, s0 = make((N, T), Hk, H, dk, dv, 90, decay), states(N, H, dk, dv, 91)
     o, _ = gla.gated_delta_chunk_fwd(*args(d), s0=s0)
     assert beyond_rounding(o, forward(d, s0, dk ** -0.5)[0]) <= TOL_ROUNDED
+
+
+# One bf16 rounding of values of any mantissa alike is off by U sqrt((1 - 1/4) / (6 ln 2)),
+# 0.425 U, in the relative 2-norm.  dq is rounded, and where it comes from the state that
+# is rounded too: sqrt(2) of it at most; dk's part from a state has a second rounded
+# factor (dv): sqrt(3).  With the usual decays and no states at either end at most half of
+# dk is that part: sqrt(1 + 2/2).  Pairs (A, B, V') add 2^-17, lost in the 2% that are left.
+ONE = 0.425 * 1.02 * U
+
+
+@pytest.mark.parametrize("decay,with_states", [("usual", False), ("usual", True), ("slow", True), ("strong", True)])
+@pytest.mark.parametrize("N,T,Hk,H,dk,dv", [(2, 300, 2, 4, 96, 192), (2, 140, 1, 3, 128, 96), (2, 130, 1, 2, 64, 64),
+                                            (1, 900, 1, 1, 96, 160), (1, 100, 1, 1, 64, 256)])
+def test_dq_and_dk_are_off_by_their_roundings(N, T, Hk, H, dk, dv, decay, with_states):
+    d, dO = make((N, T), Hk, H, dk, dv, 92, decay), make((N, T), Hk, H, dk, dv, 93)["v"]
+    s0, ds = (states(N, H, dk, dv, 94), states(N, H, dk, dv, 95)) if with_states else (None, None)
+    got = gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds)
+    zero = torch.zeros(N, H, dk, dv, device="cuda")
+    ref = backward(d, zero if s0 is None else s0, dO, zero if ds is None else ds, dk ** -0.5)
+    assert rel(got[0], ref[0]) <= 2 ** 0.5 * ONE, rel(got[0], ref[0]) / U
+    assert rel(got[1], ref[1]) <= (3 if with_states else 2) ** 0.5 * ONE, rel(got[1], ref[1]) / U
