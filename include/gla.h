@@ -433,14 +433,18 @@ gla_status conv1d_silu_decode_step(const void* x, const int32_t* slot_idx, int n
  *            Calls that may overlap on the GPU need one each.
  * Supported: dk in {64, 96, 128}; dv a multiple of 32, 32 .. 256; dt GLA_BF16
  * (GLA_F32 is GLA_ERR_UNSUPPORTED here; gated_delta_decode_step takes it).
- * States, decays and sums are fp32 or wider; the state is carried to about
- * 16 bits through the products of a chunk of 64 tokens (two bf16 terms).
+ * States, decays and sums are fp32 or wider; the products of a chunk of 64
+ * tokens take bf16 operands, two terms (16 bits) for what is not exact in
+ * bf16: s_final is off by some 3e-6 of its norm, o by its own bf16 rounding.
  *
  * gated_delta_chunk_bwd recomputes what it needs of the forward.  dO [N, T, H,
  * dv] bf16 contiguous; ds_final [N, H, dk, dv] fp32 or NULL (zeros).  grad_q,
  * grad_k [N, T, Hk, dk] and grad_v [N, T, H, dv] bf16, contiguous (summed over
  * the value heads that share a q/k head); grad_a and grad_beta [N, T, H] fp32;
  * grad_s0 [N, H, dk, dv] fp32 or NULL.  Repeated calls give the same bits.
+ * grad_v is off by its own rounding (1.7e-3 in the 2-norm); in grad_q and grad_k
+ * the states and dv enter as one bf16 term (1.8e-3, up to 2.5e-3 under slow
+ * decays); grad_a, grad_beta and grad_s0 are off by 3e-6 to 5e-6.
  * ------------------------------------------------------------------------ */
 size_t gated_delta_chunk_workspace_bytes(int N, int T, int H, int dk, int dv, int packed, int for_bwd);
 
@@ -492,7 +496,8 @@ gla_status gated_delta_decode_step(float* state, const int32_t* slot_idx, int n_
  * bf16, both contiguous; grad_weight, grad_bias as weight and bias, or NULL;
  * ws of group_norm_silu_bwd_workspace_bytes when either is wanted.  Sums over
  * rows are added in a fixed order (repeated calls give the same bits).
- * Supported: d a multiple of 8, d <= 1024, G*d <= 2^20; statistics are fp32.
+ * Supported: d a multiple of 8, d <= 1024, G*d <= 2^20; statistics are fp32,
+ * sigmoids are off by a few 2^-22 of their value, and |z| 2^-24 far out.
  * ------------------------------------------------------------------------ */
 size_t group_norm_silu_bwd_workspace_bytes(int M, int G, int d);
 

@@ -726,7 +726,7 @@ def _rows_stride(x, name):
     return ld
 
 
-def _gated_delta_args(fn, q, k, v, a, beta, lead, cu_seqlens, types):
+def _gated_delta_args(fn, q, k, v, a, beta, lead, types):
     """Check the shared arguments, whose leading dims are `lead`; returns (Hk, H,
     dk, dv, ld_qkv)."""
     if q.dtype not in types:
@@ -799,7 +799,7 @@ def gated_delta_chunk_fwd(q, k, v, a, beta, s0=None, cu_seqlens=None, o=None, s_
     sequences are packed and the leading dims are [T].  Returns (o in v's
     shape, s_final [N,H,dk,dv] fp32 or None)."""
     lead, N, T = _sequences("gated_delta_chunk_fwd", q, v, cu_seqlens)
-    Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_fwd", q, k, v, a, beta, lead, cu_seqlens,
+    Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_fwd", q, k, v, a, beta, lead,
                                           (torch.bfloat16,))
     dev = q.device
     _fit(s0, "s0", torch.float32, (N, H, dk, dv), dev)
@@ -820,7 +820,7 @@ def gated_delta_chunk_bwd(q, k, v, a, beta, dO, s0=None, ds_final=None, cu_seqle
     (dq, dk, dv, da, dbeta, ds0): dq, dk, dv bf16 in q, k and v's shapes, da and
     dbeta fp32, ds0 fp32 or None."""
     lead, N, T = _sequences("gated_delta_chunk_bwd", q, v, cu_seqlens)
-    Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_bwd", q, k, v, a, beta, lead, cu_seqlens,
+    Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_chunk_bwd", q, k, v, a, beta, lead,
                                           (torch.bfloat16,))
     dev, f32, bf16 = q.device, torch.float32, torch.bfloat16
     _fit(s0, "s0", f32, (N, H, dk, dv), dev)
@@ -851,7 +851,7 @@ def gated_delta_decode_step(state, q, k, v, a, beta, o=None, slot_idx=None, scal
     if len(lead) not in (1, 2) or v.dim() != q.dim():
         raise ValueError("gated_delta_decode_step: q must be [N, Hk, dk] or [N, T, Hk, dk]")
     N, T = lead if len(lead) == 2 else (lead[0], 1)
-    Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_decode_step", q, k, v, a, beta, lead, None,
+    Hk, H, dk, dv, ld = _gated_delta_args("gated_delta_decode_step", q, k, v, a, beta, lead,
                                           (torch.bfloat16, torch.float32))
     dev = q.device
     if state.dim() != 4 or state.shape[1:] != (H, dk, dv):

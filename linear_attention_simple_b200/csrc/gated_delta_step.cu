@@ -154,9 +154,11 @@ gla_status launch(const StepParams& p, int N, bool f32, cudaStream_t st)
 // Columns of a CTA.  64 keep the most threads on an SM, and the tokens' barriers
 // in few warps; 16 heads, whole rows against 64 columns: 300 sequences of 128 x
 // 256 252 and 212 us, of 96 x 192 with four tokens 194 and 162, one sequence 9.7
-// and 8.6.  But where whole rows leave the threads on the SM and there is one
-// token, their longer runs in memory pay: 1,280 sequences of 96 x 192 464 against
-// 488 us.  Widths that are no multiple of 64 take whole rows (300 sequences of
+// and 8.6.  But where whole rows leave as many threads on the SM (576 or more of
+// the 682 that the registers allow; 96 x 192, 64 x 192, 64 x 128, 96 x 128) and
+// there is one token, their longer runs in memory pay: 1,280 sequences of 96 x 192
+// 483 against 505 us, of 64 x 192 327 and 344, 300 of them 86 and 88; the narrower
+// two the same within 1%.  Widths that are no multiple of 64 take whole rows (300 sequences of
 // 64 x 160 68 us, 109 with 32 columns), or 32 columns while there are too few
 // CTAs (3 sequences of 96 x 96 10.0 and 9.2).
 int slice_width(int64_t units, int T, int dk, int dv)
