@@ -27,7 +27,7 @@
 // second terms would double this kernel's bytes.  With the usual decays dq is off
 // by 1.74e-3 and dk by 1.8e-3, of which 1.66e-3 is their own rounding (one term of
 // V', A and B too: 2.9e-3; 147 us here and 304 in the reverse sweep where it is
-// 171 and 332 so); with slow ones by 2.3e-3 and 2.5e-3.  The sums behind da and
+// 168 and 325 so); with slow ones by 2.3e-3 and 2.5e-3.  The sums behind da and
 // dbeta come in fp32 from the sweeps, and a warp of its own adds them up.
 //
 // The states and V' are read as the sweeps left them, in pieces of 16 values of
@@ -35,7 +35,7 @@
 // (chunk, head): a ring of stages of 64 dv columns keeps the loads going,
 // and the products of the next unit start as soon as D2 and D3 are read (D1 has
 // two buffers).  Every byte is read once, and HBM bounds it: 8 x 2,048 tokens,
-// 16 heads of 96 x 192, 920 MB in 171 us, 5.4 TB/s.  (With one term each, mma.sync,
+// 16 heads of 96 x 192, 920 MB in 168 us, 5.5 TB/s.  (With one term each, mma.sync,
 // two passes over dv and 12 warps an SM, latency did: 272 us against 146.)
 #include "gated_delta_tc.cuh"
 

@@ -680,15 +680,21 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
             ok = (PRE || warp_wait(&B.yin[warp], i & 1, ctl)) && warp_wait(&B.z, ph, ctl);
             if (!ok) break;
             tc_fence_after();
-            float s1[32], s2[32];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const Cols16 f = get16(t0 + C::PO + 16 * (s + b)), full = f + d[b];              // dvs, dv
+                const Cols16 full = get16(t0 + C::PO + 16 * (s + b)) + d[b];                     // dv
                 Cols16 g = load16(sc + kScG * kGdC + 16 * b) * full;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) g.p[j] = f2_mul(g.p[j], f2_splat(-1.f));
                 put_terms<2>(t0 + C::Y + 16 * (s + b), g);
-                if (PRE) continue;
+            }
+            warp_done(&B.w, lane);
+            const float gl = sc[kScG * kGdC + kGdC - 1 - 16 * s];
+            // what the chain does not wait for: while the products run
+            float s1[32], s2[32];
+#pragma unroll
+            for (int b = 0; b < 2 && !PRE; ++b) {
+                const Cols16 f = get16(t0 + C::PO + 16 * (s + b)), full = f + d[b];              // dvs, dv
                 const Cols16 v = load_row16(vs + 16 * b * x.rows, x.rows, left - 16 * b);
                 store_row16(vs + 16 * b * x.rows, x.rows, full);
                 Cols16 y;
@@ -705,8 +711,6 @@ gd_sweep_rev_kernel(GdParams p, const __grid_constant__ GdMap map_v, const __gri
                 // V' second term, from what this sweep has in hand: bytes cost the forward one more
                 store_piece(p.vp + ((u * nwr + wr) * 8 + 4 + s + b) * kGdPiece, low16(load16(sc + kScBeta * kGdC + 16 * b) * z), lane);
             }
-            warp_done(&B.w, lane);
-            const float gl = sc[kScG * kGdC + kGdC - 1 - 16 * s];
             // what beta has that beta~ has not, on the rounded rows: nearly always 1, and as a
             // factor of dv before its rounding it cost 2% of the backward
             if (!PRE && __any_sync(0xFFFFFFFFu, sc[kScF * kGdC + lane] != 1.f)) {
