@@ -82,17 +82,18 @@ struct Unit {
     int64_t slot;
     int hk, row, valid;     // row: the chunk's first token
     bool between;           // <E, S'> is kept for the chunk behind this one, not for this one
+    bool first;             // of its sequence
 };
-// Calls f for this CTA's units in turn, the same for all lanes, until it
+// Calls work for this CTA's units in turn, the same for all lanes, until it
 // returns false.  32 units at a time are looked up, a lane each.
 template <class F>
-__device__ __forceinline__ void for_units(const GdParams& p, int lane, F f)
+__device__ __forceinline__ void for_units(const GdParams& p, int lane, F work)
 {
     const int64_t total = p.slots * p.seqs.Hk, step = gridDim.x;
     for (int64_t base = blockIdx.x; base < total; base += 32 * step) {
         const int64_t i = base + lane * step;
         int row = 0, valid = 0;
-        bool between = false;
+        int flags = 0;
         if (i < total) {
             const int64_t slot = i / p.seqs.Hk;
             const int n = gd_seq_of_slot(p.seqs, slot);
@@ -103,7 +104,7 @@ __device__ __forceinline__ void for_units(const GdParams& p, int lane, F f)
             if (len >= 0 && c >= 0 && c * kGdC < len) {      // else between two sequences
                 row = static_cast<int>(row0 + c * kGdC);
                 valid = min(kGdC, len - static_cast<int>(c) * kGdC);
-                between = (c & 1) == 0 && (c + 1) * kGdC < len;
+                flags = ((c & 1) == 0 && (c + 1) * kGdC < len ? 1 : 0) | (c == 0 ? 2 : 0);
             }
         }
         for (uint32_t m = __ballot_sync(0xFFFFFFFFu, valid > 0); m; m &= m - 1) {
@@ -113,8 +114,10 @@ __device__ __forceinline__ void for_units(const GdParams& p, int lane, F f)
             u.hk = static_cast<int>(base + l * step - u.slot * p.seqs.Hk);
             u.row = __shfl_sync(0xFFFFFFFFu, row, l);
             u.valid = __shfl_sync(0xFFFFFFFFu, valid, l);
-            u.between = __shfl_sync(0xFFFFFFFFu, static_cast<int>(between), l) != 0;
-            if (!f(u)) return;
+            const int f = __shfl_sync(0xFFFFFFFFu, flags, l);
+            u.between = (f & 1) != 0;
+            u.first = (f & 2) != 0;
+            if (!work(u)) return;
         }
     }
 }
@@ -168,7 +171,9 @@ __device__ __forceinline__ void sums(const GdParams& p, const Unit& x, int h, in
     [[maybe_unused]] const int64_t rows = p.seqs.cu ? p.seqs.T : static_cast<int64_t>(p.seqs.N) * p.seqs.T;   // of the checking build
     const int64_t at = (static_cast<int64_t>(x.row) + 2 * lane) * H + h;
     if (2 * lane < x.valid && GLA_DCHECK(at >= 0 && at < rows * H, p.status)) {
-        p.da[at] = s + tail;
+        // nothing decays before a sequence's first token: what is left of its sum is
+        // rounding (or not finite, and stays so)
+        p.da[at] = x.first && lane == 0 && !p.s0 ? fmaf(0.f, s + tail, 0.f) : s + tail;
         p.dbeta[at] = s2.x / beta[2 * lane];
     }
     if (2 * lane + 1 < x.valid && GLA_DCHECK(at + H < rows * H, p.status)) {

@@ -590,3 +590,19 @@ def test_dq_and_dk_are_off_by_their_roundings(N, T, Hk, H, dk, dv, decay, with_s
     ref = backward(d, zero if s0 is None else s0, dO, zero if ds is None else ds, dk ** -0.5)
     assert rel(got[0], ref[0]) <= 2 ** 0.5 * ONE, rel(got[0], ref[0]) / U
     assert rel(got[1], ref[1]) <= (3 if with_states else 2) ** 0.5 * ONE, rel(got[1], ref[1]) / U
+
+
+@pytest.mark.parametrize("lens", [None, [1, 70, 0, 1, 130]])
+def test_the_first_decay_of_a_sequence_without_a_state_has_no_gradient(lens):
+    """e^a S with S = 0: exactly 0, whatever gradient the states have; with an s0
+    it is <E, e^a s0>."""
+    cu, lead = (cu_of(lens), (sum(lens),)) if lens else (None, (3, 1))
+    N = len(lens) if lens else 3
+    d, dO = make(lead, 1, 2, 96, 192, 96), make(lead, 1, 2, 96, 192, 97)["v"]
+    s0, ds = states(N, 2, 96, 192, 98), states(N, 2, 96, 192, 99)
+    first = [int(b) for b, n in zip(cu.tolist(), lens) if n] if lens else slice(None)
+    got = gla.gated_delta_chunk_bwd(*args(d), dO, ds_final=ds, cu_seqlens=cu)[3]
+    assert bool((got[first] == 0).all())
+    got = gla.gated_delta_chunk_bwd(*args(d), dO, s0=s0, ds_final=ds, cu_seqlens=cu)[3]
+    want = backward(d, s0, dO, ds, 96 ** -0.5, cu)[3]
+    assert rel(got[first], want[first]) <= TOL_DA
