@@ -61,11 +61,13 @@ gla_status gd_check(int N, int T, int Hk, int H, int dk, int dv, int64_t ld_qkv,
 // takes some 2 us a segment, passes and sweeps 15 and 6.5 a chunk (4 heads of 96 x
 // 192, forward: 16,384 tokens in 37 segments 219 us, in 22 200; 4,096 tokens of 8
 // heads in 14 132 us, in 11 122).  One piece against segments: 768 tokens of 8 heads
-// of 96 x 192 backward 167 and 142 us, 1,024 tokens of 8 heads of 64 x 64 184 and
-// 124, forward 83 and 67; but 555 tokens of two sequences of 8 heads of 128 x 128
-// 168 and 181, and 4,096 tokens of two sequences of 16 heads of 96 x 192 forward 257
-// and 270.  The backward's have an even number of chunks: it keeps the state after
-// every second one.
+// of 96 x 192 backward 136 and 111 us, 1,024 tokens of 8 heads of 64 x 64 151 and
+// 93, forward 60 and 47; but 4,096 tokens of two sequences of 16 heads of 96 x 192
+// forward 257 and 270.  Below 12 chunks both happen backward, by the number of
+// segments that fit: 640 tokens of 16 heads of 96 x 192 (four) 129 and 146, 555
+// tokens of two sequences of 8 heads of 128 x 128 (nine) 142 and 129; forward, 500
+// tokens of 8 heads of 96 x 192, 39 and 42.  The backward's have an even number of
+// chunks: it keeps the state after every second one.
 void gd_segments(GdParams& p, bool bwd)
 {
     constexpr int64_t kSms = 148;

@@ -26,16 +26,16 @@
 // against operands exact in bf16 (K, dO), or two against two (T, P, scale G Q).
 //
 // A CTA is bound by the chain of products and conversions, some 7,500 cycles a
-// chunk forward and 8,500 in reverse; it takes most of tensor memory, so an SM
+// chunk forward and 8,700 in reverse; it takes most of tensor memory, so an SM
 // holds one.
 //
 // Long sequences with few heads are therefore cut into segments that run at
 // once, as in the forward: the states that enter them come from the same pass
 // (on this direction's records); the gradients of the states that leave them
 // from a reverse pass from zeros and a hand-over with A^T.  Whole backward of
-// 16,384 tokens, in one piece and so: 4 heads of 96 x 192 2,283 us, 460 us; 16
-// heads 2,561, 1,312; 48 heads of 128 x 128 (three segments) 4,030, 2,610; of
-// 1,024 tokens and 8 heads of 64 x 64 184, 124.
+// 16,384 tokens, in one piece and so: 4 heads of 96 x 192 2,248 us, 440 us; 16
+// heads 2,444, 1,303; 48 heads of 128 x 128 (three segments) 3,939, 2,686; of
+// 1,024 tokens and 8 heads of 64 x 64 151, 93.
 #include "gated_delta_tc.cuh"
 
 namespace gla {

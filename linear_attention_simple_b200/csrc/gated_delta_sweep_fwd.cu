@@ -36,8 +36,8 @@
 // small fp32 kernel hands the states on from segment to segment, and the sweep
 // proper starts every segment from its own.  The pass needs neither Q, P nor o:
 // two of its CTAs share an SM at dk = 128 too (169 us with one each, 143 so).
-// One prompt of 16,384 tokens at 16 heads of 128 x 128: 783 us in one piece, 273
-// us so (143 + 30 + 100).
+// One prompt of 16,384 tokens at 16 heads of 128 x 128: 858 us in one piece, 287
+// us so (143 + 31 + 113).
 #include "gated_delta_tc.cuh"
 
 namespace gla {
