@@ -166,3 +166,44 @@ def test_workspaces_of_the_mixer_and_its_front_end(name):
             }.get(name, lambda: gla.gla_segment_workspace_bytes(8, 1024, 16))()
     assert need > 0
     check_workspace(mixer_calls()[name], need)
+
+
+@pytest.mark.parametrize("name", DELTA)
+def test_a_captured_call_that_is_given_the_captures_own_stream(name):
+    call = delta_calls()[name]
+    want = [t for t in call() if t is not None]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [t for t in call(stream=torch.cuda.current_stream()) if t is not None]
+    for t in got:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_threads_with_a_stream_each():
+    """Host threads that call at once, each on a stream of its own and with what the
+    binding allocates."""
+    import threading
+    calls, wants, errors = delta_calls(), {}, []
+    names = [n for n in DELTA if n != "gated_delta_decode_step"]
+    for n in names:
+        wants[n] = [t for t in calls[n]() if t is not None]
+    torch.cuda.synchronize()
+
+    def work(n):
+        side = torch.cuda.Stream()
+        for _ in range(6):
+            got = [t for t in calls[n](stream=side) if t is not None]
+            side.synchronize()
+            if not all(torch.equal(x, y) for x, y in zip(got, wants[n])):
+                errors.append(n)
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in names]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not errors and not any(t.is_alive() for t in threads)
